@@ -71,7 +71,9 @@ typedef enum {
   TQ_ERR_TIMEOUT = 8       /* a kernel gave up a bounded wait (see tq_sync_check) */
 } tq_status;
 
-typedef enum { TQ_F32 = 0, TQ_BF16 = 1 } tq_dtype;
+/* Element types.  TQ_F16 is taken by the attention calls only
+ * (tq_attend_prompt, tq_attend_paged). */
+typedef enum { TQ_F32 = 0, TQ_BF16 = 1, TQ_F16 = 2 } tq_dtype;
 
 typedef enum {
   TQ_ROT_AUTO = 0,      /* Hadamard for power-of-two d, Haar otherwise          */
@@ -181,6 +183,84 @@ tq_status tq_attend(const tq_quantizer *qv, const float *logits, int64_t ldl, in
                     int64_t G, float scale, const void *vcodes, const float *vnorms,
                     int64_t keys_per_group, int64_t key_base, int64_t nkeys, float *out,
                     int64_t ldo, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------- paged cache
+ * A quantized KV cache in pages (TurboQuant article 4.1.1: the cache's keys
+ * and values are both quantized; the pages are silent on its memory, and
+ * pages of a fixed number of tokens are how a server shares it between
+ * sequences of different lengths).
+ *
+ * tq_rows: the three packed arrays of tq_encode.  For rows of new tokens, row
+ *   t*kv_heads + h belongs to token t, KV head h.  For a cache of npages pages
+ *   of page_size tokens, row (page*kv_heads + h)*page_size + offset; slot
+ *   page*page_size + offset names a token's place in it.
+ *   signs is ignored (may be NULL) for quantizers without sign bits.
+ *   page_size: a multiple of 16 in [16, 1024].  Arrays of a cache are 16-byte
+ *   aligned. */
+typedef struct {
+  void *codes;
+  void *signs;
+  float *norms;
+} tq_rows;
+
+/* tq_paged_store: puts the encoded keys and values of `tokens` tokens into
+ * the pages, token t at slots[t] (device int64), all KV heads, in one launch.
+ * A slot outside [0, npages*page_size) stores nothing (rows that pad a
+ * batch).  Slots are otherwise distinct: where two tokens name the same slot
+ * its contents are unspecified.  Everything else in the pages is left as it
+ * was.  krows, kpages: rows of qk; vrows, vpages: rows of qv.  codes and signs
+ * of the rows 4-byte aligned, norms 8-byte.  Any quantizers of one device;
+ * rows and pages must not overlap. */
+tq_status tq_paged_store(const tq_quantizer *qk, const tq_quantizer *qv, const tq_rows *krows,
+                         const tq_rows *vrows, const int64_t *slots, int64_t tokens,
+                         int64_t kv_heads, const tq_rows *kpages, const tq_rows *vpages,
+                         int64_t npages, int page_size, void *stream);
+
+/* tq_attend_paged: causal attention of the new tokens of a batch over a
+ * paged quantized cache (one new token per sequence when decoding; several
+ * for a chunk of a prompt or for drafted tokens).
+ *   qk: the keys' quantizer, inner-product (tq_codebook) or TurboQuant-MSE;
+ *   qv: the values' quantizer, TurboQuant-MSE, b in [2, 4].  Both Hadamard,
+ *       of one d = 64 or 128, on one device.
+ *   y: queries of `dtype` (TQ_BF16 or TQ_F16), token t, head h at
+ *       y + t*ldy + h*d (ldy >= heads*d); out likewise (ldo).  y 2-byte
+ *       aligned; out 8-byte aligned and ldo a multiple of 4.  heads is a multiple of
+ *       kv_heads; query head h reads KV head h / (heads / kv_heads).
+ *   q_start: device int32 [nseq + 1]; sequence i has the new tokens
+ *       [q_start[i], q_start[i+1]), at most max_new of them (further ones
+ *       are left out), any of them possibly none.  Tokens of no sequence, and
+ *       those at or behind total_q, are left as they were in out.
+ *   kv_len: device int32 [nseq]; the sequence's keys, its new tokens (already
+ *       stored) the last of them: new token j of n sees the first
+ *       kv_len - n + j + 1 keys.  A token that sees none gets zeros.
+ *   page_table: device int32, sequence i's pages in order at
+ *       page_table + i*ldt, max_pages entries (keys that lie beyond are not
+ *       attended).  Only the entries that kv_len needs are read; an entry
+ *       outside [0, npages) holds no keys.
+ *   scale: multiplies the logits before the softmax; finite.
+ *   workspace: device, 16-byte aligned, tq_attend_paged_workspace_bytes of
+ *       the same sizes (it depends on the device's SM count); a call may not
+ *       share it with another that may run at the same time.
+ * out_h = sum_k softmax_k(scale s_hk) v^_k with s_hk the estimate of tq_score
+ * (or, without sign bits, <y, x^_k>) and v^_k = ||v_k|| R^T c[codes_k].  The
+ * rotated queries, the centroids and the weights are fp16 operands (each
+ * rounded to within 2^-11, the queries and weights under a power-of-two
+ * scale), products are accumulated in fp32 and the softmax is fp32: out is
+ * within about 2^-9 sum_k softmax_k ||v_k|| / sqrt(d) of the exact value per
+ * coordinate beside its own rounding, for scaled logits up to about 30.
+ * Lengths and tables are read on the device: the call can be captured in a
+ * graph and replayed with other values in the same buffers.
+ * nseq == 0, total_q == 0 or max_new == 0: no-op. */
+size_t tq_attend_paged_workspace_bytes(const tq_quantizer *qk, const tq_quantizer *qv, int64_t total_q,
+                                       int64_t nseq, int64_t heads, int64_t kv_heads, int64_t max_new,
+                                       int64_t max_pages, int page_size);
+tq_status tq_attend_paged(const tq_quantizer *qk, const tq_quantizer *qv, tq_dtype dtype, const void *y,
+                          int64_t ldy, int64_t total_q, const int32_t *q_start, int64_t nseq,
+                          int64_t max_new, int64_t heads, int64_t kv_heads, const tq_rows *kpages,
+                          const tq_rows *vpages, int64_t npages, int page_size,
+                          const int32_t *page_table, int64_t ldt, int64_t max_pages,
+                          const int32_t *kv_len, float scale, void *out, int64_t ldo,
+                          void *workspace, size_t workspace_bytes, void *stream);
 
 /* On-the-fly QJL matrix (TurboQuant article 2.3.2: the random projection is
  * generated from a pseudo-random sequence instead of being stored).

@@ -16,7 +16,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtq.so")
 
-TQ_F32, TQ_BF16 = 0, 1
+TQ_F32, TQ_BF16, TQ_F16 = 0, 1, 2
 ROTATIONS = {"auto": 0, "hadamard": 1, "haar": 2}
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported configuration",
           3: "misaligned pointer or leading dimension", 4: "out of memory",
@@ -40,6 +40,10 @@ class _Info(ctypes.Structure):
                 ("coord_mse", ctypes.c_double)]
 
 
+class _Rows(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("signs", ctypes.c_void_p), ("norms", ctypes.c_void_p)]
+
+
 def lib() -> ctypes.CDLL:
     """Load libtq.so from the package directory (raises if it was not built)."""
     global _lib
@@ -50,6 +54,7 @@ def lib() -> ctypes.CDLL:
                           "`python online_vector_quantization_tq_b200/build.py`")
     L = ctypes.CDLL(LIB_PATH)
     vp, i64, i32, u64, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64, ctypes.c_size_t
+    rows = ctypes.POINTER(_Rows)
     sigs = {
         "tq_status_string": (ctypes.c_char_p, [i32]),
         "tq_codebook": (i32, [i32, i32, i32, u64, i32, ctypes.POINTER(vp)]),
@@ -62,6 +67,10 @@ def lib() -> ctypes.CDLL:
         "tq_set_qjl_onthefly": (i32, [vp, i32]),
         "tq_attend_workspace_bytes": (sz, [vp, i64, i64, i64]),
         "tq_attend": (i32, [vp, vp, i64, i64, i64, ctypes.c_float, vp, vp, i64, i64, i64, vp, i64, vp, sz, vp]),
+        "tq_paged_store": (i32, [vp, vp, rows, rows, vp, i64, i64, rows, rows, i64, i32, vp]),
+        "tq_attend_paged_workspace_bytes": (sz, [vp, vp, i64, i64, i64, i64, i64, i64, i32]),
+        "tq_attend_paged": (i32, [vp, vp, i32, vp, i64, i64, vp, i64, i64, i64, i64, rows, rows, i64, i32, vp, i64,
+                                  i64, vp, ctypes.c_float, vp, i64, vp, sz, vp]),
         "tq_qjl_matrix": (i32, [vp, vp, vp]),
         "tq_codebook_get": (i32, [vp, vp, vp, vp]),
         "tq_tables_get": (i32, [vp, vp, vp, vp]),
@@ -140,6 +149,32 @@ class Encoded:
         return self
 
 
+@dataclass
+class PagedCache:
+    """Packed rows of a cache's keys, or of its values, in pages (include/tq.h:
+    tq_rows).  Page p holds page_size tokens of every KV head."""
+    codes: torch.Tensor   # uint8 [npages, kv_heads, page_size, code_bytes]
+    signs: torch.Tensor   # uint8 [npages, kv_heads, page_size, sign_bytes]
+    norms: torch.Tensor   # float32 [npages, kv_heads, page_size, 2]
+
+    def check(self, q: "Quantizer"):
+        """Shapes, types and contiguity that the library relies on: it reads and
+        writes whole rows of q's quantizer."""
+        if self.codes.dim() != 4:
+            raise ValueError(f"PagedCache.codes must have 4 dimensions (got {self.codes.dim()})")
+        lead = tuple(self.codes.shape[:3])
+        for name, t, dtype, row in (("codes", self.codes, torch.uint8, q.code_bytes),
+                                    ("signs", self.signs, torch.uint8, q.sign_bytes),
+                                    ("norms", self.norms, torch.float32, 2)):
+            if t is None and row == 0:
+                continue
+            if t.dtype != dtype or tuple(t.shape) != lead + (row,):
+                raise ValueError(f"PagedCache.{name} must be {dtype} {lead + (row,)} (got {t.dtype} {tuple(t.shape)})")
+            if t.numel() and not t.is_contiguous():
+                raise ValueError(f"PagedCache.{name} must be contiguous (got strides {t.stride()})")
+        return self
+
+
 class Quantizer:
     """Owned tq_quantizer handle."""
 
@@ -194,6 +229,12 @@ class Quantizer:
         return Encoded(torch.empty((n, self.code_bytes), dtype=torch.uint8, device=device),
                        torch.empty((n, self.sign_bytes), dtype=torch.uint8, device=device),
                        torch.empty((n, 2), dtype=torch.float32, device=device))
+
+    def empty_paged(self, npages: int, kv_heads: int, page_size: int, device="cuda") -> PagedCache:
+        lead = (npages, kv_heads, page_size)
+        return PagedCache(torch.empty(lead + (self.code_bytes,), dtype=torch.uint8, device=device),
+                          torch.empty(lead + (self.sign_bytes,), dtype=torch.uint8, device=device),
+                          torch.empty(lead + (2,), dtype=torch.float32, device=device))
 
 
 def tq_codebook(d: int, b: int, m: int = 0, seed: int = 0, rotation: str = "auto") -> Quantizer:
@@ -336,6 +377,107 @@ def tq_attend(qv: Quantizer, logits: torch.Tensor, groups: int, G: int, venc: En
         qv.handle, _ptr(logits), _ld(logits), groups, G, float(scale), _ptr(venc.codes),
         _ptr(venc.norms), keys_per_group, key_base, n, _ptr(out), _ld(out), _ptr(workspace), workspace.numel(),
         _stream(stream)))
+    return out
+
+
+def _dtype16(x: torch.Tensor) -> int:
+    if x.dtype == torch.bfloat16:
+        return TQ_BF16
+    if x.dtype == torch.float16:
+        return TQ_F16
+    raise TypeError(f"unsupported dtype {x.dtype}")
+
+
+def _ld_rows(x: torch.Tensor) -> int:
+    """_ld, but a single row's stride (which torch leaves open) does not count."""
+    ld = _ld(x)
+    return ld if x.shape[0] > 1 else x.shape[1]
+
+
+def _rows(t) -> _Rows:
+    return _Rows(t.codes.data_ptr(), 0 if t.signs is None else t.signs.data_ptr(), t.norms.data_ptr())
+
+
+def _vector(t: torch.Tensor, dtype, name: str, length: int | None = None) -> torch.Tensor:
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.dim() != 1 or not t.is_contiguous() or (length is not None and t.numel() != length):
+        raise ValueError(f"{name} must be a contiguous 1-D tensor" + ("" if length is None else f" of {length}"))
+    return t
+
+
+def _cuda(**tensors):
+    for name, t in tensors.items():
+        if t is not None and t.numel() and not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _check_caches(qk: Quantizer, qv: Quantizer, kcache: PagedCache, vcache: PagedCache):
+    """(npages, kv_heads, page_size) that both arrays agree on."""
+    kcache.check(qk)
+    vcache.check(qv)
+    if kcache.codes.shape[:3] != vcache.codes.shape[:3]:
+        raise ValueError("kcache and vcache must have the same pages, KV heads and page size")
+    _cuda(kcache=kcache.codes, vcache=vcache.codes)
+    return kcache.codes.shape[:3]
+
+
+def tq_paged_store(qk: Quantizer, qv: Quantizer, kenc: Encoded, venc: Encoded, slots: torch.Tensor,
+                   kcache: PagedCache, vcache: PagedCache, stream=None) -> None:
+    """Store encoded keys and values of new tokens (row t*kv_heads + h: token
+    t, head h) into the pages, token t at slot slots[t] = page*page_size +
+    offset (int64; a slot outside the cache stores nothing)."""
+    npages, kv_heads, page_size = _check_caches(qk, qv, kcache, vcache)
+    _vector(slots, torch.int64, "slots")
+    tokens = slots.numel()
+    for q, e, name in ((qk, kenc, "kenc"), (qv, venc, "venc")):
+        e.check()
+        want = (tokens * kv_heads, q.code_bytes)
+        if tuple(e.codes.shape) != want or e.norms.shape[0] != want[0] or (q.m and e.signs.shape[0] != want[0]):
+            raise ValueError(f"{name} must have {want[0]} rows of {want[1]} code bytes (got {tuple(e.codes.shape)})")
+    _cuda(kenc=kenc.codes, venc=venc.codes, slots=slots)
+    _check("tq_paged_store", lib().tq_paged_store(
+        qk.handle, qv.handle, _rows(kenc), _rows(venc), _ptr(slots), tokens, kv_heads, _rows(kcache), _rows(vcache),
+        npages, page_size, _stream(stream)))
+
+
+def attend_paged_workspace(qk: Quantizer, qv: Quantizer, total_q: int, nseq: int, heads: int, kv_heads: int,
+                           max_new: int, max_pages: int, page_size: int, device="cuda") -> torch.Tensor:
+    return _workspace(lib().tq_attend_paged_workspace_bytes(
+        qk.handle, qv.handle, total_q, nseq, heads, kv_heads, max_new, max_pages, page_size), device)
+
+
+def tq_attend_paged(qk: Quantizer, qv: Quantizer, y: torch.Tensor, q_start: torch.Tensor, kcache: PagedCache,
+                    vcache: PagedCache, page_table: torch.Tensor, kv_len: torch.Tensor, max_new: int, scale: float,
+                    out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """Causal attention of new tokens over a paged quantized cache: y [tokens,
+    heads*d] (bf16 or fp16), sequence i's new tokens q_start[i] to q_start[i+1]
+    (at most max_new), its pages page_table[i], its keys kv_len[i] (the new
+    tokens' last among them)."""
+    npages, kv_heads, page_size = _check_caches(qk, qv, kcache, vcache)
+    total_q, ldy = y.shape[0], _ld_rows(y)
+    if y.shape[1] % (qk.d * kv_heads) != 0:
+        raise ValueError(f"y must have a whole number of heads of {qk.d} for each of {kv_heads} KV heads")
+    heads = y.shape[1] // qk.d
+    nseq = kv_len.numel()
+    _vector(q_start, torch.int32, "q_start", nseq + 1)
+    _vector(kv_len, torch.int32, "kv_len")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != nseq:
+        raise TypeError(f"page_table must be an int32 tensor of {nseq} rows")
+    if out is None:
+        out = torch.empty((total_q, y.shape[1]), dtype=y.dtype, device=y.device)
+    elif out.dtype != y.dtype or out.shape != y.shape:
+        raise ValueError("out must have y's shape and type")
+    max_pages = page_table.shape[1]
+    if workspace is None:
+        workspace = attend_paged_workspace(qk, qv, total_q, nseq, heads, kv_heads, max_new, max_pages, page_size,
+                                           y.device)
+    _cuda(y=y, q_start=q_start, page_table=page_table, kv_len=kv_len, out=out, workspace=workspace)
+    _check("tq_attend_paged", lib().tq_attend_paged(
+        qk.handle, qv.handle, _dtype16(y), _ptr(y), ldy, total_q, _ptr(q_start), nseq, max_new, heads, kv_heads,
+        _rows(kcache), _rows(vcache), npages, page_size, _ptr(page_table), _ld_rows(page_table), max_pages, _ptr(kv_len),
+        float(scale), _ptr(out), _ld_rows(out), _ptr(workspace), workspace.numel(), _stream(stream)))
     return out
 
 

@@ -137,6 +137,94 @@ tq_status tq_attend(const tq_quantizer *qv, const float *logits, int64_t ldl, in
                            ldo, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
+// Shared checks of the paged cache: page size, array pointers and alignment.
+static tq_status check_pages(const tq_quantizer *q, const tq_rows *r, int64_t npages, int page_size) {
+  if (!r || npages < 0 || page_size < 16 || page_size > 1024 || page_size % 16 != 0) return TQ_ERR_INVALID_ARG;
+  if (npages > 0x7fffffff) return TQ_ERR_TOO_LARGE;
+  if (npages == 0) return TQ_OK;
+  if (!r->codes || (!r->signs && q->m > 0) || !r->norms) return TQ_ERR_INVALID_ARG;
+  if (!aligned(r->codes, 16) || (q->m > 0 && !aligned(r->signs, 16)) || !aligned(r->norms, 16))
+    return TQ_ERR_ALIGNMENT;
+  return TQ_OK;
+}
+
+tq_status tq_paged_store(const tq_quantizer *qk, const tq_quantizer *qv, const tq_rows *krows, const tq_rows *vrows,
+                         const int64_t *slots, int64_t tokens, int64_t kv_heads, const tq_rows *kpages,
+                         const tq_rows *vpages, int64_t npages, int page_size, void *stream) {
+  if (!qk || !qv || tokens < 0 || kv_heads < 1) return TQ_ERR_INVALID_ARG;
+  tq_status st = check_pages(qk, kpages, npages, page_size);
+  if (st == TQ_OK) st = check_pages(qv, vpages, npages, page_size);
+  if (st != TQ_OK) return st;
+  if (tokens == 0 || npages == 0) return TQ_OK;  // nothing to store, or no slot to store it in
+  const tq_quantizer *q[2] = {qk, qv};
+  const tq_rows *r[2] = {krows, vrows};
+  for (int i = 0; i < 2; ++i) {
+    if (!r[i] || !r[i]->codes || (!r[i]->signs && q[i]->m > 0) || !r[i]->norms) return TQ_ERR_INVALID_ARG;
+    if (!aligned(r[i]->codes, 4) || (q[i]->m > 0 && !aligned(r[i]->signs, 4)) || !aligned(r[i]->norms, 8))
+      return TQ_ERR_ALIGNMENT;
+  }
+  if (!slots) return TQ_ERR_INVALID_ARG;
+  if (!aligned(slots, 8)) return TQ_ERR_ALIGNMENT;
+  if (kv_heads > 65536 || tokens > ((int64_t)1 << 40) / kv_heads) return TQ_ERR_TOO_LARGE;
+  if (qk->device < 0 || qv->device != qk->device) return TQ_ERR_UNSUPPORTED;
+  DeviceGuard g(qk->device);
+  if (!g.ok) return TQ_ERR_CUDA;
+  return tq::paged_store_launch(qk, qv, *krows, *vrows, slots, tokens, (int)kv_heads, *kpages, *vpages, npages,
+                                page_size, static_cast<cudaStream_t>(stream));
+}
+
+// Sizes of an attention call over pages that the kernels' index types hold.
+static tq_status check_paged_sizes(const tq_quantizer *qk, const tq_quantizer *qv, int64_t total_q, int64_t nseq,
+                                   int64_t heads, int64_t kv_heads, int64_t max_new, int64_t max_pages,
+                                   int page_size) {
+  if (!qk || !qv || total_q < 0 || nseq < 0 || heads < 1 || kv_heads < 1 || max_new < 0 || max_pages < 0 ||
+      page_size < 16 || page_size > 1024 || page_size % 16 != 0 || heads % kv_heads != 0)
+    return TQ_ERR_INVALID_ARG;
+  if (!tq::attend_paged_supported(qk, qv)) return TQ_ERR_UNSUPPORTED;
+  const int64_t big = (int64_t)1 << 30;
+  if (total_q > big || nseq > (1 << 24) || heads > (1 << 16) || max_new > big / heads || max_pages > big / page_size)
+    return TQ_ERR_TOO_LARGE;
+  return TQ_OK;
+}
+
+size_t tq_attend_paged_workspace_bytes(const tq_quantizer *qk, const tq_quantizer *qv, int64_t total_q, int64_t nseq,
+                                       int64_t heads, int64_t kv_heads, int64_t max_new, int64_t max_pages,
+                                       int page_size) {
+  if (check_paged_sizes(qk, qv, total_q, nseq, heads, kv_heads, max_new, max_pages, page_size) != TQ_OK) return 0;
+  if (total_q == 0 || nseq == 0 || max_new == 0 || qk->device < 0) return 0;
+  DeviceGuard g(qk->device);
+  if (!g.ok) return 0;
+  return tq::attend_paged_ws_bytes(qk, nseq, heads, kv_heads, max_new, max_pages, page_size);
+}
+
+tq_status tq_attend_paged(const tq_quantizer *qk, const tq_quantizer *qv, tq_dtype dtype, const void *y, int64_t ldy,
+                          int64_t total_q, const int32_t *q_start, int64_t nseq, int64_t max_new, int64_t heads,
+                          int64_t kv_heads, const tq_rows *kpages, const tq_rows *vpages, int64_t npages,
+                          int page_size, const int32_t *page_table, int64_t ldt, int64_t max_pages,
+                          const int32_t *kv_len, float scale, void *out, int64_t ldo, void *workspace,
+                          size_t workspace_bytes, void *stream) {
+  tq_status st = check_paged_sizes(qk, qv, total_q, nseq, heads, kv_heads, max_new, max_pages, page_size);
+  if (st != TQ_OK) return st;
+  if (dtype != TQ_BF16 && dtype != TQ_F16) return TQ_ERR_UNSUPPORTED;
+  st = check_pages(qk, kpages, npages, page_size);
+  if (st == TQ_OK) st = check_pages(qv, vpages, npages, page_size);
+  if (st != TQ_OK) return st;
+  if (total_q == 0 || nseq == 0 || max_new == 0) return TQ_OK;
+  if (!y || !q_start || !kv_len || (!page_table && max_pages > 0) || !out || !std::isfinite(scale))
+    return TQ_ERR_INVALID_ARG;
+  if (ldy < heads * qk->d || ldo < heads * qk->d || ldt < max_pages) return TQ_ERR_INVALID_ARG;
+  if (!aligned(y, 2) || !aligned(out, 8) || ldo % 4 != 0 || !aligned(q_start, 4) || !aligned(kv_len, 4) ||
+      !aligned(page_table, 4))
+    return TQ_ERR_ALIGNMENT;
+  if (!workspace || !aligned(workspace, 16)) return TQ_ERR_WORKSPACE;
+  if (qk->device < 0 || qv->device != qk->device) return TQ_ERR_UNSUPPORTED;
+  DeviceGuard g(qk->device);
+  if (!g.ok) return TQ_ERR_CUDA;
+  const tq::PagedArgs a{dtype,     y,   ldy,       total_q, q_start, nseq,  max_new, heads, kv_heads,  *kpages,        *vpages,
+                        npages,    page_size, page_table, ldt,     max_pages, kv_len, scale, out,   ldo, workspace, workspace_bytes};
+  return tq::attend_paged_launch(qk, qv, a, static_cast<cudaStream_t>(stream));
+}
+
 tq_status tq_set_qjl_onthefly(tq_quantizer *q, int enable) {
   if (!q) return TQ_ERR_INVALID_ARG;
   q->kt.qjl_otf = enable ? 1 : 0;

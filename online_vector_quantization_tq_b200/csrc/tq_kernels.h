@@ -64,6 +64,33 @@ size_t attend_ws_bytes(int64_t groups, int64_t G, int d, int64_t nkeys);
 tq_status attend_launch(const tq_quantizer *qv, const float *logits, int64_t ldl, int64_t groups, int64_t G,
                         float scale, const void *vcodes, const float *vnorms, int64_t kpg, int64_t key_base,
                         int64_t nkeys, float *out, int64_t ldo, void *ws, size_t ws_bytes, cudaStream_t st);
+// a quantized KV cache in pages
+struct PagedArgs {
+  tq_dtype dtype;
+  const void *y;
+  int64_t ldy, total_q;
+  const int32_t *q_start;
+  int64_t nseq, max_new, heads, kv_heads;
+  tq_rows kpages, vpages;
+  int64_t npages;
+  int page_size;
+  const int32_t *table;
+  int64_t ldt, max_pages;
+  const int32_t *kv_len;
+  float scale;
+  void *out;
+  int64_t ldo;
+  void *workspace;
+  size_t workspace_bytes;
+};
+tq_status paged_store_launch(const tq_quantizer *qk, const tq_quantizer *qv, const tq_rows &krows,
+                             const tq_rows &vrows, const int64_t *slots, int64_t tokens, int kv_heads,
+                             const tq_rows &kpages, const tq_rows &vpages, int64_t npages, int page_size,
+                             cudaStream_t st);
+bool attend_paged_supported(const tq_quantizer *qk, const tq_quantizer *qv);
+size_t attend_paged_ws_bytes(const tq_quantizer *qk, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t max_new,
+                             int64_t max_pages, int page_size);
+tq_status attend_paged_launch(const tq_quantizer *qk, const tq_quantizer *qv, const PagedArgs &a, cudaStream_t st);
 // S generated on the device from its stream key: count fp16 entries, row-major
 tq_status qjl_matrix_launch(uint64_t key, int64_t count, uint16_t *s16, cudaStream_t st);
 tq_status rerank_launch(const float *y, int64_t nq, int64_t ldy, const void *x, bool bf16, int64_t n, int64_t ldx,
