@@ -1,0 +1,6 @@
+// Paged attention of few rows: head dimension 64, inner-product keys.
+#include "tq_paged_rows.cuh"
+
+namespace tq {
+template tq_status paged_rows_launch<64, true>(const PagedParams &, int, int, int64_t, cudaStream_t);
+}  // namespace tq
