@@ -184,6 +184,34 @@ tq_status tq_attend(const tq_quantizer *qv, const float *logits, int64_t ldl, in
                     int64_t keys_per_group, int64_t key_base, int64_t nkeys, float *out,
                     int64_t ldo, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------- prompts
+ * tq_attend_prompt: causal attention of whole prompts on their raw 16-bit
+ * queries, keys and values, before these are encoded into the cache (the
+ * article quantizes the cache of what has been generated; a prompt attends
+ * to itself at full precision).
+ *   q: any quantizer with d = 64 or 128: gives the head dimension, the device
+ *       and the error word (tq_sync_check).
+ *   y, k, v: `dtype` (TQ_BF16 or TQ_F16); token t, head h at y + t*ldy + h*d
+ *       (heads of them), k + t*ldk + h*d and v + t*ldv + h*d (kv_heads).
+ *       16-byte aligned, leading dimensions multiples of 8 (slices of one
+ *       projection's output need no copies); out likewise.  heads is a
+ *       multiple of kv_heads, by at most 128; query head h reads KV head
+ *       h / (heads / kv_heads).  out must not overlap the inputs.
+ *   cu_seqlens: device int32 [nseq + 1], not decreasing, within [0, total]:
+ *       sequence i is the tokens [cu_seqlens[i], cu_seqlens[i+1]), possibly
+ *       none.  Tokens of no sequence are left as they were in out.
+ *   scale: multiplies the logits before the softmax; finite, of either sign.
+ * out_t = sum_{j <= t} softmax_j(scale <y_t, k_j>) v_j over t's sequence:
+ * products and sums in fp32, the weights rounded to `dtype` (up to 2^8, before
+ * the division by their fp32 sum).  What a token does not see does not reach
+ * its output, whatever it holds.  Takes no workspace; lengths are read on the
+ * device, so a captured call can be replayed with others.
+ * total == 0 or nseq == 0: no-op. */
+tq_status tq_attend_prompt(const tq_quantizer *q, tq_dtype dtype, const void *y, int64_t ldy, const void *k,
+                           int64_t ldk, const void *v, int64_t ldv, int64_t total,
+                           const int32_t *cu_seqlens, int64_t nseq, int64_t heads, int64_t kv_heads,
+                           float scale, void *out, int64_t ldo, void *stream);
+
 /* ---------------------------------------------------------------- paged cache
  * A quantized KV cache in pages (TurboQuant article 4.1.1: the cache's keys
  * and values are both quantized; the pages are silent on its memory, and

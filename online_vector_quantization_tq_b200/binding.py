@@ -67,6 +67,8 @@ def lib() -> ctypes.CDLL:
         "tq_set_qjl_onthefly": (i32, [vp, i32]),
         "tq_attend_workspace_bytes": (sz, [vp, i64, i64, i64]),
         "tq_attend": (i32, [vp, vp, i64, i64, i64, ctypes.c_float, vp, vp, i64, i64, i64, vp, i64, vp, sz, vp]),
+        "tq_attend_prompt": (i32, [vp, i32, vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, i64, ctypes.c_float, vp, i64,
+                                   vp]),
         "tq_paged_store": (i32, [vp, vp, rows, rows, vp, i64, i64, rows, rows, i64, i32, vp]),
         "tq_attend_paged_workspace_bytes": (sz, [vp, vp, i64, i64, i64, i64, i64, i64, i32]),
         "tq_attend_paged": (i32, [vp, vp, i32, vp, i64, i64, vp, i64, i64, i64, i64, rows, rows, i64, i32, vp, i64,
@@ -420,6 +422,35 @@ def _check_caches(qk: Quantizer, qv: Quantizer, kcache: PagedCache, vcache: Page
         raise ValueError("kcache and vcache must have the same pages, KV heads and page size")
     _cuda(kcache=kcache.codes, vcache=vcache.codes)
     return kcache.codes.shape[:3]
+
+
+def tq_attend_prompt(q: Quantizer, y: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                     scale: float, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention of packed prompts on raw rows: y [tokens, heads*d], k
+    and v [tokens, kv_heads*d] (bf16 or fp16; views of one projection's output
+    will do), sequence i the tokens cu_seqlens[i] to cu_seqlens[i+1] (int32).
+    q, any quantizer, gives d and the device.  Rows of out for tokens of no
+    sequence are not written."""
+    total = y.shape[0]
+    if y.dim() != 2 or k.dim() != 2 or k.shape != v.shape or k.shape[0] != total:
+        raise ValueError("y, k and v must be 2-D with the same tokens, k and v of one shape")
+    if k.shape[1] == 0 or k.shape[1] % q.d != 0 or y.shape[1] == 0 or y.shape[1] % k.shape[1] != 0:
+        raise ValueError(f"y must have a whole number of heads of {q.d} for each KV head of k and v")
+    if k.dtype != y.dtype or v.dtype != y.dtype:
+        raise TypeError("y, k and v must have one type")
+    _vector(cu_seqlens, torch.int32, "cu_seqlens")
+    if cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must have one entry more than there are sequences")
+    if out is None:
+        out = torch.empty((total, y.shape[1]), dtype=y.dtype, device=y.device)
+    elif out.dtype != y.dtype or out.shape != y.shape:
+        raise ValueError("out must have y's shape and type")
+    _cuda(y=y, k=k, v=v, cu_seqlens=cu_seqlens, out=out)
+    _check("tq_attend_prompt", lib().tq_attend_prompt(
+        q.handle, _dtype16(y), _ptr(y), _ld_rows(y), _ptr(k), _ld_rows(k), _ptr(v), _ld_rows(v), total,
+        _ptr(cu_seqlens), cu_seqlens.numel() - 1, y.shape[1] // q.d, k.shape[1] // q.d, float(scale), _ptr(out),
+        _ld_rows(out), _stream(stream)))
+    return out
 
 
 def tq_paged_store(qk: Quantizer, qv: Quantizer, kenc: Encoded, venc: Encoded, slots: torch.Tensor,

@@ -137,6 +137,30 @@ tq_status tq_attend(const tq_quantizer *qv, const float *logits, int64_t ldl, in
                            ldo, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
+tq_status tq_attend_prompt(const tq_quantizer *q, tq_dtype dtype, const void *y, int64_t ldy, const void *k,
+                           int64_t ldk, const void *v, int64_t ldv, int64_t total, const int32_t *cu_seqlens,
+                           int64_t nseq, int64_t heads, int64_t kv_heads, float scale, void *out, int64_t ldo,
+                           void *stream) {
+  if (!q || total < 0 || nseq < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0) return TQ_ERR_INVALID_ARG;
+  if ((q->d != 64 && q->d != 128) || (dtype != TQ_BF16 && dtype != TQ_F16) || heads / kv_heads > 128)
+    return TQ_ERR_UNSUPPORTED;
+  if (total > (1 << 30) || nseq > (1 << 24) || heads > (1 << 16)) return TQ_ERR_TOO_LARGE;
+  if (total == 0 || nseq == 0) return TQ_OK;
+  if (!y || !k || !v || !cu_seqlens || !out || !std::isfinite(scale)) return TQ_ERR_INVALID_ARG;
+  const int64_t w = heads * q->d, wk = kv_heads * q->d;
+  if (ldy < w || ldo < w || ldk < wk || ldv < wk) return TQ_ERR_INVALID_ARG;
+  if (!aligned(y, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || ldy % 8 != 0 || ldk % 8 != 0 ||
+      ldv % 8 != 0 || ldo % 8 != 0 || !aligned(cu_seqlens, 4))
+    return TQ_ERR_ALIGNMENT;
+  const int64_t far = (int64_t)1 << 38;  // a tensor map's strides end at 2^40 bytes
+  if (ldy > far || ldk > far || ldv > far) return TQ_ERR_TOO_LARGE;
+  if (q->device < 0) return TQ_ERR_UNSUPPORTED;
+  DeviceGuard g(q->device);
+  if (!g.ok) return TQ_ERR_CUDA;
+  const tq::PromptArgs a{dtype, y, k, v, ldy, ldk, ldv, total, cu_seqlens, nseq, heads, kv_heads, scale, out, ldo};
+  return tq::attend_prompt_launch(q, a, static_cast<cudaStream_t>(stream));
+}
+
 // Shared checks of the paged cache: page size, array pointers and alignment.
 static tq_status check_pages(const tq_quantizer *q, const tq_rows *r, int64_t npages, int page_size) {
   if (!r || npages < 0 || page_size < 16 || page_size > 1024 || page_size % 16 != 0) return TQ_ERR_INVALID_ARG;

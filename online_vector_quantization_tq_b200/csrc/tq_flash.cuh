@@ -1,0 +1,190 @@
+// The softmax half of attention tiles whose products run on tcgen05: shared
+// by the prompt kernel and the paged kernel for many new tokens.
+//
+// A warpgroup (four warps) owns a tile of 128 query rows, one row per thread.
+// Its logits S (128 x 128 keys, fp32) lie in TMEM; the weights P go back as
+// 16-bit values over S's first 64 columns, where the second product reads
+// them as its A operand, and the output accumulator O (128 x D, fp32) stays in
+// TMEM until the end.
+//
+// The exponent's reference is the running maximum, but it moves (and O and the
+// running sum are rescaled) only when the maximum has grown by more than
+// 2^kSlack since: weights then stay below 2^kSlack, which both 16-bit types and
+// the fp32 sums hold without loss, and after the first tiles O is hardly ever
+// read back.
+//
+// 128 x 128 exponentials cost the special-function units as many cycles as
+// the tile's two products cost the tensor cores, so some of them run on the
+// FMA pipe instead (ex2_poly2).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "tq_sm100.cuh"
+
+namespace tq {
+namespace flash {
+
+constexpr float kSlack = 8.f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t &>(d))
+      : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t &>(d))
+      : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t &>(d))
+      : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+  return d;
+}
+
+// 2^x of two values on the FMA pipe: x = n + f with n the nearest integer
+// (round to nearest by adding 1.5 2^23) and |f| <= 1/2, 2^f by a polynomial
+// times 2^n made from n's bits.  Below -127 the result is 0 exactly (2^-127's
+// exponent field is 0) and a NaN stays one.  Coefficients: minimax fit of the relative error
+// over |f| <= 1/2, largest error 2^-13.2 (degree 3, for bf16 weights, rounded
+// at 2^-9) and 2^-18.4 (degree 4, for fp16 weights, rounded at 2^-12).
+template <bool BF16>
+__device__ __forceinline__ float2 ex2_poly2(float2 x) {
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.x));  // -127
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.y));
+  const float2 magic = make_float2(12582912.f, 12582912.f);
+  const float2 t = add2(x, magic);
+  const float2 n = add2(t, make_float2(-12582912.f, -12582912.f));
+  const float2 f = fma2(n, make_float2(-1.f, -1.f), x);
+  float2 p;
+  if constexpr (BF16) {
+    p = fma2(f, make_float2(0.05500893294811249f, 0.05500893294811249f), make_float2(0.2422109693288803f, 0.2422109693288803f));
+    p = fma2(f, p, make_float2(0.6932829022407532f, 0.6932829022407532f));
+  } else {
+    p = fma2(f, make_float2(0.009582852944731712f, 0.009582852944731712f), make_float2(0.055906426161527634f, 0.055906426161527634f));
+    p = fma2(f, p, make_float2(0.24024099111557007f, 0.24024099111557007f));
+    p = fma2(f, p, make_float2(0.6931241750717163f, 0.6931241750717163f));
+  }
+  p = fma2(f, p, make_float2(1.f, 1.f));
+  return mul2(p, make_float2(__uint_as_float(0x3F800000u + (__float_as_uint(t.x) << 23)),
+                             __uint_as_float(0x3F800000u + (__float_as_uint(t.y) << 23))));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float2 v) {
+  uint32_t r;
+  if constexpr (BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+  return r;
+}
+
+// One row's running softmax state, in base 2: the exponent's reference and
+// the sum of the weights.
+struct Row {
+  float ref = -INFINITY, sum = 0.f;
+};
+
+// O *= f, one row per thread (whole warps)
+template <int D>
+__device__ __forceinline__ void scale_rows(uint32_t o, float f) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    uint32_t v[32];
+    sm100::tmem_ld32(o + c, v);
+    sm100::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+    sm100::tmem_st32(o + c, v);
+  }
+  sm100::tmem_wait_st();
+}
+
+// One tile of 128 keys: S at `s` -> P over it; `o` rescaled when the reference
+// moves (first: O is not there yet).  mult >= 0 turns logits into base-2
+// exponents.  MASK: the row sees the tile's first `see` keys alone.  PAIRS of
+// eight pairs of exponentials run on the FMA pipe.
+// KN (the paged cache): logits and weights carry factors of their key, read
+// from shared memory (kn multiplies the logit, vn the weight behind the sum).
+template <int D, bool BF16, bool MASK, bool KN, int PAIRS>
+__device__ __forceinline__ void softmax_tile(uint32_t s, uint32_t o, bool first, float mult, int see, Row &row,
+                                             const float *kn = nullptr, const float *vn = nullptr) {
+  float x[128];
+  {
+    uint32_t(*v)[32] = reinterpret_cast<uint32_t(*)[32]>(x);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) sm100::tmem_ld32(s + 32 * c, v[c]);
+    sm100::tmem_wait_ld();
+  }
+  if constexpr (KN) {
+#pragma unroll
+    for (int i = 0; i < 128; i += 4) {
+      const float4 k = *reinterpret_cast<const float4 *>(kn + i);
+      const float2 a = mul2(make_float2(x[i], x[i + 1]), make_float2(k.x, k.y));
+      const float2 b = mul2(make_float2(x[i + 2], x[i + 3]), make_float2(k.z, k.w));
+      x[i] = a.x, x[i + 1] = a.y, x[i + 2] = b.x, x[i + 3] = b.y;
+    }
+  }
+  if constexpr (MASK) {
+#pragma unroll
+    for (int i = 0; i < 128; ++i) x[i] = i < see ? x[i] : -INFINITY;
+  }
+  float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+  for (int i = 4; i < 128; i += 8) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      top[k] = i + 4 + k < 128 ? fmaxf(top[k], fmaxf(x[i + k], x[i + 4 + k])) : fmaxf(top[k], x[i + k]);
+  }
+  const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mult;
+  // a row without visible keys keeps its reference (0 * inf is a NaN: not greater)
+  const bool grow = most > row.ref + kSlack || (row.ref == -INFINITY && most > -INFINITY);
+  if (__any_sync(0xffffffffu, grow)) {
+    float f = 1.f;
+    if (most > row.ref) {
+      f = ex2(row.ref - most);  // 0 for the first visible keys
+      row.ref = most;
+      row.sum *= f;
+    }
+    if (!first) scale_rows<D>(o, f);
+  }
+  const float base = row.ref == -INFINITY ? 0.f : -row.ref;
+  const float2 m2 = make_float2(mult, mult), b2 = make_float2(base, base);
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const int k = 64 * h + 2 * i;
+      float2 e = fma2(make_float2(x[k], x[k + 1]), m2, b2);
+      if (i % 8 >= 8 - PAIRS)
+        e = ex2_poly2<BF16>(e);
+      else
+        e = make_float2(ex2(e.x), ex2(e.y));
+      sum[i & 1] = add2(sum[i & 1], e);
+      if constexpr (KN) e = mul2(e, *reinterpret_cast<const float2 *>(vn + k));
+      w[i] = pack16<BF16>(e);
+    }
+    sm100::tmem_st32(s + 32 * h, w);
+  }
+  row.sum += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+  sm100::tmem_wait_st();
+}
+
+}  // namespace flash
+}  // namespace tq

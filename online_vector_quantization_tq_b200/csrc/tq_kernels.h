@@ -64,6 +64,19 @@ size_t attend_ws_bytes(int64_t groups, int64_t G, int d, int64_t nkeys);
 tq_status attend_launch(const tq_quantizer *qv, const float *logits, int64_t ldl, int64_t groups, int64_t G,
                         float scale, const void *vcodes, const float *vnorms, int64_t kpg, int64_t key_base,
                         int64_t nkeys, float *out, int64_t ldo, void *ws, size_t ws_bytes, cudaStream_t st);
+// attention of whole prompts on raw queries, keys and values
+struct PromptArgs {
+  tq_dtype dtype;
+  const void *y, *k, *v;
+  int64_t ldy, ldk, ldv, total;
+  const int32_t *cu;
+  int64_t nseq, heads, kv_heads;
+  float scale;
+  void *out;
+  int64_t ldo;
+};
+tq_status attend_prompt_launch(const tq_quantizer *q, const PromptArgs &a, cudaStream_t st);
+
 // a quantized KV cache in pages
 struct PagedArgs {
   tq_dtype dtype;
