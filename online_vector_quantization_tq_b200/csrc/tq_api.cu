@@ -218,7 +218,7 @@ size_t tq_attend_paged_workspace_bytes(const tq_quantizer *qk, const tq_quantize
   if (total_q == 0 || nseq == 0 || max_new == 0 || qk->device < 0) return 0;
   DeviceGuard g(qk->device);
   if (!g.ok) return 0;
-  return tq::attend_paged_ws_bytes(qk, nseq, heads, kv_heads, max_new, max_pages, page_size);
+  return tq::attend_paged_ws_bytes(qk, total_q, nseq, heads, kv_heads, max_new);
 }
 
 tq_status tq_attend_paged(const tq_quantizer *qk, const tq_quantizer *qv, tq_dtype dtype, const void *y, int64_t ldy,

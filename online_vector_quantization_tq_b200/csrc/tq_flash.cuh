@@ -94,10 +94,18 @@ __device__ __forceinline__ uint32_t pack16(float2 v) {
 }
 
 // One row's running softmax state, in base 2: the exponent's reference and
-// the sum of the weights.
+// the sum of the weights.  Where keys bring factors of their own (the value
+// norms of the paged cache), scale is the power of two above those seen, and
+// weights and sum are relative to ref + scale.
 struct Row {
-  float ref = -INFINITY, sum = 0.f;
+  float ref = -INFINITY, sum = 0.f, scale = -100.f;
 };
+
+// Exponent of the power of two above v (v >= 0), kept where neither it nor
+// the weights under it leave fp32
+__device__ __forceinline__ float exponent_above(float v) {
+  return fminf(fmaxf((float)((int)(__float_as_uint(v) >> 23) - 126), -100.f), 100.f);
+}
 
 // O *= f, one row per thread (whole warps)
 template <int D>
@@ -114,73 +122,101 @@ __device__ __forceinline__ void scale_rows(uint32_t o, float f) {
   sm100::tmem_wait_st();
 }
 
+// Logits of 32 columns as they come from TMEM, times their keys' factors and
+// masked.
+template <bool MASK, bool KN>
+__device__ __forceinline__ void columns(float (&x)[32], int col, int see, const float *kn) {
+  if constexpr (KN) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const float4 k = *reinterpret_cast<const float4 *>(kn + col + i);
+      const float2 a = mul2(make_float2(x[i], x[i + 1]), make_float2(k.x, k.y));
+      const float2 b = mul2(make_float2(x[i + 2], x[i + 3]), make_float2(k.z, k.w));
+      if constexpr (MASK) {
+        x[i] = k.x < 0.f ? -INFINITY : a.x;
+        x[i + 1] = k.y < 0.f ? -INFINITY : a.y;
+        x[i + 2] = k.z < 0.f ? -INFINITY : b.x;
+        x[i + 3] = k.w < 0.f ? -INFINITY : b.y;
+      } else {
+        x[i] = a.x, x[i + 1] = a.y, x[i + 2] = b.x, x[i + 3] = b.y;
+      }
+    }
+  }
+  if constexpr (MASK) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = col + i < see ? x[i] : -INFINITY;
+  }
+}
+
 // One tile of 128 keys: S at `s` -> P over it; `o` rescaled when the reference
 // moves (first: O is not there yet).  mult >= 0 turns logits into base-2
 // exponents.  MASK: the row sees the tile's first `see` keys alone.  PAIRS of
 // eight pairs of exponentials run on the FMA pipe.
 // KN (the paged cache): logits and weights carry factors of their key, read
-// from shared memory (kn multiplies the logit, vn the weight behind the sum).
+// from shared memory: kn multiplies the logit (below 0: no such key, looked at
+// under MASK), vn the weight behind the sum; vmost is the largest vn.
+// S is read twice, for the maximum and for the weights, 32 columns at a time,
+// each read issued before the columns in hand are worked on: a row of 128
+// logits in registers would leave too few for the rest.  (P's columns reach no
+// further than S's that are read already.)
 template <int D, bool BF16, bool MASK, bool KN, int PAIRS>
 __device__ __forceinline__ void softmax_tile(uint32_t s, uint32_t o, bool first, float mult, int see, Row &row,
-                                             const float *kn = nullptr, const float *vn = nullptr) {
-  float x[128];
-  {
-    uint32_t(*v)[32] = reinterpret_cast<uint32_t(*)[32]>(x);
+                                             const float *kn = nullptr, const float *vn = nullptr, float vmost = 0.f) {
+  uint32_t buf[2][32];
+  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  sm100::tmem_ld32(s, buf[0]);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) sm100::tmem_ld32(s + 32 * c, v[c]);
+  for (int c = 0; c < 4; ++c) {
     sm100::tmem_wait_ld();
-  }
-  if constexpr (KN) {
+    sm100::tmem_ld32(s + 32 * ((c + 1) & 3), buf[(c + 1) & 1]);
+    float(&x)[32] = reinterpret_cast<float(&)[32]>(buf[c & 1]);
+    columns<MASK, KN>(x, 32 * c, see, kn);
 #pragma unroll
-    for (int i = 0; i < 128; i += 4) {
-      const float4 k = *reinterpret_cast<const float4 *>(kn + i);
-      const float2 a = mul2(make_float2(x[i], x[i + 1]), make_float2(k.x, k.y));
-      const float2 b = mul2(make_float2(x[i + 2], x[i + 3]), make_float2(k.z, k.w));
-      x[i] = a.x, x[i + 1] = a.y, x[i + 2] = b.x, x[i + 3] = b.y;
-    }
-  }
-  if constexpr (MASK) {
+    for (int i = 0; i < 32; i += 8)
 #pragma unroll
-    for (int i = 0; i < 128; ++i) x[i] = i < see ? x[i] : -INFINITY;
-  }
-  float top[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-  for (int i = 4; i < 128; i += 8) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      top[k] = i + 4 + k < 128 ? fmaxf(top[k], fmaxf(x[i + k], x[i + 4 + k])) : fmaxf(top[k], x[i + k]);
+      for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], fmaxf(x[i + k], x[i + 4 + k]));
   }
   const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mult;
-  // a row without visible keys keeps its reference (0 * inf is a NaN: not greater)
-  const bool grow = most > row.ref + kSlack || (row.ref == -INFINITY && most > -INFINITY);
+  bool grow = most > row.ref + kSlack || (row.ref == -INFINITY && most > -INFINITY);
+  float scale = row.scale;
+  if constexpr (KN) {
+    scale = fmaxf(scale, exponent_above(vmost));
+    grow |= scale > row.scale;
+  }
+  sm100::tmem_wait_ld();
   if (__any_sync(0xffffffffu, grow)) {
-    float f = 1.f;
+    float up = scale - row.scale;
+    row.scale = scale;
     if (most > row.ref) {
-      f = ex2(row.ref - most);  // 0 for the first visible keys
+      up += most - row.ref;  // infinite for the first visible keys
       row.ref = most;
-      row.sum *= f;
     }
+    const float f = ex2(-up);
+    row.sum *= f;
     if (!first) scale_rows<D>(o, f);
   }
-  const float base = row.ref == -INFINITY ? 0.f : -row.ref;
+  const float base = row.ref == -INFINITY ? 0.f : KN ? -(row.ref + row.scale) : -row.ref;
   const float2 m2 = make_float2(mult, mult), b2 = make_float2(base, base);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t w[32];
+  for (int c = 0; c < 4; ++c) {
+    if (c > 0) sm100::tmem_wait_ld();
+    if (c < 3) sm100::tmem_ld32(s + 32 * (c + 1), buf[(c + 1) & 1]);
+    float(&x)[32] = reinterpret_cast<float(&)[32]>(buf[c & 1]);
+    columns<MASK, KN>(x, 32 * c, see, kn);
+    uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const int k = 64 * h + 2 * i;
-      float2 e = fma2(make_float2(x[k], x[k + 1]), m2, b2);
+    for (int i = 0; i < 16; ++i) {
+      float2 e = fma2(make_float2(x[2 * i], x[2 * i + 1]), m2, b2);
       if (i % 8 >= 8 - PAIRS)
         e = ex2_poly2<BF16>(e);
       else
         e = make_float2(ex2(e.x), ex2(e.y));
       sum[i & 1] = add2(sum[i & 1], e);
-      if constexpr (KN) e = mul2(e, *reinterpret_cast<const float2 *>(vn + k));
+      if constexpr (KN) e = mul2(e, *reinterpret_cast<const float2 *>(vn + 32 * c + 2 * i));
       w[i] = pack16<BF16>(e);
     }
-    sm100::tmem_st32(s + 32 * h, w);
+    sm100::tmem_st16(s + 16 * c, w);
   }
   row.sum += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
   sm100::tmem_wait_st();

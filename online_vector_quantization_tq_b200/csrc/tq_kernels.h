@@ -101,8 +101,8 @@ tq_status paged_store_launch(const tq_quantizer *qk, const tq_quantizer *qv, con
                              const tq_rows &kpages, const tq_rows &vpages, int64_t npages, int page_size,
                              cudaStream_t st);
 bool attend_paged_supported(const tq_quantizer *qk, const tq_quantizer *qv);
-size_t attend_paged_ws_bytes(const tq_quantizer *qk, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t max_new,
-                             int64_t max_pages, int page_size);
+size_t attend_paged_ws_bytes(const tq_quantizer *qk, int64_t total_q, int64_t nseq, int64_t heads, int64_t kv_heads,
+                             int64_t max_new);
 tq_status attend_paged_launch(const tq_quantizer *qk, const tq_quantizer *qv, const PagedArgs &a, cudaStream_t st);
 // S generated on the device from its stream key: count fp16 entries, row-major
 tq_status qjl_matrix_launch(uint64_t key, int64_t count, uint16_t *s16, cudaStream_t st);

@@ -64,61 +64,178 @@ __global__ void __launch_bounds__(256) k_paged_store(const StoreParams p) {
   }
 }
 
+// ---------------------------------------------------------------- queries
+
+// Rotated queries (and their projections) of all rows as fp16 operands of the
+// kernel of many rows: row (token * heads + head) is R y / U, and for
+// inner-product keys S R y / (64 U) behind it, U a power of two above the row's
+// largest coordinate, which goes to qscale.  Coordinates stand where the
+// expansion of packed codes and signs puts them.  16 rows a block.
+template <int D, bool IP>
+__global__ void __launch_bounds__(128) k_paged_queries(const __grid_constant__ PagedParams p, int w) {
+  constexpr int V = D / 32, DQ = IP ? 2 * D : D;
+  __shared__ __align__(16) uint16_t yh[IP ? 16 * D : 1], yl[IP ? 16 * D : 1];
+  __shared__ __align__(16) uint16_t stage[16 * DQ];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t row0 = (int64_t)blockIdx.x * 16, total = p.total_q * p.heads;
+  float v[4][V];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = row0 + 4 * warp + i;
+    const bool there = row < total;
+    const int64_t at = there ? row / p.heads * p.ldy + row % p.heads * D + lane * V : 0;
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[i][e] = there ? load16(p.y, at + e, p.bf16) : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) warp_rotate<D>(v[i], p.kdiag, lane);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * warp + i;
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) top = fmaxf(top, fabsf(v[i][e]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float up = pow2_above(top), down = 1.0f / up;
+    if (lane == 0 && row0 + r < total) p.qscale[row0 + r] = up;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const int j = lane * V + e;
+      const float x = v[i][e] * down;
+      const __half hi = __float2half_rn(x);
+      stage[r * DQ + (w == 1 ? j / 32 * 32 + 8 * (j % 4) + j % 32 / 4 : j)] = __half_as_ushort(hi);
+      if constexpr (IP) {
+        yh[r * D + j] = __half_as_ushort(hi);
+        yl[r * D + j] = __half_as_ushort(__float2half_rn(x - __half2float(hi)));
+      }
+    }
+  }
+  __syncthreads();
+  if constexpr (IP) {
+    // p = S y~ with y~ as two fp16 terms; warp w has the 8-column tiles w, w + 4, ..
+    const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int t = warp; t < D / 8; t += 4) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint32_t *srow = reinterpret_cast<const uint32_t *>(p.qjl + (t * 8 + r) * D);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t b0 = __ldg(srow + 8 * k + c), b1 = __ldg(srow + 8 * k + c + 4);
+#pragma unroll
+        for (int term = 0; term < 2; ++term) {
+          const uint32_t *ya = reinterpret_cast<const uint32_t *>((term ? yl : yh) + r * D + 16 * k) + c;
+          const uint32_t a[4] = {ya[0], ya[8 * (D / 2)], ya[4], ya[8 * (D / 2) + 4]};
+          mma16816(acc, a, b0, b1);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = t * 8 + 2 * c + (e & 1), b = j % 32;  // bits k and k + 16 of a word are neighbours
+        stage[(r + 8 * (e >> 1)) * DQ + D + j / 32 * 32 + (b < 16 ? 2 * b : 2 * (b - 16) + 1)] =
+            __half_as_ushort(__float2half_rn(acc[e] * (1.0f / 64.0f)));
+      }
+    }
+    __syncthreads();
+  }
+  const int64_t n = min((int64_t)16, total - row0) * (DQ / 8);
+  uint4 *to = reinterpret_cast<uint4 *>(p.qprep + row0 * DQ);
+  for (int i = tid; i < n; i += 128) to[i] = reinterpret_cast<const uint4 *>(stage)[i];
+}
+
 // ---------------------------------------------------------------- join
 
-// Joins the key ranges of a row and rotates it back: one block of four warps
-// per row, which take the ranges in turn (so that their loads overlap) and
-// are added up in the order of the warps.
-template <int D>
+// Output rows from the normalized rows of whole blocks, or from the partial
+// results of the runs that share a block (added up in their order), rotated
+// back.  WARPS warps a row take its runs in turn, so that their loads overlap:
+// one where there are rows enough to fill the machine.
+template <int D, int WARPS>
 __global__ void __launch_bounds__(128) k_attend_paged_join(const __grid_constant__ PagedParams p) {
   constexpr int V = D / 32;
   __shared__ float s_v[4][D], s_l[4];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t per = (int64_t)p.max_new * p.group;
-  const int64_t w = blockIdx.x;
-  const int row = (int)(w % per);
-  const int head = (int)(w / per % p.kv_heads), seq = (int)(w / per / p.kv_heads);
-  const Seq s = seq_of(p, seq);
-  if (row >= s.n * p.group) return;
-  const int count = p.splits[seq];
-  if (count == 1) return;  // written by its work item
-  const float2 *ml = p.part_ml + w * p.nsplit;
-  const float *po = p.part_o + w * p.nsplit * D + lane * V;
-  float M = -INFINITY;
-  for (int i = lane; i < count; i += 32) M = fmaxf(M, ml[i].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.f, v[V];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WARPS;
+  const int64_t gr = (int64_t)blockIdx.x * (4 / WARPS) + warp / WARPS;
+  const int64_t token = gr / p.heads;
+  const int h = (int)(gr % p.heads), head = h / p.group;
+  // the last sequence that starts at or before the token
+  bool there = gr < p.total_q * p.heads;
+  int lo = 0, hi = p.nseq;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (__ldg(p.q_start + mid) <= token)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const Seq s = seq_of(p, lo);
+  there = there && token >= s.start && token < s.start + s.n;
+  float v[V], L = 0.f;
 #pragma unroll
   for (int e = 0; e < V; ++e) v[e] = 0.f;
+  bool alone = true;
+  if (there) {
+    const PagedCut &c = s.n * p.group <= p.few.upto ? p.few : p.many;
+    const int row = (int)(token - s.start) * p.group + h % p.group, block = row / c.rows;
+    const int units = units_of(p, c, s, block);
+    if (units > 0) {
+      int64_t u0 = __ldg(c.first + lo) + head * head_units(p, c, s);
+      for (int k = 0; k < block; ++k) u0 += units_of(p, c, s, k);
+      const int64_t per = run_units(c, __ldg(c.first + p.nseq));
+      const int b0 = (int)(u0 / per), b1 = (int)((u0 + units - 1) / per);
+      if (b0 == b1) {
+        if (part == 0) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) v[e] = p.whole[gr * D + lane * V + e];
+          L = 1.f;
+        }
+      } else {
+        alone = false;
+        const int in = row % c.rows;
+        auto at = [&](int b) { return ((int64_t)2 * b + (b == b0 ? 1 : 0)) * c.rows + in; };
+        float M = -INFINITY;
+        for (int b = b0 + lane; b <= b1; b += 32) M = fmaxf(M, c.part_ml[at(b)].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
 #pragma unroll 4
-  for (int i = warp; i < count; i += 4) {
-    const float2 a = ml[i];
-    float b[V];
+        for (int b = b0 + part; b <= b1; b += WARPS) {
+          const float2 a = c.part_ml[at(b)];
+          const float *po = c.part_o + at(b) * D + lane * V;
+          float x[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) b[e] = po[(int64_t)i * D + e];
-    if (a.y != 0.f) {  // the row sees some of the range's keys
-      const float f = a.x == -INFINITY ? 0.f : ex2(a.x - M);
-      L = fmaf(f, a.y, L);
+          for (int e = 0; e < V; ++e) x[e] = po[e];
+          if (a.y != 0.f) {  // the row sees some of the run's keys
+            const float f = a.x == -INFINITY ? 0.f : ex2(a.x - M);
+            L = fmaf(f, a.y, L);
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[e] = fmaf(f, b[e], v[e]);
+            for (int e = 0; e < V; ++e) v[e] = fmaf(f, x[e], v[e]);
+          }
+        }
+      }
     }
   }
+  if constexpr (WARPS > 1) {
+    if (!alone) {  // (of the whole block: it has one row)
 #pragma unroll
-  for (int e = 0; e < V; ++e) s_v[warp][lane * V + e] = v[e];
-  if (lane == 0) s_l[warp] = L;
-  __syncthreads();
-  if (warp > 0) return;
-  L = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+      for (int e = 0; e < V; ++e) s_v[warp][lane * V + e] = v[e];
+      if (lane == 0) s_l[warp] = L;
+    }
+    __syncthreads();
+    if (warp > 0) return;
+    if (!alone) {
+      L = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const int j = lane * V + e;
+        v[e] = s_v[0][j] + s_v[1][j] + s_v[2][j] + s_v[3][j];
+      }
+    }
+  }
+  if (!there) return;
   const float inv = L != 0.f ? 1.0f / L : 0.f;
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    const int j = lane * V + e;
-    v[e] = (s_v[0][j] + s_v[1][j] + s_v[2][j] + s_v[3][j]) * inv;
-  }
+  for (int e = 0; e < V; ++e) v[e] *= inv;
   warp_rotate_back<D>(v, p.vdiag, lane);
-  write_row<D>(p.out, (int64_t)(s.start + row / p.group) * p.ldo + (int64_t)(head * p.group + row % p.group) * D, v,
-               lane, p.bf16);
+  write_row<D>(p.out, token * p.ldo + (int64_t)h * D, v, lane, p.bf16);
 }
 
 int device_sms() {
@@ -128,40 +245,66 @@ int device_sms() {
   return sms > 0 ? sms : 1;
 }
 
+// Sequences of more rows go to the kernel of many rows, whose blocks of 128
+// or 256 rows cost the same however few of their rows are there.
+constexpr int kFewRows = 32;
+
+// Sizes of a call and where its pieces lie in the workspace
 struct Plan {
-  int64_t tiles, nsplit, items, rows;  // rows: of partial results
-  int target;
-  size_t part_ml, splits, total;  // offsets after part_o
+  PagedCut few{}, many{};
+  size_t few_o, few_ml, few_first, many_o, many_ml, many_first, whole, qprep, qscale, total;
 };
 
-Plan plan_of(int d, int64_t nseq, int64_t kv_heads, int64_t group, int64_t max_new, int64_t cap, int sms) {
+Plan plan_of(const tq_quantizer *qk, int64_t total_q, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t max_new,
+             int sms) {
   Plan L{};
-  L.tiles = (max_new * group + kPagedRows - 1) / kPagedRows;
-  const int64_t base = nseq * kv_heads * L.tiles;
-  // about six work items per resident block (two per SM), so that the blocks
-  // that end early find others to run
-  L.target = 12 * sms;
-  const int64_t want = (L.target + base - 1) / base;
-  L.nsplit = std::max<int64_t>(1, std::min<int64_t>(want, (cap + kPagedMinSplit - 1) / kPagedMinSplit));
-  L.items = base * L.nsplit;
-  L.rows = L.nsplit > 1 ? nseq * kv_heads * max_new * group * L.nsplit : 0;
-  size_t off = (size_t)L.rows * d * sizeof(float);
-  L.part_ml = off;
-  off += (size_t)L.rows * sizeof(float2);
-  L.splits = off;
-  off += (size_t)nseq * sizeof(int);
+  const int d = qk->d;
+  const bool ip = qk->m > 0;
+  const int64_t most = std::min(max_new, total_q) * (heads / kv_heads);
+  const bool many = most > kFewRows;
+  // 8 rows a block where that is all there is: twice the warps on an SM
+  L.few = PagedCut{most <= 8 ? 8 : 16, 64, 0, many ? kFewRows : 0x7fffffff, sms, 4, nullptr, nullptr, nullptr};
+  if (many) L.many = PagedCut{ip && d == 128 ? 128 : 256, 128, kFewRows, 0x7fffffff, sms, 2, nullptr, nullptr, nullptr};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += (bytes + 255) & ~size_t(255);
+    return at;
+  };
+  auto cut = [&](const PagedCut &c, size_t &o, size_t &ml, size_t &first) {
+    o = take((size_t)2 * c.grid * c.rows * d * sizeof(float));
+    ml = take((size_t)2 * c.grid * c.rows * sizeof(float2));
+    first = take(c.grid ? (size_t)(nseq + 1) * sizeof(int64_t) : 0);
+  };
+  cut(L.few, L.few_o, L.few_ml, L.few_first);
+  cut(L.many, L.many_o, L.many_ml, L.many_first);
+  L.whole = take((size_t)total_q * heads * d * sizeof(float));
+  L.qprep = take(many ? (size_t)total_q * heads * d * (ip ? 4 : 2) : 0);
+  L.qscale = take(many ? (size_t)total_q * heads * sizeof(float) : 0);
   L.total = off + 256;
   return L;
 }
 
 template <int D>
-tq_status launch_paged(const PagedParams &prm, const tq_quantizer *qk, const tq_quantizer *qv, int64_t items,
-                       cudaStream_t st) {
-  const tq_status rc = qk->m ? paged_rows_launch<D, true>(prm, qk->w, qv->w, items, st)
-                             : paged_rows_launch<D, false>(prm, qk->w, qv->w, items, st);
-  if (rc != TQ_OK || prm.nsplit == 1) return rc;
-  const int64_t rows = (int64_t)prm.nseq * prm.kv_heads * prm.max_new * prm.group;
-  k_attend_paged_join<D><<<(unsigned)rows, 128, 0, st>>>(prm);
+tq_status launch_paged(const PagedParams &prm, const tq_quantizer *qk, const tq_quantizer *qv, cudaStream_t st) {
+  tq_status rc = TQ_OK;
+  const int64_t rows = prm.total_q * prm.heads;
+  if (prm.many.grid > 0) {
+    const unsigned blocks = (unsigned)((rows + 15) / 16);
+    if (qk->m)
+      k_paged_queries<D, true><<<blocks, 128, 0, st>>>(prm, qk->w);
+    else
+      k_paged_queries<D, false><<<blocks, 128, 0, st>>>(prm, qk->w);
+    if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
+    rc = qk->m ? paged_tiles_launch<D, true>(prm, qk->w, qv->w, st) : paged_tiles_launch<D, false>(prm, qk->w, qv->w, st);
+    if (rc != TQ_OK) return rc;
+  }
+  rc = qk->m ? paged_rows_launch<D, true>(prm, qk->w, qv->w, st) : paged_rows_launch<D, false>(prm, qk->w, qv->w, st);
+  if (rc != TQ_OK) return rc;
+  if (rows >= 32 * (int64_t)prm.few.grid)
+    k_attend_paged_join<D, 1><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(prm);
+  else
+    k_attend_paged_join<D, 4><<<(unsigned)rows, 128, 0, st>>>(prm);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
@@ -199,18 +342,18 @@ bool attend_paged_supported(const tq_quantizer *qk, const tq_quantizer *qv) {
          (qk->d == 64 || qk->d == 128) && qv->m == 0 && qv->w >= 2 && qv->w <= 4 && qk->w >= 1 && qk->w <= 4;
 }
 
-size_t attend_paged_ws_bytes(const tq_quantizer *qk, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t max_new,
-                             int64_t max_pages, int page_size) {
-  return plan_of(qk->d, nseq, kv_heads, heads / kv_heads, max_new, max_pages * page_size, device_sms()).total;
+size_t attend_paged_ws_bytes(const tq_quantizer *qk, int64_t total_q, int64_t nseq, int64_t heads, int64_t kv_heads,
+                             int64_t max_new) {
+  return plan_of(qk, total_q, nseq, heads, kv_heads, max_new, device_sms()).total;
 }
 
 tq_status attend_paged_launch(const tq_quantizer *qk, const tq_quantizer *qv, const PagedArgs &a, cudaStream_t st) {
   PagedParams prm{};
   const int64_t group = a.heads / a.kv_heads;
-  const Plan L = plan_of(qk->d, a.nseq, a.kv_heads, group, a.max_new, a.max_pages * a.page_size, device_sms());
+  const Plan L = plan_of(qk, a.total_q, a.nseq, a.heads, a.kv_heads, a.max_new, device_sms());
   if (!a.workspace || a.workspace_bytes < L.total) return TQ_ERR_WORKSPACE;
-  if (L.items > 0x7fffffff || L.rows > ((int64_t)1 << 40)) return TQ_ERR_TOO_LARGE;
-  uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(a.workspace) + 15) & ~uintptr_t(15));
+  if (a.total_q * a.heads > 0x7fffffff) return TQ_ERR_TOO_LARGE;
+  uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(a.workspace) + 255) & ~uintptr_t(255));
   prm.y = a.y;
   prm.ldy = a.ldy;
   prm.q_start = a.q_start;
@@ -243,13 +386,19 @@ tq_status attend_paged_launch(const tq_quantizer *qk, const tq_quantizer *qv, co
   prm.kappa = qk->kt.qjl_scale;
   prm.out = a.out;
   prm.ldo = a.ldo;
-  prm.tiles = (int)L.tiles;
-  prm.nsplit = (int)L.nsplit;
-  prm.target = L.target;
-  prm.part_o = reinterpret_cast<float *>(base);
-  prm.part_ml = reinterpret_cast<float2 *>(base + L.part_ml);
-  prm.splits = reinterpret_cast<int *>(base + L.splits);
-  return qk->d == 64 ? launch_paged<64>(prm, qk, qv, L.items, st) : launch_paged<128>(prm, qk, qv, L.items, st);
+  prm.few = L.few;
+  prm.many = L.many;
+  prm.few.first = reinterpret_cast<int64_t *>(base + L.few_first);
+  prm.few.part_o = reinterpret_cast<float *>(base + L.few_o);
+  prm.few.part_ml = reinterpret_cast<float2 *>(base + L.few_ml);
+  prm.many.first = reinterpret_cast<int64_t *>(base + L.many_first);
+  prm.many.part_o = reinterpret_cast<float *>(base + L.many_o);
+  prm.many.part_ml = reinterpret_cast<float2 *>(base + L.many_ml);
+  prm.whole = reinterpret_cast<float *>(base + L.whole);
+  prm.qprep = reinterpret_cast<uint16_t *>(base + L.qprep);
+  prm.qscale = reinterpret_cast<float *>(base + L.qscale);
+  prm.err = qk->d_err;
+  return qk->d == 64 ? launch_paged<64>(prm, qk, qv, st) : launch_paged<128>(prm, qk, qv, st);
 }
 
 }  // namespace tq

@@ -1,6 +1,6 @@
 // Shared by the kernels of attention over a paged quantized cache: their
-// parameters, the split of a batch into work items, and the rotation of a row
-// held by one warp.
+// parameters, how a batch is cut into work, and the rotation of a row held by
+// one warp.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -10,8 +10,21 @@
 
 namespace tq {
 
-constexpr int kPagedRows = 16;       // query rows (new token x query head of a group) of a work item
-constexpr int kPagedMinSplit = 256;  // keys of a work item at least, where a sequence has them
+// How a batch is cut into work: a sequence's query rows (new token x query
+// head of a group, token-major) in blocks of `rows`, each with the keys that
+// its last row sees in units of `unit` keys.  The units of all (sequence, KV
+// head, block), in this order, form one line that the kernel's blocks share
+// out in equal contiguous runs, whatever the lengths are; a block of rows
+// whose units fall to several runs is put together at the end from their
+// partial results.  Sequences of more than `above` and at most `upto` rows.
+struct PagedCut {
+  int rows, unit, above, upto;
+  int grid;          // runs
+  int least;         // units of a run, at least
+  int64_t *first;    // [nseq + 1]: each sequence's first unit (written by the kernel's block 0)
+  float *part_o;     // [2 * grid][rows][D]: unnormalized outputs, rotated domain
+  float2 *part_ml;   // [2 * grid][rows]: (maximum, sum) in base 2
+};
 
 struct PagedParams {
   const void *y;  // 16-bit queries
@@ -33,18 +46,19 @@ struct PagedParams {
   float kappa;
   void *out;
   int64_t ldo;
-  int tiles;       // row tiles of a sequence and KV head, at most
-  int nsplit;      // key ranges of a sequence, at most
-  int target;      // work items wanted
-  float *part_o;   // [nseq * kv_heads][max_new * group][nsplit][D], rotated domain
-  float2 *part_ml; // same rows: (max, sum) in base 2
-  int *splits;     // [nseq]: key ranges in use
+  PagedCut few, many;  // for the kernel of few rows and the kernel of many (its grid 0: not launched)
+  float *whole;     // [total_q * heads][D]: normalized rows of blocks that one run had whole, rotated domain
+  uint16_t *qprep;  // many: [total_q * heads][D or 2 D] rotated queries, and their projections, fp16
+  float *qscale;    // many: [total_q * heads] power of two that undoes their scaling
+  int *err;
 };
 
-// Work items of up to 16 rows: one kernel per (D, inner-product keys) file,
-// chosen by the code widths of keys and values.
+// Few rows: one kernel per (D, inner-product keys) file, chosen by the code
+// widths of keys and values.  Many rows: likewise.
 template <int D, bool IP>
-tq_status paged_rows_launch(const PagedParams &prm, int wk, int wv, int64_t items, cudaStream_t st);
+tq_status paged_rows_launch(const PagedParams &prm, int wk, int wv, cudaStream_t st);
+template <int D, bool IP>
+tq_status paged_tiles_launch(const PagedParams &prm, int wk, int wv, cudaStream_t st);
 
 namespace paged {
 
@@ -59,6 +73,18 @@ __device__ __forceinline__ float load16(const void *p, int64_t i, int bf16) {
 }
 __device__ __forceinline__ uint16_t store16(float v, int bf16) {
   return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Power of two above v (v >= 0), kept where its reciprocal is normal too
+__device__ __forceinline__ float pow2_above(float v) {
+  const uint32_t e = (__float_as_uint(v) >> 23) + 1u;  // biased exponent, one up
+  return __uint_as_float(min(max(e, 2u), 252u) << 23);
 }
 
 // Unnormalized Walsh-Hadamard transform of D values held by one warp, lane l
@@ -142,25 +168,129 @@ __device__ __forceinline__ Seq seq_of(const PagedParams &p, int i) {
   return s;
 }
 
-struct Split {
-  int keys;   // keys of a range
-  int count;  // ranges
+__device__ __forceinline__ int blocks_of(const PagedParams &p, const PagedCut &c, const Seq &s) {
+  const int rows = s.n * p.group;
+  return rows > c.above && rows <= c.upto ? (rows + c.rows - 1) / c.rows : 0;
+}
+// Keys that the last row of block k sees (the first of its rows may see fewer)
+__device__ __forceinline__ int seen_by(const PagedParams &p, const PagedCut &c, const Seq &s, int k) {
+  const int last = min((k + 1) * c.rows, s.n * p.group) - 1;
+  return max(0, min(s.len, s.kv - s.n + 1 + last / p.group));
+}
+__device__ __forceinline__ int units_of(const PagedParams &p, const PagedCut &c, const Seq &s, int k) {
+  return (seen_by(p, c, s, k) + c.unit - 1) / c.unit;
+}
+__device__ __forceinline__ int64_t head_units(const PagedParams &p, const PagedCut &c, const Seq &s) {
+  int64_t u = 0;
+  for (int k = 0, n = blocks_of(p, c, s); k < n; ++k) u += units_of(p, c, s, k);
+  return u;
+}
+__device__ __forceinline__ int64_t run_units(const PagedCut &c, int64_t total) {
+  return max((total + c.grid - 1) / c.grid, (int64_t)c.least);
+}
+
+// Where a run stands: the units [unit, unit + take) of a block of rows.
+struct Cursor {
+  int seq, head, block, unit, take;
+  int units;     // of the block
+  int64_t left;  // units of the run from here on
+  Seq s;
+
+  __device__ bool whole() const { return take == units; }
+  // partial results of a block that this run has in part: a run has at most
+  // two such blocks, one that began before it and one that goes on behind it
+  __device__ int slot() const { return 2 * (int)blockIdx.x + (unit == 0 ? 1 : 0); }
+  __device__ void load(const PagedParams &p, const PagedCut &c) {
+    units = units_of(p, c, s, block);
+    take = (int)min((int64_t)(units - unit), left);
+  }
+  // the next block of rows with units; false at the end of the run
+  __device__ bool next(const PagedParams &p, const PagedCut &c) {
+    left -= take;
+    if (left <= 0) return false;
+    unit = 0;
+    for (;;) {
+      if (++block >= blocks_of(p, c, s)) {
+        block = 0;
+        if (++head >= p.kv_heads) {
+          head = 0;
+          do {
+            if (++seq >= p.nseq) return false;
+            s = seq_of(p, seq);
+          } while (blocks_of(p, c, s) == 0);
+        }
+      }
+      load(p, c);
+      if (units > 0) return true;
+    }
+  }
 };
 
-// The key ranges of a sequence of `len` keys: about `target` work items of
-// equal length over the whole batch, at least kPagedMinSplit keys each, at
-// most nsplit ranges a sequence, whole multiples of `step` keys.  `work` =
-// sum over sequences of keys * row tiles * KV heads.
-__device__ __forceinline__ Split split_of(const PagedParams &p, int64_t work, int len, int step) {
-  int64_t per = (work + p.target - 1) / p.target;
-  per = max(per, (int64_t)kPagedMinSplit);
-  per = max(per, (int64_t)(len + p.nsplit - 1) / p.nsplit);
-  per = (per + step - 1) / step * step;
-  per = min(per, (int64_t)1 << 30);
-  Split s;
-  s.keys = (int)per;
-  s.count = max(1, (int)((len + per - 1) / per));
-  return s;
+// The start of this block's run, found by one warp (block 0's also writes
+// c.first): sequence, head, block, unit and units of the run; false if there
+// is none.
+__device__ __forceinline__ bool find_run(const PagedParams &p, const PagedCut &c, int64_t *found) {
+  const int lane = threadIdx.x & 31;
+  int64_t total = 0;
+  for (int i0 = 0; i0 < p.nseq; i0 += 32) {
+    const int64_t u = i0 + lane < p.nseq ? head_units(p, c, seq_of(p, i0 + lane)) * p.kv_heads : 0;
+    int64_t in = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t b = __shfl_up_sync(0xffffffffu, in, o);
+      if (lane >= o) in += b;
+    }
+    if (blockIdx.x == 0 && i0 + lane < p.nseq) c.first[i0 + lane] = total + in - u;
+    total += __shfl_sync(0xffffffffu, in, 31);
+  }
+  if (blockIdx.x == 0 && lane == 0) c.first[p.nseq] = total;
+  const int64_t per = run_units(c, total), from = per * blockIdx.x;
+  if (from >= total) return false;
+  int64_t before = 0;
+  for (int i0 = 0; i0 < p.nseq; i0 += 32) {
+    Seq s{};
+    int64_t hu = 0;
+    if (i0 + lane < p.nseq) {
+      s = seq_of(p, i0 + lane);
+      hu = head_units(p, c, s);
+    }
+    int64_t in = hu * p.kv_heads;
+    const int64_t u = in;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t b = __shfl_up_sync(0xffffffffu, in, o);
+      if (lane >= o) in += b;
+    }
+    const int64_t at = from - (before + in - u);
+    if (u > 0 && at >= 0 && at < u) {
+      int64_t rest = at % hu;
+      int k = 0;
+      for (;; ++k) {
+        const int n = units_of(p, c, s, k);
+        if (rest < n) break;
+        rest -= n;
+      }
+      found[0] = i0 + lane;
+      found[1] = at / hu;
+      found[2] = k;
+      found[3] = rest;
+      found[4] = min(per, total - from);
+    }
+    before += __shfl_sync(0xffffffffu, in, 31);
+    if (before > from) break;
+  }
+  return true;
+}
+__device__ __forceinline__ Cursor start_run(const PagedParams &p, const PagedCut &c, const int64_t *found) {
+  Cursor u;
+  u.seq = (int)found[0];
+  u.head = (int)found[1];
+  u.block = (int)found[2];
+  u.unit = (int)found[3];
+  u.left = found[4];
+  u.s = seq_of(p, u.seq);
+  u.load(p, c);
+  return u;
 }
 
 }  // namespace paged

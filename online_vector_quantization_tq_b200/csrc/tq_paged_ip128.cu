@@ -2,5 +2,5 @@
 #include "tq_paged_rows.cuh"
 
 namespace tq {
-template tq_status paged_rows_launch<128, true>(const PagedParams &, int, int, int64_t, cudaStream_t);
+template tq_status paged_rows_launch<128, true>(const PagedParams &, int, int, cudaStream_t);
 }  // namespace tq

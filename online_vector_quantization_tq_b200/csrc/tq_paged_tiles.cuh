@@ -1,0 +1,564 @@
+// Attention of many query rows over a sequence's pages (chunks of a prompt,
+// long drafts): the kernel of tq_attend_paged for sequences of more rows than
+// the kernel of few rows should take.  Instantiated in tq_paged_many_*.cu.
+//
+// As the prompt kernel (tq_flash.cuh has the softmax), with key and value tiles
+// that are expanded from the packed pages instead of copied: both products run
+// on tcgen05 with fp16 operands, and the norms multiply logits and weights as
+// fp32 factors of their column.  Inner-product keys are operands of twice the
+// width, [c | +-64 gamma sqrt(pi/2)/d], against queries [R y | S R y / 64].
+//
+// One block per SM works off its run of units (PagedCut; a unit is a tile of
+// 128 keys).  Two warpgroups of softmax share the tensor cores:
+//   a block of more than 128 rows: each has a tile of 128 of the rows, and
+//     both go through the same key tiles;
+//   fewer rows (and inner-product keys of d = 128, whose two query tiles would
+//     leave no room for keys): both have the same rows, and take the key tiles
+//     in turn; their results are added up at the end.
+//
+//   warps 0-3, 4-7   softmax; they also fetch their queries and put out results
+//   warps 8-11       expand keys, one row a thread; norms
+//   warps 12-14      expand values
+//   warp 15          tcgen05
+//
+// Keys and values share one ring of slots (a tile of 16-bit rows, 128-byte
+// swizzle), in the order in which the products first need them.
+#pragma once
+
+#include "tq_expand.cuh"
+#include "tq_flash.cuh"
+#include "tq_paged.cuh"
+
+namespace tq {
+
+namespace {
+
+using namespace paged;
+
+constexpr int kTile = 128;
+constexpr int kTilesThreads = 512;
+constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 15;
+constexpr int kValueThreads = 96;
+constexpr int kNorms = 8;  // tiles whose norms are kept: more than the ring holds
+
+template <int D, bool IP>
+struct TileSmem {
+  static constexpr int kHalf = kTile * 128;              // 128 rows of 64 elements
+  static constexpr int kSlot = kHalf * (D / 64);
+  static constexpr int kSlots = D == 64 ? 8 : 4;
+  static constexpr int kWide = IP ? 2 : 1;               // slots of a key tile
+  static constexpr int kQTiles = IP && D == 128 ? 1 : 2;
+  static constexpr int kRows = kTile * kQTiles;          // rows of a block
+  static constexpr int kQ = 0, kQTile = kSlot * kWide, kRing = kQTiles * kQTile;
+  static constexpr int kKn = kRing + kSlots * kSlot, kVn = kKn + kNorms * kTile * 4;
+  static constexpr int kBytes = kVn + kNorms * kTile * 4 + 1024;
+};
+
+// Ring positions of key and value tiles: `lead` key tiles first (one where both
+// warpgroups see every tile, two where they take turns), then a value tile and
+// the next key tile by turns.  Keys and values are filled by different warps,
+// each of which sees of a slot's barrier only the phase's parity; a phase is
+// told from the one before the last because a filler's positions are never
+// more than the ring's slots apart, and slots become free in (nearly) the order
+// of their positions.  Where every key tile has two of the four slots, starting
+// each segment with its own lead would set value tiles five apart: there the
+// order runs on from one segment to the next.
+template <int WIDE, bool ON>
+struct RingPlan {
+  int lead, tiles;
+  int base, before;  // position of the segment's first slot; key tiles before the segment
+  __device__ int value(int j) const {
+    if (ON) return 2 * WIDE + (before + j) * (WIDE + 1);
+    return base + min(lead, tiles) * WIDE + j + WIDE * min(j, max(tiles - lead, 0));
+  }
+  __device__ int key(int j) const {
+    if (ON) return before + j < 2 ? (before + j) * WIDE : value(j - 2) + 1;
+    return j < lead ? base + j * WIDE : value(j - lead) + 1;
+  }
+  __device__ void done() {
+    base += tiles * (WIDE + 1);
+    before += tiles;
+  }
+};
+
+template <int D, bool IP>
+using Ring = RingPlan<TileSmem<D, IP>::kWide, IP && D == 128>;
+
+// Tiles of a segment, as every role sees them
+struct Segment {
+  bool turns;     // the warpgroups take key tiles in turn
+  int row0, rows; // first row of the block, rows of the sequence
+  int hidden, seen;
+  int t0, tiles;  // key tiles
+};
+template <int D, bool IP>
+__device__ __forceinline__ Segment segment_of(const PagedParams &p, const Cursor &cur) {
+  using SM = TileSmem<D, IP>;
+  Segment g;
+  g.rows = cur.s.n * p.group;
+  g.row0 = cur.block * SM::kRows;
+  g.turns = SM::kQTiles == 1 || g.rows - g.row0 <= kTile;
+  g.hidden = cur.s.kv - cur.s.n + 1;
+  g.seen = seen_by(p, p.many, cur.s, cur.block);
+  g.t0 = cur.unit;
+  g.tiles = cur.take;
+  return g;
+}
+// Key tiles of the segment for warpgroup i (whose first row is row0 + 128 i where they do not take turns)
+__device__ __forceinline__ int tiles_of(const PagedParams &p, const Cursor &cur, const Segment &g, int i) {
+  if (g.turns) return (g.tiles + 1 - i) / 2;
+  const int last = min(g.row0 + kTile * (i + 1), g.rows) - 1;
+  const int seen = max(0, min(cur.s.len, g.hidden + last / p.group));
+  return min(max((seen + kTile - 1) / kTile - g.t0, 0), g.tiles);
+}
+
+// fp16 centroids of a 32-coordinate group as four 16-byte chunks of row r,
+// from chunk 4 g on
+template <int W>
+__device__ __forceinline__ void expand_group(uint8_t *tile, int r, int g, const uint32_t *words,
+                                             const uint32_t (&tlo)[4], const uint32_t (&thi)[4]) {
+  uint32_t lo[8], hi[8];
+  expand_codes<W>(words, tlo, thi, lo, hi);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int chunk = 4 * g + k;
+    *reinterpret_cast<uint4 *>(tile + (chunk >> 3) * (kTile * 128) + sm100::sw128_offset(r, chunk & 7)) =
+        make_uint4(sm100::prmt(lo[2 * k], hi[2 * k], 0x5140u), sm100::prmt(lo[2 * k], hi[2 * k], 0x7362u),
+                   sm100::prmt(lo[2 * k + 1], hi[2 * k + 1], 0x5140u), sm100::prmt(lo[2 * k + 1], hi[2 * k + 1], 0x7362u));
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t *w, const uint8_t *from) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(from) + i / 4);
+      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+    }
+  } else if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(from) + i / 2);
+      w[i] = v.x, w[i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(from) + i);
+  }
+}
+
+// byte tables of the fp16 centroids
+__device__ __forceinline__ void byte_tables(const uint16_t *c, uint32_t (&lo)[4], uint32_t (&hi)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    lo[i] = hi[i] = 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      lo[i] |= (uint32_t)(c[4 * i + k] & 0xFF) << (8 * k);
+      hi[i] |= (uint32_t)(c[4 * i + k] >> 8) << (8 * k);
+    }
+  }
+}
+
+template <int D, bool IP, int WK, int WV>
+__global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const __grid_constant__ PagedParams p) {
+  using SM = TileSmem<D, IP>;
+  constexpr int DQ = IP ? 2 * D : D;  // elements of a query operand's row
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float *s_kn = reinterpret_cast<float *>(smem + SM::kKn), *s_vn = reinterpret_cast<float *>(smem + SM::kVn);
+  __shared__ uint64_t full[SM::kSlots], empty[SM::kSlots], q_full[2], s_full[2], p_full[2], merge, merged;
+  __shared__ uint32_t s_tmem;
+  __shared__ int64_t s_run[5];
+  __shared__ int s_some, s_gap[kNorms][4];
+  __shared__ float s_vmost[kNorms][4];
+  __shared__ float2 s_ml[kTile];
+  __shared__ volatile int s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (warp == 0) {
+    const bool some = find_run(p, p.many, s_run);
+    if (lane == 0) s_some = some;
+  } else if (warp == 1 && lane == 0) {
+    for (int i = 0; i < SM::kSlots; ++i) {
+      sm100::mbar_init(&full[i], kTile);
+      sm100::mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      sm100::mbar_init(&q_full[i], kTile);
+      sm100::mbar_init(&s_full[i], 1);
+      sm100::mbar_init(&p_full[i], kTile);
+    }
+    sm100::mbar_init(&merge, kTile);
+    sm100::mbar_init(&merged, kTile);
+    s_abort = 0;
+    sm100::fence_barrier_init();
+  }
+  __syncthreads();
+  if (!s_some) return;
+  if (warp == kMmaWarp) {
+    sm100::tmem_alloc(&s_tmem, 512);
+    sm100::tmem_relinquish();
+  }
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  Cursor cur = start_run(p, p.many, s_run);
+  Ring<D, IP> ring{1, 0, 0, 0};
+  // the next segment's tiles in the ring
+  auto enter = [&](const Segment &g) {
+    ring.lead = g.turns ? 2 : 1;
+    ring.tiles = g.tiles;
+  };
+
+  if (warp >= kKeyWarp && warp < kMmaWarp) {
+    const bool keys = warp < kValueWarp;
+    uint32_t tlo[4], thi[4];
+    byte_tables(keys ? p.ck : p.cv, tlo, thi);
+    auto wait_slot = [&](int at) {
+      return at < SM::kSlots ||
+             sm100::mbar_wait_abort(&empty[at % SM::kSlots], (uint32_t)((at / SM::kSlots - 1) & 1), &s_abort, p.err, 121);
+    };
+    auto row_of = [&](const Segment &g, int key) -> int64_t {  // packed row of a key, -1: none
+      if (key >= g.seen) return -1;
+      const int page = __ldg(p.table + (int64_t)cur.seq * p.ldt + key / p.page_size);
+      if (page < 0 || page >= p.npages) return -1;
+      return ((int64_t)page * p.kv_heads + cur.head) * p.page_size + key % p.page_size;
+    };
+    bool ok = true;
+    do {
+      const Segment g = segment_of<D, IP>(p, cur);
+      enter(g);
+      for (int j = 0; j < g.tiles && ok; ++j) {
+        if (keys) {
+          const int r = tid - 32 * kKeyWarp, key = (g.t0 + j) * kTile + r;
+          const int64_t row = row_of(g, key);
+          uint32_t w[WK * D / 32], sw[IP ? D / 32 : 1];
+          float2 kn = make_float2(row < 0 && key < g.seen ? -1.f : 0.f, 0.f);
+          float vn = 0.f;
+          if (row >= 0) {
+            load_words<WK * D / 32>(w, p.kcodes + row * (WK * D / 8));
+            if constexpr (IP) load_words<D / 32>(sw, p.ksigns + row * (D / 8));
+            kn = __ldg(p.knorms + row);
+            vn = __ldg(&p.vnorms[row].x);
+          } else {
+#pragma unroll
+            for (int i = 0; i < WK * D / 32; ++i) w[i] = 0u;
+#pragma unroll
+            for (int i = 0; i < (IP ? D / 32 : 1); ++i) sw[i] = 0u;
+          }
+          const int at = ring.key(j);
+          ok = wait_slot(at);
+          if (!ok) break;
+          uint8_t *slot = smem + SM::kRing + (at % SM::kSlots) * SM::kSlot;
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) expand_group<WK>(slot, r, q, w + q * WK, tlo, thi);
+          const int nr = (ring.before + j) % kNorms;
+          s_kn[nr * kTile + r] = kn.x;
+          s_vn[nr * kTile + r] = vn;
+          const bool gap = __any_sync(0xffffffffu, kn.x < 0.f);
+          float most = vn;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+          if (lane == 0) {
+            s_gap[nr][warp - kKeyWarp] = gap;
+            s_vmost[nr][warp - kKeyWarp] = most;
+          }
+          sm100::fence_proxy_async();
+          sm100::mbar_arrive(&full[at % SM::kSlots]);
+          if constexpr (IP) {
+            ok = wait_slot(at + 1);
+            if (!ok) break;
+            uint8_t *signs = smem + SM::kRing + ((at + 1) % SM::kSlots) * SM::kSlot;
+            const uint32_t h = __half_as_ushort(__float2half_rn(kn.y * (64.f * p.kappa)));
+            const uint32_t minus = (h | h << 16) ^ 0x80008000u;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {  // elements 2 k and 2 k + 1 of a group: bits k and k + 16 of its word
+              uint32_t v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int k = 4 * (c & 3) + e;
+                v[e] = ((sw[c >> 2] << (15 - k)) & 0x80008000u) ^ minus;
+              }
+              *reinterpret_cast<uint4 *>(signs + (c >> 3) * SM::kHalf + sm100::sw128_offset(r, c & 7)) =
+                  make_uint4(v[0], v[1], v[2], v[3]);
+            }
+            sm100::fence_proxy_async();
+            sm100::mbar_arrive(&full[(at + 1) % SM::kSlots]);
+          }
+        } else {
+          // (row, group of 32 coordinates) pairs dealt over the threads
+          constexpr int G = D / 32, N = (kTile * G + kValueThreads - 1) / kValueThreads;
+          const int t = tid - 32 * kValueWarp;
+          uint32_t w[N][WV];
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int u = t + i * kValueThreads;
+#pragma unroll
+            for (int k = 0; k < WV; ++k) w[i][k] = 0u;
+            if (u < kTile * G) {
+              const int64_t row = row_of(g, (g.t0 + j) * kTile + u / G);
+              if (row >= 0) load_words<WV>(w[i], p.vcodes + row * (WV * D / 8) + (u % G) * (4 * WV));
+            }
+          }
+          const int at = ring.value(j);
+          ok = wait_slot(at);
+          if (!ok) break;
+          uint8_t *slot = smem + SM::kRing + (at % SM::kSlots) * SM::kSlot;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int u = t + i * kValueThreads;
+            if (u < kTile * G) expand_group<WV>(slot, u / G, u % G, w[i], tlo, thi);
+          }
+          sm100::fence_proxy_async();
+          sm100::mbar_arrive(&full[at % SM::kSlots]);
+          if (t < kTile - kValueThreads) sm100::mbar_arrive(&full[at % SM::kSlots]);  // 128 arrivals, as for keys
+        }
+      }
+      ring.done();
+    } while (ok && cur.next(p, p.many));
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      const uint32_t iqk = sm100::idesc_f16_f32(kTile, kTile) | (p.scale < 0.f ? 1u << 13 : 0u);  // negate A
+      const uint32_t ipv = sm100::idesc_f16_f32(kTile, D) | (1u << 16);
+      const uint32_t base = sm100::smem_u32(smem);
+      int nq[2] = {0, 0}, np[2] = {0, 0};  // uses of q_full, p_full so far
+      bool ok = true;
+      auto wait_full = [&](int at) {
+        return sm100::mbar_wait_abort(&full[at % SM::kSlots], (uint32_t)((at / SM::kSlots) & 1), &s_abort, p.err, 122);
+      };
+      do {
+        const Segment g = segment_of<D, IP>(p, cur);
+      enter(g);
+        const int cnt[2] = {tiles_of(p, cur, g, 0), tiles_of(p, cur, g, 1)};
+        auto logits = [&](int i, int j) {  // S_i = Q K_j^T
+          const uint32_t q = base + SM::kQ + (g.turns ? 0 : i) * SM::kQTile;
+          const int at = ring.key(j);
+#pragma unroll
+          for (int ks = 0; ks < DQ / 16; ++ks) {
+            if (ks % (D / 16) == 0) {
+              ok = ok && wait_full(at + ks / (D / 16));
+              if (!ok) return;
+            }
+            const int slot = (at + ks / (D / 16)) % SM::kSlots, in = ks % (D / 16);
+            sm100::mma_f16(tmem + kTile * i, sm100::desc_sw128(q + (ks / 4) * SM::kHalf + (ks % 4) * 32),
+                           sm100::desc_sw128(base + SM::kRing + slot * SM::kSlot + (in / 4) * SM::kHalf + (in % 4) * 32),
+                           iqk, ks != 0);
+          }
+          sm100::mma_commit(&s_full[i]);
+        };
+        auto free_keys = [&](int j) {
+          for (int k = 0; k < SM::kWide; ++k) sm100::mma_commit(&empty[(ring.key(j) + k) % SM::kSlots]);
+        };
+        auto output = [&](int i, int j, bool fresh) {  // O_i += P_i V_j
+          ok = ok && sm100::mbar_wait_abort(&p_full[i], (uint32_t)(np[i]++ & 1), &s_abort, p.err, 123);
+          const int at = ring.value(j);
+          ok = ok && wait_full(at);
+          if (!ok) return;
+          sm100::tc_fence_after();
+          const uint32_t v = base + SM::kRing + (at % SM::kSlots) * SM::kSlot;
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks)
+            sm100::mma_f16_ts(tmem + 2 * kTile + kTile * i, tmem + kTile * i + 8 * ks,
+                              sm100::desc_sw128_mn(v + ks * 2048, SM::kHalf, 1024), ipv, !fresh || ks != 0);
+        };
+        auto free_value = [&](int j) { sm100::mma_commit(&empty[(ring.value(j)) % SM::kSlots]); };
+        for (int i = 0; i < (g.turns ? 1 : 2) && ok; ++i)
+          ok = sm100::mbar_wait_abort(&q_full[i], (uint32_t)(nq[i]++ & 1), &s_abort, p.err, 124);
+        sm100::tc_fence_after();
+        if (g.turns) {
+          for (int j = 0; j < 2 && j < g.tiles && ok; ++j) {
+            logits(j, j);
+            if (ok) free_keys(j);
+          }
+          for (int j = 0; j < g.tiles && ok; ++j) {
+            output(j & 1, j, j < 2);
+            if (ok) free_value(j);
+            if (ok && j + 2 < g.tiles) {
+              logits(j & 1, j + 2);
+              if (ok) free_keys(j + 2);
+            } else if (ok) {
+              sm100::mma_commit(&s_full[j & 1]);  // the warpgroup's output is complete
+            }
+          }
+        } else {
+          for (int i = 0; i < 2 && ok; ++i)
+            if (cnt[i]) logits(i, 0);
+          if (ok) free_keys(0);
+          for (int j = 0; j < g.tiles && ok; ++j) {
+            for (int i = 0; i < 2 && ok; ++i) {
+              if (j >= cnt[i]) continue;
+              output(i, j, j == 0);
+              if (ok && j + 1 < cnt[i])
+                logits(i, j + 1);
+              else if (ok)
+                sm100::mma_commit(&s_full[i]);
+            }
+            if (ok) free_value(j);
+            if (ok && j + 1 < g.tiles) free_keys(j + 1);
+          }
+        }
+        ring.done();
+      } while (ok && cur.next(p, p.many));
+    }
+  } else {
+    const int i = warp >> 2, r = tid & (kTile - 1);
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t S = tmem + kTile * i + lanes, O = tmem + 2 * kTile + kTile * i + lanes;
+    const float unit = fabsf(p.scale) * 1.4426950408889634f;
+    int ns = 0, nm = 0;  // uses of s_full, of merge
+    bool ok = true;
+    do {
+      const Segment g = segment_of<D, IP>(p, cur);
+      enter(g);
+      const int cnt = tiles_of(p, cur, g, i);
+      const int first = g.row0 + (g.turns ? 0 : kTile * i), row = first + r;
+      const bool mine = row < g.rows;
+      const int64_t at = (int64_t)(cur.s.start + (mine ? row / p.group : 0)) * p.heads + cur.head * p.group +
+                         (mine ? row % p.group : 0);
+      // 0 would turn a masked logit, -inf, into a NaN
+      const float mult = fminf(fmaxf((mine ? __ldg(p.qscale + at) : 1.f) * unit, 1.17549435e-38f), 3.402823466e38f);
+      if (i == 0 || !g.turns) {
+        uint8_t *q = smem + SM::kQ + i * SM::kQTile;
+        const uint4 *from = reinterpret_cast<const uint4 *>(p.qprep + at * DQ);
+#pragma unroll 8
+        for (int c = 0; c < DQ / 8; ++c)
+          *reinterpret_cast<uint4 *>(q + (c >> 3) * SM::kHalf + sm100::sw128_offset(r, c & 7)) =
+              mine ? __ldg(from + c) : make_uint4(0u, 0u, 0u, 0u);
+        sm100::fence_proxy_async();
+        sm100::mbar_arrive(&q_full[i]);
+      }
+      const int lim = mine ? min(g.hidden + row / p.group, cur.s.len) : cur.s.len;
+      const int lim_first = min(g.hidden + first / p.group, cur.s.len);
+      flash::Row st;
+      for (int n = 0; n < cnt; ++n) {
+        const int j = g.turns ? 2 * n + i : n, nr = (ring.before + j) % kNorms;
+        ok = sm100::mbar_wait_abort(&s_full[i], (uint32_t)(ns++ & 1), &s_abort, p.err, 125);
+        if (!ok) break;
+        sm100::tc_fence_after();
+        const float *kn = s_kn + nr * kTile, *vn = s_vn + nr * kTile;
+        const float most = fmaxf(fmaxf(s_vmost[nr][0], s_vmost[nr][1]), fmaxf(s_vmost[nr][2], s_vmost[nr][3]));
+        const int end = (g.t0 + j + 1) * kTile;
+        if (end > lim_first || (s_gap[nr][0] | s_gap[nr][1] | s_gap[nr][2] | s_gap[nr][3]))
+          flash::softmax_tile<D, false, true, true, 2>(S, O, n == 0, mult, lim - (end - kTile), st, kn, vn, most);
+        else
+          flash::softmax_tile<D, false, false, true, 2>(S, O, n == 0, mult, 0, st, kn, vn, most);
+        sm100::tc_fence_before();
+        sm100::mbar_arrive(&p_full[i]);
+      }
+      if (ok && cnt) ok = sm100::mbar_wait_abort(&s_full[i], (uint32_t)(ns++ & 1), &s_abort, p.err, 126);
+      if (!ok) break;
+      sm100::tc_fence_after();
+      float M = st.sum != 0.f ? st.ref + st.scale : -INFINITY, L = st.sum, f0 = L != 0.f ? 1.f : 0.f, f1 = 0.f;
+      if (g.turns) {
+        if (i == 1) {
+          s_ml[r] = make_float2(M, L);
+          sm100::tc_fence_before();
+          sm100::mbar_arrive(&merge);
+        } else {
+          ok = sm100::mbar_wait_abort(&merge, (uint32_t)(nm & 1), &s_abort, p.err, 127);
+          if (!ok) break;
+          sm100::tc_fence_after();
+          const float2 b = s_ml[r];
+          const float top = fmaxf(M, b.x);
+          if (L != 0.f) f0 = flash::ex2(M - top);
+          if (b.y != 0.f) f1 = flash::ex2(b.x - top);
+          L = f0 * L + f1 * b.y;
+          M = top;
+        }
+      }
+      if (i == 0 || !g.turns) {
+        const bool whole = cur.whole();
+        const int64_t slot = (int64_t)cur.slot() * SM::kRows + (row - g.row0);
+        float *to = whole ? p.whole + at * D : p.many.part_o + slot * D;
+        if (whole) {
+          const float inv = L != 0.f ? 1.0f / L : 0.f;
+          f0 *= inv;
+          f1 *= inv;
+        } else if (mine) {
+          p.many.part_ml[slot] = make_float2(M, L);
+        }
+        const bool other = g.turns && __any_sync(0xffffffffu, f1 != 0.f);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t v[32], b[32];
+          sm100::tmem_ld32(O + c, v);
+          if (other) sm100::tmem_ld32(O + kTile + c, b);
+          sm100::tmem_wait_ld();
+          float *x = reinterpret_cast<float *>(v);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            x[k] = f0 != 0.f ? x[k] * f0 : 0.f;  // (an output that no product wrote may hold anything)
+            if (other && f1 != 0.f) x[k] = fmaf(__uint_as_float(b[k]), f1, x[k]);
+          }
+          if (mine)
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4 *>(to + c + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+        }
+      }
+      if (g.turns) {
+        // the second warpgroup's output is read before its next product
+        sm100::tc_fence_before();
+        if (i == 0)
+          sm100::mbar_arrive(&merged);
+        else
+          ok = sm100::mbar_wait_abort(&merged, (uint32_t)(nm & 1), &s_abort, p.err, 128);
+        ++nm;
+      }
+      ring.done();
+    } while (ok && cur.next(p, p.many));
+  }
+  sm100::tc_fence_before();
+  __syncthreads();
+  if (s_abort) {
+    // a role gave up: products in flight are waited for (bounded) before the
+    // block's memory is released
+    __shared__ uint64_t last;
+    if (warp == kMmaWarp && lane == 0) {
+      sm100::mbar_init(&last, 1);
+      sm100::fence_barrier_init();
+      sm100::mma_commit(&last);
+      sm100::mbar_wait(&last, 0, p.err, 129);
+    }
+    __syncthreads();
+  }
+  if (warp == kMmaWarp) sm100::tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool IP, int WK, int WV>
+tq_status launch_tiles(const PagedParams &prm, cudaStream_t st) {
+  auto kern = k_attend_paged_tiles<D, IP, WK, WV>;
+  constexpr int smem = TileSmem<D, IP>::kBytes;
+  static_assert(smem <= 232448 - 8192, "shared memory");
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return TQ_ERR_CUDA;
+  kern<<<(unsigned)prm.many.grid, kTilesThreads, smem, st>>>(prm);
+  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+template <int D, bool IP, int WK>
+tq_status launch_tiles_wv(const PagedParams &prm, int wv, cudaStream_t st) {
+  switch (wv) {
+    case 2: return launch_tiles<D, IP, WK, 2>(prm, st);
+    case 3: return launch_tiles<D, IP, WK, 3>(prm, st);
+    case 4: return launch_tiles<D, IP, WK, 4>(prm, st);
+  }
+  return TQ_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+template <int D, bool IP>
+tq_status paged_tiles_launch(const PagedParams &prm, int wk, int wv, cudaStream_t st) {
+  switch (wk) {
+    case 1: return launch_tiles_wv<D, IP, 1>(prm, wv, st);
+    case 2: return launch_tiles_wv<D, IP, 2>(prm, wv, st);
+    case 3: return launch_tiles_wv<D, IP, 3>(prm, wv, st);
+    case 4: return launch_tiles_wv<D, IP, 4>(prm, wv, st);
+  }
+  return TQ_ERR_UNSUPPORTED;
+}
+
+}  // namespace tq

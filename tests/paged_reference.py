@@ -24,11 +24,13 @@ def unpack(rows, t):
     return e
 
 
-def attend(y, limits, scale, ke, tk, ve, tv, dtype):
+def attend(y, limits, scale, ke, tk, ve, tv, dtype, many=False):
     """y: rows x d; row i sees the first limits[i] keys.  Returns the exact
     output and, per coordinate, the most that fp16 operands (rotated query and
     its projection, centroids, weights; each rounded once) with fp32 sums and
-    one rounding of the output can be off."""
+    one rounding of the output can be off.  many: of the kernel of many rows,
+    whose residual norms are fp16 operands too, whose projections share the
+    query's scale, and some of whose exponentials are polynomials (2^-18.4)."""
     d, n = tk.d, len(ke["norm"])
     yt, p = o.prepare_query(y, tk)
     x = scale * o.score(yt, p, ke, tk)
@@ -45,16 +47,18 @@ def attend(y, limits, scale, ke, tk, ve, tv, dtype):
         # p itself comes from the query as two fp16 terms and fp32 sums
         perr = (np.abs(yt) @ np.abs(tk.S).T) * (H * H + (d / 16 + 2) * F)
         err += g * (ap.sum(1) * H + perr.sum(1) + 2 * ap.max(1, initial=0.0) * HS * d)[:, None]
+        if many:
+            err += (g * H + HS / 64) * (ap.sum(1) * (1 + H) + perr.sum(1))[:, None] + g * (128 * top * HS * d)
         size = size + g * ap.sum(1)[:, None]
     # fp32: the rotation's 21 adds, the MMA's sums, the scaling
-    err = (err + size * (d / 8 + 24) * F) * scale * ke["norm"][None] + np.abs(x) * 4 * F + 2.0 ** -21
+    err = (err + size * (d / 8 + 24) * F) * abs(scale) * ke["norm"][None] + np.abs(x) * 4 * F + 2.0 ** -21
     see = np.arange(n)[None] < np.asarray(limits)[:, None]
     x = np.where(see, x, -np.inf)
     m = x.max(1, initial=-np.inf, keepdims=True)
     w = np.exp(x - np.where(np.isfinite(m), m, 0.0))
     total = w.sum(1, keepdims=True)
     w = w / np.where(total > 0, total, 1.0)
-    eps = np.where(see, np.expm1(err), 0.0)
+    eps = np.where(see, np.expm1(err) + (2.0 ** -18.4 if many else 0.0), 0.0)
     mean = (w * eps).sum(1, keepdims=True)
     rel = (1 + eps) / np.maximum(1 - mean, 0.1) - 1 + 2 * H + H * H + (n / 16 + 40) * F
     cv = tv.centroids[ve["codes"]]

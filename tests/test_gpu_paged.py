@@ -80,7 +80,7 @@ class Batch:
         self.table_dev = torch.from_numpy(table).cuda()
 
 
-def check(out, batch, y, q_start, news, kv_lens, heads, tk, tv, scale, dtype):
+def check(out, batch, y, q_start, news, kv_lens, heads, tk, tv, scale, dtype, many=False):
     """Compares every row of every sequence; returns the worst share of the bound."""
     group, d, worst = heads // batch.kv_heads, tk.d, 0.0
     for i, (n, kv) in enumerate(zip(news, kv_lens)):
@@ -91,7 +91,7 @@ def check(out, batch, y, q_start, news, kv_lens, heads, tk, tv, scale, dtype):
             cols = slice(h * group * d, (h + 1) * group * d)
             limits = np.repeat(np.clip(kv - n + 1 + np.arange(n), 0, len(batch.rows[0][i][h][2])), group)
             ref, bound = attend(y[rows, cols].reshape(n * group, d), limits, scale, unpack(batch.rows[0][i][h], tk),
-                                tk, unpack(batch.rows[1][i][h], tv), tv, dtype)
+                                tk, unpack(batch.rows[1][i][h], tv), tv, dtype, many)
             got = out[rows, cols].reshape(n * group, d)
             assert np.all(np.isfinite(got)), f"sequence {i}, head {h}"
             ratio = np.abs(got - ref) / bound.clip(1e-30)
@@ -101,7 +101,7 @@ def check(out, batch, y, q_start, news, kv_lens, heads, tk, tv, scale, dtype):
     return worst
 
 
-def run_case(tq, d, kb, ip, vb, kv_heads, group, page, seqs, dtype, seed, gap=2, q_scale=1.0):
+def run_case(tq, d, kb, ip, vb, kv_heads, group, page, seqs, dtype, seed, gap=2, q_scale=1.0, many=False, scale=None):
     """seqs: (new tokens, keys) of each sequence.  `gap` tokens that belong to
     no sequence stand before the first and behind the last."""
     rng = np.random.default_rng(seed)
@@ -114,7 +114,7 @@ def run_case(tq, d, kb, ip, vb, kv_heads, group, page, seqs, dtype, seed, gap=2,
     wide = torch.from_numpy(rng.standard_normal((total, heads * d + 24)).astype(np.float32) * q_scale)
     y = wide.to(DT[dtype]).cuda()[:, 8: 8 + heads * d]  # a view with a leading dimension of its own
     out = torch.full((total, heads * d + 8), -7.0, dtype=DT[dtype], device="cuda")
-    scale = 1.0 / math.sqrt(d)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
     view = out[:, : heads * d]
     got = tq.tq_attend_paged(qk, qv, y, torch.tensor(starts, dtype=torch.int32, device="cuda"), *batch.caches,
                              batch.table_dev, torch.tensor(kv_lens, dtype=torch.int32, device="cuda"),
@@ -123,7 +123,7 @@ def run_case(tq, d, kb, ip, vb, kv_heads, group, page, seqs, dtype, seed, gap=2,
     res = out.float().cpu().numpy().astype(np.float64)
     assert np.all(res[:, heads * d:] == -7.0) and np.all(res[:gap] == -7.0) and np.all(res[starts[-1]:] == -7.0)
     return check(res, batch, y.float().cpu().numpy().astype(np.float64), starts, news, kv_lens, heads, tk, tv, scale,
-                 dtype)
+                 dtype, many)
 
 
 SMALL = [(1, 1), (1, 17), (1, 0), (0, 40), (1, 300), (1, 63), (1, 64), (1, 65)]
