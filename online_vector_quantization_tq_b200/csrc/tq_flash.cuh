@@ -165,7 +165,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t s, uint32_t o, bool first,
   uint32_t buf[2][32];
   float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
   sm100::tmem_ld32(s, buf[0]);
-#pragma unroll
+#pragma unroll 2
   for (int c = 0; c < 4; ++c) {
     sm100::tmem_wait_ld();
     sm100::tmem_ld32(s + 32 * ((c + 1) & 3), buf[(c + 1) & 1]);
@@ -198,9 +198,9 @@ __device__ __forceinline__ void softmax_tile(uint32_t s, uint32_t o, bool first,
   const float base = row.ref == -INFINITY ? 0.f : KN ? -(row.ref + row.scale) : -row.ref;
   const float2 m2 = make_float2(mult, mult), b2 = make_float2(base, base);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
+#pragma unroll 2
   for (int c = 0; c < 4; ++c) {
-    if (c > 0) sm100::tmem_wait_ld();
+    sm100::tmem_wait_ld();
     if (c < 3) sm100::tmem_ld32(s + 32 * (c + 1), buf[(c + 1) & 1]);
     float(&x)[32] = reinterpret_cast<float(&)[32]>(buf[c & 1]);
     columns<MASK, KN>(x, 32 * c, see, kn);

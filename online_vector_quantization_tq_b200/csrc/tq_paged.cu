@@ -145,20 +145,20 @@ __global__ void __launch_bounds__(128) k_paged_queries(const __grid_constant__ P
 
 // ---------------------------------------------------------------- join
 
-// Output rows from the normalized rows of whole blocks, or from the partial
-// results of the runs that share a block (added up in their order), rotated
-// back.  WARPS warps a row take its runs in turn, so that their loads overlap:
-// one where there are rows enough to fill the machine.
-template <int D, int WARPS>
-__global__ void __launch_bounds__(128) k_attend_paged_join(const __grid_constant__ PagedParams p) {
-  constexpr int V = D / 32;
-  __shared__ float s_v[4][D], s_l[4];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WARPS;
-  const int64_t gr = (int64_t)blockIdx.x * (4 / WARPS) + warp / WARPS;
-  const int64_t token = gr / p.heads;
-  const int h = (int)(gr % p.heads), head = h / p.group;
+// Where the result of a token's rows lies: what all heads of it share
+struct Place {
+  bool there;       // the token belongs to a sequence
+  Seq s;
+  const PagedCut *c;
+  int row0;         // the token's first row in its sequence's KV head
+  int64_t units0;   // first unit of KV head 0's block
+  int64_t head_units, per;
+  int units;        // of the block
+};
+// By one warp
+__device__ __forceinline__ Place find_token(const PagedParams &p, int64_t token) {
+  const int lane = threadIdx.x & 31;
   // the last sequence that starts at or before the token
-  bool there = gr < p.total_q * p.heads;
   int lo = 0, hi = p.nseq;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
@@ -167,61 +167,91 @@ __global__ void __launch_bounds__(128) k_attend_paged_join(const __grid_constant
     else
       hi = mid;
   }
-  const Seq s = seq_of(p, lo);
-  there = there && token >= s.start && token < s.start + s.n;
-  float v[V], L = 0.f;
+  Place f{};
+  f.s = seq_of(p, lo);
+  f.there = token >= f.s.start && token < f.s.start + f.s.n;
+  if (!f.there) return f;
+  const PagedCut &c = f.s.n * p.group <= p.few.upto ? p.few : p.many;
+  f.c = &c;
+  f.row0 = (int)(token - f.s.start) * p.group;
+  f.per = run_units(c, __ldg(c.first + p.nseq));
+  for (int k = lane, n = blocks_of(p, c, f.s); k < n; k += 32) f.head_units += units_of(p, c, f.s, k);
 #pragma unroll
-  for (int e = 0; e < V; ++e) v[e] = 0.f;
-  bool alone = true;
-  if (there) {
-    const PagedCut &c = s.n * p.group <= p.few.upto ? p.few : p.many;
-    const int row = (int)(token - s.start) * p.group + h % p.group, block = row / c.rows;
-    const int units = units_of(p, c, s, block);
-    if (units > 0) {
-      int64_t u0 = __ldg(c.first + lo) + head * head_units(p, c, s);
-      for (int k = 0; k < block; ++k) u0 += units_of(p, c, s, k);
-      const int64_t per = run_units(c, __ldg(c.first + p.nseq));
-      const int b0 = (int)(u0 / per), b1 = (int)((u0 + units - 1) / per);
-      if (b0 == b1) {
-        if (part == 0) {
+  for (int o = 16; o > 0; o >>= 1) f.head_units += __shfl_xor_sync(0xffffffffu, f.head_units, o);
+  f.units0 = __ldg(c.first + lo);
+  return f;
+}
+
+// Output rows from the normalized rows of whole blocks, or from the partial
+// results of the runs that share a block (added up in their order), rotated
+// back.  A block of threads takes a token's heads, a warp each; or, where rows
+// are few and shared by many runs, one row with WARPS warps that take its runs
+// in turn, so that their loads overlap.
+template <int D, int WARPS>
+__global__ void __launch_bounds__(128) k_attend_paged_join(const __grid_constant__ PagedParams p) {
+  constexpr int V = D / 32;
+  __shared__ float s_v[4][D], s_l[4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t token = WARPS == 1 ? blockIdx.x : blockIdx.x / p.heads;
+  const Place f = find_token(p, token);
+  if (!f.there) return;
+  const PagedCut &c = *f.c;
+  int block = -1, units = 0;
+  int64_t before = 0;  // units of a KV head's blocks before this one
+  for (int h = WARPS == 1 ? warp : (int)(blockIdx.x % p.heads); h < p.heads; h += WARPS == 1 ? 4 : p.heads) {
+    const int head = h / p.group, row = f.row0 + h % p.group;
+    if (row / c.rows != block) {
+      block = row / c.rows;
+      before = 0;
+      for (int k = lane; k < block; k += 32) before += units_of(p, c, f.s, k);
 #pragma unroll
-          for (int e = 0; e < V; ++e) v[e] = p.whole[gr * D + lane * V + e];
-          L = 1.f;
-        }
-      } else {
-        alone = false;
-        const int in = row % c.rows;
-        auto at = [&](int b) { return ((int64_t)2 * b + (b == b0 ? 1 : 0)) * c.rows + in; };
-        float M = -INFINITY;
-        for (int b = b0 + lane; b <= b1; b += 32) M = fmaxf(M, c.part_ml[at(b)].x);
+      for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+      units = units_of(p, c, f.s, block);
+    }
+    float v[V], L = 0.f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int e = 0; e < V; ++e) v[e] = 0.f;
+    const int64_t u0 = f.units0 + head * f.head_units + before;
+    // (units of a call that fit 32 bits, as nearly all do, need no 64-bit division)
+    const bool narrow = u0 + units < 0x7fffffff && f.per < 0x7fffffff;
+    const int b0 = narrow ? (int)((uint32_t)u0 / (uint32_t)f.per) : (int)(u0 / f.per);
+    const int64_t u1 = u0 + max(units, 1) - 1;
+    const int b1 = narrow ? (int)((uint32_t)u1 / (uint32_t)f.per) : (int)(u1 / f.per);
+    if (units > 0 && b0 == b1) {
+      if (WARPS == 1 || warp == 0) {
+        const float *from = p.whole + (token * p.heads + h) * D + lane * V;
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = from[e];
+        L = 1.f;
+      }
+    } else if (units > 0) {
+      const int in = row % c.rows;
+      auto at = [&](int b) { return ((int64_t)2 * b + (b == b0 ? 1 : 0)) * c.rows + in; };
+      float M = -INFINITY;
+      for (int b = b0 + lane; b <= b1; b += 32) M = fmaxf(M, c.part_ml[at(b)].x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
 #pragma unroll 4
-        for (int b = b0 + part; b <= b1; b += WARPS) {
-          const float2 a = c.part_ml[at(b)];
-          const float *po = c.part_o + at(b) * D + lane * V;
-          float x[V];
+      for (int b = b0 + (WARPS == 1 ? 0 : warp); b <= b1; b += WARPS) {
+        const float2 a = c.part_ml[at(b)];
+        const float *po = c.part_o + at(b) * D + lane * V;
+        float x[V];
 #pragma unroll
-          for (int e = 0; e < V; ++e) x[e] = po[e];
-          if (a.y != 0.f) {  // the row sees some of the run's keys
-            const float f = a.x == -INFINITY ? 0.f : ex2(a.x - M);
-            L = fmaf(f, a.y, L);
+        for (int e = 0; e < V; ++e) x[e] = po[e];
+        if (a.y != 0.f) {  // the row sees some of the run's keys
+          const float g = a.x == -INFINITY ? 0.f : ex2(a.x - M);
+          L = fmaf(g, a.y, L);
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[e] = fmaf(f, x[e], v[e]);
-          }
+          for (int e = 0; e < V; ++e) v[e] = fmaf(g, x[e], v[e]);
         }
       }
     }
-  }
-  if constexpr (WARPS > 1) {
-    if (!alone) {  // (of the whole block: it has one row)
+    if constexpr (WARPS > 1) {
 #pragma unroll
       for (int e = 0; e < V; ++e) s_v[warp][lane * V + e] = v[e];
       if (lane == 0) s_l[warp] = L;
-    }
-    __syncthreads();
-    if (warp > 0) return;
-    if (!alone) {
+      __syncthreads();
+      if (warp > 0) return;
       L = s_l[0] + s_l[1] + s_l[2] + s_l[3];
 #pragma unroll
       for (int e = 0; e < V; ++e) {
@@ -229,13 +259,12 @@ __global__ void __launch_bounds__(128) k_attend_paged_join(const __grid_constant
         v[e] = s_v[0][j] + s_v[1][j] + s_v[2][j] + s_v[3][j];
       }
     }
-  }
-  if (!there) return;
-  const float inv = L != 0.f ? 1.0f / L : 0.f;
+    const float inv = L != 0.f ? 1.0f / L : 0.f;
 #pragma unroll
-  for (int e = 0; e < V; ++e) v[e] *= inv;
-  warp_rotate_back<D>(v, p.vdiag, lane);
-  write_row<D>(p.out, token * p.ldo + (int64_t)h * D, v, lane, p.bf16);
+    for (int e = 0; e < V; ++e) v[e] *= inv;
+    warp_rotate_back<D>(v, p.vdiag, lane);
+    write_row<D>(p.out, token * p.ldo + (int64_t)h * D, v, lane, p.bf16);
+  }
 }
 
 int device_sms() {
@@ -263,8 +292,8 @@ Plan plan_of(const tq_quantizer *qk, int64_t total_q, int64_t nseq, int64_t head
   const int64_t most = std::min(max_new, total_q) * (heads / kv_heads);
   const bool many = most > kFewRows;
   // 8 rows a block where that is all there is: twice the warps on an SM
-  L.few = PagedCut{most <= 8 ? 8 : 16, 64, 0, many ? kFewRows : 0x7fffffff, sms, 4, nullptr, nullptr, nullptr};
-  if (many) L.many = PagedCut{ip && d == 128 ? 128 : 256, 128, kFewRows, 0x7fffffff, sms, 2, nullptr, nullptr, nullptr};
+  L.few = PagedCut{most <= 8 ? 8 : 16, 6, 0, many ? kFewRows : 0x7fffffff, sms, 4, nullptr, nullptr, nullptr};
+  if (many) L.many = PagedCut{ip && d == 128 ? 128 : 256, 7, kFewRows, 0x7fffffff, sms, 2, nullptr, nullptr, nullptr};
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -301,8 +330,8 @@ tq_status launch_paged(const PagedParams &prm, const tq_quantizer *qk, const tq_
   }
   rc = qk->m ? paged_rows_launch<D, true>(prm, qk->w, qv->w, st) : paged_rows_launch<D, false>(prm, qk->w, qv->w, st);
   if (rc != TQ_OK) return rc;
-  if (rows >= 32 * (int64_t)prm.few.grid)
-    k_attend_paged_join<D, 1><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(prm);
+  if (rows >= 16 * (int64_t)prm.few.grid)
+    k_attend_paged_join<D, 1><<<(unsigned)prm.total_q, 128, 0, st>>>(prm);
   else
     k_attend_paged_join<D, 4><<<(unsigned)rows, 128, 0, st>>>(prm);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
@@ -368,6 +397,8 @@ tq_status attend_paged_launch(const tq_quantizer *qk, const tq_quantizer *qv, co
   prm.max_new = (int)a.max_new;
   prm.max_pages = (int)a.max_pages;
   prm.page_size = a.page_size;
+  const uint32_t p16 = (uint32_t)a.page_size / 16;
+  prm.page_magic = (uint32_t)((((uint64_t)1 << 31) + p16 - 1) / p16);
   prm.npages = a.npages;
   prm.kcodes = static_cast<const uint8_t *>(a.kpages.codes);
   prm.ksigns = static_cast<const uint8_t *>(a.kpages.signs);

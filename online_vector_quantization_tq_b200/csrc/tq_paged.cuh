@@ -12,7 +12,7 @@ namespace tq {
 
 // How a batch is cut into work: a sequence's query rows (new token x query
 // head of a group, token-major) in blocks of `rows`, each with the keys that
-// its last row sees in units of `unit` keys.  The units of all (sequence, KV
+// its last row sees in units of 2^unit keys.  The units of all (sequence, KV
 // head, block), in this order, form one line that the kernel's blocks share
 // out in equal contiguous runs, whatever the lengths are; a block of rows
 // whose units fall to several runs is put together at the end from their
@@ -35,6 +35,10 @@ struct PagedParams {
   int64_t ldt;
   int64_t total_q;
   int nseq, heads, kv_heads, group, max_new, max_pages, page_size;
+  // ceil(2^31 / (page_size / 16)): key / page_size = (key / 16) * 2 * page_magic >> 32 for keys below 2^29 (a page
+  // has at most 64 times 16 keys, so the product's excess stays below one)
+  uint32_t page_magic;
+  __device__ int page_of(int key) const { return (int)__umulhi((uint32_t)key >> 4 << 1, page_magic); }
   int64_t npages;
   const uint8_t *kcodes, *ksigns, *vcodes;
   const float2 *knorms, *vnorms;
@@ -178,7 +182,7 @@ __device__ __forceinline__ int seen_by(const PagedParams &p, const PagedCut &c, 
   return max(0, min(s.len, s.kv - s.n + 1 + last / p.group));
 }
 __device__ __forceinline__ int units_of(const PagedParams &p, const PagedCut &c, const Seq &s, int k) {
-  return (seen_by(p, c, s, k) + c.unit - 1) / c.unit;
+  return (seen_by(p, c, s, k) + (1 << c.unit) - 1) >> c.unit;
 }
 __device__ __forceinline__ int64_t head_units(const PagedParams &p, const PagedCut &c, const Seq &s) {
   int64_t u = 0;

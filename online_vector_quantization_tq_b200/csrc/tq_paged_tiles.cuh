@@ -18,8 +18,8 @@
 //
 //   warps 0-3, 4-7   softmax; they also fetch their queries and put out results
 //   warps 8-11       expand keys, one row a thread; norms
-//   warps 12-14      expand values
-//   warp 15          tcgen05
+//   warps 12-15      expand values, one row a thread
+//   warp 16          tcgen05
 //
 // Keys and values share one ring of slots (a tile of 16-bit rows, 128-byte
 // swizzle), in the order in which the products first need them.
@@ -36,9 +36,11 @@ namespace {
 using namespace paged;
 
 constexpr int kTile = 128;
-constexpr int kTilesThreads = 512;
-constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 15;
-constexpr int kValueThreads = 96;
+constexpr int kTilesThreads = 640;  // warps 17-19 only complete the last warpgroup
+// Registers move to the softmax: a warpgroup's share, whose sum is no more
+// than the block was launched with (launch_tiles checks).
+constexpr int kSoftmaxRegs = 128, kExpandRegs = 72, kMmaRegs = 72;
+constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16;
 constexpr int kNorms = 8;  // tiles whose norms are kept: more than the ring holds
 
 template <int D, bool IP>
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
   using SM = TileSmem<D, IP>;
   constexpr int DQ = IP ? 2 * D : D;  // elements of a query operand's row
   extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *smem = smem_raw + ((0u - sm100::smem_u32(smem_raw)) & 1023u);
   float *s_kn = reinterpret_cast<float *>(smem + SM::kKn), *s_vn = reinterpret_cast<float *>(smem + SM::kVn);
   __shared__ uint64_t full[SM::kSlots], empty[SM::kSlots], q_full[2], s_full[2], p_full[2], merge, merged;
   __shared__ uint32_t s_tmem;
@@ -214,57 +216,85 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
   };
 
   if (warp >= kKeyWarp && warp < kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kExpandRegs));
     const bool keys = warp < kValueWarp;
+    const int r = tid & (kTile - 1);
     uint32_t tlo[4], thi[4];
     byte_tables(keys ? p.ck : p.cv, tlo, thi);
     auto wait_slot = [&](int at) {
       return at < SM::kSlots ||
              sm100::mbar_wait_abort(&empty[at % SM::kSlots], (uint32_t)((at / SM::kSlots - 1) & 1), &s_abort, p.err, 121);
     };
-    auto row_of = [&](const Segment &g, int key) -> int64_t {  // packed row of a key, -1: none
-      if (key >= g.seen) return -1;
-      const int page = __ldg(p.table + (int64_t)cur.seq * p.ldt + key / p.page_size);
-      if (page < 0 || page >= p.npages) return -1;
-      return ((int64_t)page * p.kv_heads + cur.head) * p.page_size + key % p.page_size;
-    };
+    constexpr int kBehind = -2;  // a page index: the key lies behind those that are seen
     bool ok = true;
     do {
       const Segment g = segment_of<D, IP>(p, cur);
       enter(g);
-      for (int j = 0; j < g.tiles && ok; ++j) {
-        if (keys) {
-          const int r = tid - 32 * kKeyWarp, key = (g.t0 + j) * kTile + r;
-          const int64_t row = row_of(g, key);
-          uint32_t w[WK * D / 32], sw[IP ? D / 32 : 1];
-          float2 kn = make_float2(row < 0 && key < g.seen ? -1.f : 0.f, 0.f);
-          float vn = 0.f;
-          if (row >= 0) {
-            load_words<WK * D / 32>(w, p.kcodes + row * (WK * D / 8));
-            if constexpr (IP) load_words<D / 32>(sw, p.ksigns + row * (D / 8));
-            kn = __ldg(p.knorms + row);
-            vn = __ldg(&p.vnorms[row].x);
-          } else {
+      const int32_t *table = p.table + (int64_t)cur.seq * p.ldt;
+      const int64_t page_rows = (int64_t)p.kv_heads * p.page_size, head_row = (int64_t)cur.head * p.page_size;
+      // A tile's packed rows are loaded one tile ahead, their page indices two:
+      // the loads' latency passes while the tile before is expanded.
+      auto page_of = [&](int j) {
+        const int key = (g.t0 + j) * kTile + r;
+        if (j >= g.tiles || key >= g.seen) return kBehind;
+        const int page = __ldg(table + p.page_of(key));
+        return page >= 0 && page < p.npages ? page : -1;
+      };
+      auto row_of = [&](int j, int page) {
+        const int key = (g.t0 + j) * kTile + r;
+        return page * page_rows + head_row + (key - p.page_of(key) * p.page_size);
+      };
+      // (each group of 32 coordinates is loaded again as soon as it is used, so
+      // that one row of registers is enough)
+      constexpr int G = D / 32;
+      int page = page_of(1);
+      if (keys) {
+        uint32_t w[G][WK], sw[IP ? G : 1];
+        float2 n = make_float2(0.f, 0.f);
+        float v = 0.f;
+        {
+          const int pg = page_of(0);
+          const int64_t row = pg >= 0 ? row_of(0, pg) : 0;
 #pragma unroll
-            for (int i = 0; i < WK * D / 32; ++i) w[i] = 0u;
+          for (int q = 0; q < G; ++q) {
 #pragma unroll
-            for (int i = 0; i < (IP ? D / 32 : 1); ++i) sw[i] = 0u;
+            for (int i = 0; i < WK; ++i) w[q][i] = 0u;
+            if (pg >= 0) load_words<WK>(w[q], p.kcodes + row * (WK * D / 8) + q * (4 * WK));
           }
+          if constexpr (IP) {
+#pragma unroll
+            for (int q = 0; q < G; ++q) sw[q] = 0u;
+            if (pg >= 0) load_words<G>(sw, p.ksigns + row * (D / 8));
+          }
+          if (pg >= 0) {
+            n = __ldg(p.knorms + row);
+            v = __ldg(&p.vnorms[row].x);
+          } else if (pg == -1) {
+            n.x = -1.f;
+          }
+        }
+        for (int j = 0; j < g.tiles; ++j) {
+          const int pg = page;
+          const int64_t row = pg >= 0 ? row_of(j + 1, pg) : 0;
+          page = page_of(j + 2);
           const int at = ring.key(j);
           ok = wait_slot(at);
           if (!ok) break;
           uint8_t *slot = smem + SM::kRing + (at % SM::kSlots) * SM::kSlot;
 #pragma unroll
-          for (int q = 0; q < D / 32; ++q) expand_group<WK>(slot, r, q, w + q * WK, tlo, thi);
+          for (int q = 0; q < G; ++q) {
+            expand_group<WK>(slot, r, q, w[q], tlo, thi);
+            if (pg >= 0) load_words<WK>(w[q], p.kcodes + row * (WK * D / 8) + q * (4 * WK));
+          }
           const int nr = (ring.before + j) % kNorms;
-          s_kn[nr * kTile + r] = kn.x;
-          s_vn[nr * kTile + r] = vn;
-          const bool gap = __any_sync(0xffffffffu, kn.x < 0.f);
-          float most = vn;
+          s_kn[nr * kTile + r] = n.x;
+          s_vn[nr * kTile + r] = v;
+          const bool gap = __any_sync(0xffffffffu, n.x < 0.f);
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+          for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
           if (lane == 0) {
             s_gap[nr][warp - kKeyWarp] = gap;
-            s_vmost[nr][warp - kKeyWarp] = most;
+            s_vmost[nr][warp - kKeyWarp] = v;
           }
           sm100::fence_proxy_async();
           sm100::mbar_arrive(&full[at % SM::kSlots]);
@@ -272,55 +302,61 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
             ok = wait_slot(at + 1);
             if (!ok) break;
             uint8_t *signs = smem + SM::kRing + ((at + 1) % SM::kSlots) * SM::kSlot;
-            const uint32_t h = __half_as_ushort(__float2half_rn(kn.y * (64.f * p.kappa)));
+            const uint32_t h = __half_as_ushort(__float2half_rn(n.y * (64.f * p.kappa)));
             const uint32_t minus = (h | h << 16) ^ 0x80008000u;
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {  // elements 2 k and 2 k + 1 of a group: bits k and k + 16 of its word
-              uint32_t v[4];
+              uint32_t e[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int k = 4 * (c & 3) + e;
-                v[e] = ((sw[c >> 2] << (15 - k)) & 0x80008000u) ^ minus;
-              }
+              for (int i = 0; i < 4; ++i) e[i] = ((sw[c >> 2] << (15 - (4 * (c & 3) + i))) & 0x80008000u) ^ minus;
               *reinterpret_cast<uint4 *>(signs + (c >> 3) * SM::kHalf + sm100::sw128_offset(r, c & 7)) =
-                  make_uint4(v[0], v[1], v[2], v[3]);
+                  make_uint4(e[0], e[1], e[2], e[3]);
             }
+            if (pg >= 0) load_words<G>(sw, p.ksigns + row * (D / 8));
             sm100::fence_proxy_async();
             sm100::mbar_arrive(&full[(at + 1) % SM::kSlots]);
           }
-        } else {
-          // (row, group of 32 coordinates) pairs dealt over the threads
-          constexpr int G = D / 32, N = (kTile * G + kValueThreads - 1) / kValueThreads;
-          const int t = tid - 32 * kValueWarp;
-          uint32_t w[N][WV];
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int u = t + i * kValueThreads;
-#pragma unroll
-            for (int k = 0; k < WV; ++k) w[i][k] = 0u;
-            if (u < kTile * G) {
-              const int64_t row = row_of(g, (g.t0 + j) * kTile + u / G);
-              if (row >= 0) load_words<WV>(w[i], p.vcodes + row * (WV * D / 8) + (u % G) * (4 * WV));
-            }
+          n = make_float2(pg == -1 ? -1.f : 0.f, 0.f);
+          v = 0.f;
+          if (pg >= 0) {
+            n = __ldg(p.knorms + row);
+            v = __ldg(&p.vnorms[row].x);
           }
+        }
+      } else {
+        uint32_t w[G][WV];
+        {
+          const int pg = page_of(0);
+          const int64_t row = pg >= 0 ? row_of(0, pg) : 0;
+#pragma unroll
+          for (int q = 0; q < G; ++q) {
+#pragma unroll
+            for (int i = 0; i < WV; ++i) w[q][i] = 0u;
+            if (pg >= 0) load_words<WV>(w[q], p.vcodes + row * (WV * D / 8) + q * (4 * WV));
+          }
+        }
+        for (int j = 0; j < g.tiles; ++j) {
+          const int pg = page;
+          const int64_t row = pg >= 0 ? row_of(j + 1, pg) : 0;
+          page = page_of(j + 2);
           const int at = ring.value(j);
           ok = wait_slot(at);
           if (!ok) break;
           uint8_t *slot = smem + SM::kRing + (at % SM::kSlots) * SM::kSlot;
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int u = t + i * kValueThreads;
-            if (u < kTile * G) expand_group<WV>(slot, u / G, u % G, w[i], tlo, thi);
+          for (int q = 0; q < G; ++q) {
+            expand_group<WV>(slot, r, q, w[q], tlo, thi);
+            if (pg >= 0) load_words<WV>(w[q], p.vcodes + row * (WV * D / 8) + q * (4 * WV));
           }
           sm100::fence_proxy_async();
           sm100::mbar_arrive(&full[at % SM::kSlots]);
-          if (t < kTile - kValueThreads) sm100::mbar_arrive(&full[at % SM::kSlots]);  // 128 arrivals, as for keys
         }
       }
       ring.done();
     } while (ok && cur.next(p, p.many));
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) {
+  } else if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+    if (warp == kMmaWarp && lane == 0) {
       const uint32_t iqk = sm100::idesc_f16_f32(kTile, kTile) | (p.scale < 0.f ? 1u << 13 : 0u);  // negate A
       const uint32_t ipv = sm100::idesc_f16_f32(kTile, D) | (1u << 16);
       const uint32_t base = sm100::smem_u32(smem);
@@ -404,6 +440,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
       } while (ok && cur.next(p, p.many));
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int i = warp >> 2, r = tid & (kTile - 1);
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t S = tmem + kTile * i + lanes, O = tmem + 2 * kTile + kTile * i + lanes;
@@ -534,6 +571,11 @@ tq_status launch_tiles(const PagedParams &prm, cudaStream_t st) {
   constexpr int smem = TileSmem<D, IP>::kBytes;
   static_assert(smem <= 232448 - 8192, "shared memory");
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return TQ_ERR_CUDA;
+  // a split beyond what the block holds would wait for ever
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess ||
+      fa.numRegs * kTilesThreads < 128 * (2 * kSoftmaxRegs + 2 * kExpandRegs + kMmaRegs))
+    return TQ_ERR_CUDA;
   kern<<<(unsigned)prm.many.grid, kTilesThreads, smem, st>>>(prm);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }

@@ -162,7 +162,7 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
                 const __grid_constant__ CUtensorMap mv, const __grid_constant__ PromptParams p) {
   using SM = PromptSmem<D>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *smem = smem_raw + ((0u - sm100::smem_u32(smem_raw)) & 1023u);
   __shared__ uint64_t q_full[2], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], t_full[kStages],
       t_ok[kStages], s_full[2], p_full[2];
   __shared__ uint32_t s_tmem;
