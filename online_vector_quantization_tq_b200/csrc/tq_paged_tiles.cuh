@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
     } while (ok && cur.next(p, p.many));
   } else if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
-    if (warp == kMmaWarp && lane == 0) {
+    if (warp == kMmaWarp && sm100::elect_one()) {
       const uint32_t iqk = sm100::idesc_f16_f32(kTile, kTile) | (p.scale < 0.f ? 1u << 13 : 0u);  // negate A
       const uint32_t ipv = sm100::idesc_f16_f32(kTile, D) | (1u << 16);
       const uint32_t base = sm100::smem_u32(smem);
@@ -370,18 +370,19 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
       enter(g);
         const int cnt[2] = {tiles_of(p, cur, g, 0), tiles_of(p, cur, g, 1)};
         auto logits = [&](int i, int j) {  // S_i = Q K_j^T
-          const uint32_t q = base + SM::kQ + (g.turns ? 0 : i) * SM::kQTile;
-          const int at = ring.key(j);
+          // (a step along the operand advances the descriptor's address field, in units of 16 bytes)
+          const uint64_t q = sm100::desc_sw128(base + SM::kQ + (g.turns ? 0 : i) * SM::kQTile);
 #pragma unroll
-          for (int ks = 0; ks < DQ / 16; ++ks) {
-            if (ks % (D / 16) == 0) {
-              ok = ok && wait_full(at + ks / (D / 16));
-              if (!ok) return;
+          for (int w = 0; w < SM::kWide; ++w) {
+            const int at = ring.key(j) + w;
+            ok = ok && wait_full(at);
+            if (!ok) return;
+            const uint64_t k = sm100::desc_sw128(base + SM::kRing + (at % SM::kSlots) * SM::kSlot);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = ((ks / 4) * SM::kHalf + (ks % 4) * 32) / 16;
+              sm100::mma_f16(tmem + kTile * i, q + (w * SM::kSlot / 16 + off), k + off, iqk, (w | ks) != 0);
             }
-            const int slot = (at + ks / (D / 16)) % SM::kSlots, in = ks % (D / 16);
-            sm100::mma_f16(tmem + kTile * i, sm100::desc_sw128(q + (ks / 4) * SM::kHalf + (ks % 4) * 32),
-                           sm100::desc_sw128(base + SM::kRing + slot * SM::kSlot + (in / 4) * SM::kHalf + (in % 4) * 32),
-                           iqk, ks != 0);
           }
           sm100::mma_commit(&s_full[i]);
         };
@@ -394,11 +395,11 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
           ok = ok && wait_full(at);
           if (!ok) return;
           sm100::tc_fence_after();
-          const uint32_t v = base + SM::kRing + (at % SM::kSlots) * SM::kSlot;
+          const uint64_t v = sm100::desc_sw128_mn(base + SM::kRing + (at % SM::kSlots) * SM::kSlot, SM::kHalf, 1024);
 #pragma unroll
           for (int ks = 0; ks < kTile / 16; ++ks)
-            sm100::mma_f16_ts(tmem + 2 * kTile + kTile * i, tmem + kTile * i + 8 * ks,
-                              sm100::desc_sw128_mn(v + ks * 2048, SM::kHalf, 1024), ipv, !fresh || ks != 0);
+            sm100::mma_f16_ts(tmem + 2 * kTile + kTile * i, tmem + kTile * i + 8 * ks, v + ks * (2048 / 16), ipv,
+                              !fresh || ks != 0);
         };
         auto free_value = [&](int j) { sm100::mma_commit(&empty[(ring.value(j)) % SM::kSlots]); };
         for (int i = 0; i < (g.turns ? 1 : 2) && ok; ++i)

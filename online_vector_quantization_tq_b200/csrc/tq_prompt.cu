@@ -258,26 +258,28 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       }
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
+    if (sm100::elect_one()) {
       const uint32_t type = BF16 ? sm100::idesc_bf16_f32(kTile, kTile) : sm100::idesc_f16_f32(kTile, kTile);
       const uint32_t iqk = type | (p.negative ? 1u << 13 : 0u);  // negate A
       const uint32_t ipv = (BF16 ? sm100::idesc_bf16_f32(kTile, D) : sm100::idesc_f16_f32(kTile, D)) | (1u << 16);
       const uint32_t base = sm100::smem_u32(smem);
       auto logits = [&](int i, int j) {
-        const uint32_t q = base + SM::kQ + i * SM::kOne, k = base + SM::kK + (j % kStages) * SM::kOne;
+        // (a step along the operand advances the descriptor's address field, in units of 16 bytes)
+        const uint64_t q = sm100::desc_sw128(base + SM::kQ + i * SM::kOne);
+        const uint64_t k = sm100::desc_sw128(base + SM::kK + (j % kStages) * SM::kOne);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks / 4) * SM::kHalf + (ks % 4) * 32;
-          sm100::mma_f16(tmem + kTile * i, sm100::desc_sw128(q + off), sm100::desc_sw128(k + off), iqk, ks != 0);
+          const uint32_t off = ((ks / 4) * SM::kHalf + (ks % 4) * 32) / 16;
+          sm100::mma_f16(tmem + kTile * i, q + off, k + off, iqk, ks != 0);
         }
         sm100::mma_commit(&s_full[i]);
       };
       auto output = [&](int i, int j) {
-        const uint32_t v = base + SM::kV + (j % kStages) * SM::kOne;
+        const uint64_t v = sm100::desc_sw128_mn(base + SM::kV + (j % kStages) * SM::kOne, SM::kHalf, 1024);
 #pragma unroll
         for (int ks = 0; ks < kTile / 16; ++ks)
-          sm100::mma_f16_ts(tmem + 2 * kTile + kTile * i, tmem + kTile * i + 8 * ks,
-                            sm100::desc_sw128_mn(v + ks * 2048, SM::kHalf, 1024), ipv, (j | ks) != 0);
+          sm100::mma_f16_ts(tmem + 2 * kTile + kTile * i, tmem + kTile * i + 8 * ks, v + ks * (2048 / 16), ipv,
+                            (j | ks) != 0);
       };
       bool ok = sm100::mbar_wait_abort(&k_full[0], 0, &s_abort, p.err, 103);
       for (int i = 0; i < 2 && ok; ++i)

@@ -123,6 +123,19 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// One thread of a warp whose 32 threads are all here.  Inside a branch on it the
+// compiler knows that a single thread runs, and keeps addresses and
+// descriptors in uniform registers (a branch on the lane number does not tell).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // ------------------------------------------------------------------ TMA
 // 2-D tiled load of box {c0 (inner), c1} into shared memory, completing on
 // `bar` (transaction bytes must have been announced with mbar_expect_tx).
