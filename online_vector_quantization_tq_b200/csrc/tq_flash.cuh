@@ -1,5 +1,5 @@
-// The softmax half of attention tiles whose products run on tcgen05: shared
-// by the prompt kernel and the paged kernel for many new tokens.
+// The softmax half of attention tiles whose products run on tcgen05: of the
+// prompt kernel and of the paged kernel for many new tokens.
 //
 // A warpgroup (four warps) owns a tile of 128 query rows, one row per thread.
 // Its logits S (128 x 128 keys, fp32) lie in TMEM; the weights P go back as
@@ -12,6 +12,10 @@
 // 2^kSlack since: weights then stay below 2^kSlack, which both 16-bit types and
 // the fp32 sums hold without loss, and after the first tiles O is hardly ever
 // read back.
+//
+// A tile's chain (logits, softmax, weighted sum, next logits) is what bounds
+// both kernels, so the weights are handed over in two halves: the second
+// product starts on the first 64 keys while the others' weights are computed.
 //
 // 128 x 128 exponentials cost the special-function units as many cycles as
 // the tile's two products cost the tensor cores, so some of them run on the
@@ -122,46 +126,109 @@ __device__ __forceinline__ void scale_rows(uint32_t o, float f) {
   sm100::tmem_wait_st();
 }
 
-// Logits of 32 columns as they come from TMEM, times their keys' factors and
-// masked.
-template <bool MASK, bool KN>
-__device__ __forceinline__ void columns(float (&x)[32], int col, int see, const float *kn) {
-  if constexpr (KN) {
-#pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      const float4 k = *reinterpret_cast<const float4 *>(kn + col + i);
-      const float2 a = mul2(make_float2(x[i], x[i + 1]), make_float2(k.x, k.y));
-      const float2 b = mul2(make_float2(x[i + 2], x[i + 3]), make_float2(k.z, k.w));
-      if constexpr (MASK) {
-        x[i] = k.x < 0.f ? -INFINITY : a.x;
-        x[i + 1] = k.y < 0.f ? -INFINITY : a.y;
-        x[i + 2] = k.z < 0.f ? -INFINITY : b.x;
-        x[i + 3] = k.w < 0.f ? -INFINITY : b.y;
-      } else {
-        x[i] = a.x, x[i + 1] = a.y, x[i + 2] = b.x, x[i + 3] = b.y;
-      }
-    }
+// Moves a row's reference up to `most` (base 2, of this tile) where it has
+// grown by more than the slack, by whole warps; sum and O follow.  first: O is
+// not there yet.  `scale` is what row.scale becomes (no less than it was).
+template <int D>
+__device__ __forceinline__ void move_reference(uint32_t o, bool first, float most, float scale, Row &row) {
+  const bool grow = most > row.ref + kSlack || (row.ref == -INFINITY && most > -INFINITY) || scale > row.scale;
+  if (!__any_sync(0xffffffffu, grow)) return;
+  float up = scale - row.scale;
+  row.scale = scale;
+  if (most > row.ref) {
+    up += most - row.ref;  // infinite for the first visible keys
+    row.ref = most;
   }
-  if constexpr (MASK) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = col + i < see ? x[i] : -INFINITY;
-  }
+  const float f = ex2(-up);
+  row.sum *= f;
+  if (!first) scale_rows<D>(o, f);
 }
 
-// One tile of 128 keys: S at `s` -> P over it; `o` rescaled when the reference
-// moves (first: O is not there yet).  mult >= 0 turns logits into base-2
-// exponents.  MASK: the row sees the tile's first `see` keys alone.  PAIRS of
-// eight pairs of exponentials run on the FMA pipe.
-// KN (the paged cache): logits and weights carry factors of their key, read
-// from shared memory: kn multiplies the logit (below 0: no such key, looked at
-// under MASK), vn the weight behind the sum; vmost is the largest vn.
-// S is read twice, for the maximum and for the weights, 32 columns at a time,
-// each read issued before the columns in hand are worked on: a row of 128
-// logits in registers would leave too few for the rest.  (P's columns reach no
-// further than S's that are read already.)
-template <int D, bool BF16, bool MASK, bool KN, int PAIRS>
+// Weights are in TMEM: the product that reads them may start
+__device__ __forceinline__ void hand_over(uint64_t *bar) {
+  sm100::tmem_wait_st();
+  sm100::tc_fence_before();
+  sm100::mbar_arrive(bar);
+}
+
+// One tile of 128 keys: S at `s` -> P over it, handed over by halves (64 keys
+// each) on two barriers.  mult >= 0 turns logits into base-2 exponents.  MASK:
+// the row sees the tile's first `see` keys alone.  PAIRS of eight pairs of
+// exponentials run on the FMA pipe (prompt of 8192 tokens, d = 128, us: 0 1030,
+// 2 968, 3 992, 4 992).  The row's 128 logits stay in registers: reading S
+// twice, 32 columns at a time, took 1040 us instead of 968.
+template <int D, bool BF16, bool MASK, int PAIRS>
 __device__ __forceinline__ void softmax_tile(uint32_t s, uint32_t o, bool first, float mult, int see, Row &row,
-                                             const float *kn = nullptr, const float *vn = nullptr, float vmost = 0.f) {
+                                             uint64_t *half, uint64_t *full) {
+  float x[128];
+  uint32_t(*v)[32] = reinterpret_cast<uint32_t(*)[32]>(x);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) sm100::tmem_ld32(s + 32 * c, v[c]);
+  sm100::tmem_wait_ld();
+  if constexpr (MASK) {
+#pragma unroll
+    for (int i = 0; i < 128; ++i) x[i] = i < see ? x[i] : -INFINITY;
+  }
+  float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+  for (int i = 4; i < 124; i += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], fmaxf(x[i + k], x[i + 4 + k]));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], x[124 + k]);
+  const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mult;
+  move_reference<D>(o, first, most, row.scale, row);
+  const float base = row.ref == -INFINITY ? 0.f : -row.ref;
+  const float2 m2 = make_float2(mult, mult), b2 = make_float2(base, base);
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const int k = 64 * h + 2 * i;
+      float2 e = fma2(make_float2(x[k], x[k + 1]), m2, b2);
+      if (i % 8 >= 8 - PAIRS)
+        e = ex2_poly2<BF16>(e);
+      else
+        e = make_float2(ex2(e.x), ex2(e.y));
+      sum[i & 1] = add2(sum[i & 1], e);
+      w[i] = pack16<BF16>(e);
+    }
+    sm100::tmem_st32(s + 32 * h, w);
+    hand_over(h == 0 ? half : full);
+  }
+  row.sum += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+}
+
+// The same for keys that bring factors of their own, in shared memory (the
+// norms of the paged cache): kn multiplies the logit (below 0: no such key,
+// looked at under MASK), vn the weight behind the sum; vmost is the largest vn.
+// fp16 weights.  S is read twice, for the maximum and for the weights, 32
+// columns at a time, each read issued before the columns in hand are worked on:
+// the warps that expand operands leave no registers for a row of 128 logits.
+// (P's columns reach no further than S's that are read already.)
+template <bool MASK>
+__device__ __forceinline__ void keyed_columns(float (&x)[32], int col, int see, const float *kn) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const float4 k = *reinterpret_cast<const float4 *>(kn + col + i);
+    const float2 a = mul2(make_float2(x[i], x[i + 1]), make_float2(k.x, k.y));
+    const float2 b = mul2(make_float2(x[i + 2], x[i + 3]), make_float2(k.z, k.w));
+    if constexpr (MASK) {
+      x[i] = k.x < 0.f || col + i >= see ? -INFINITY : a.x;
+      x[i + 1] = k.y < 0.f || col + i + 1 >= see ? -INFINITY : a.y;
+      x[i + 2] = k.z < 0.f || col + i + 2 >= see ? -INFINITY : b.x;
+      x[i + 3] = k.w < 0.f || col + i + 3 >= see ? -INFINITY : b.y;
+    } else {
+      x[i] = a.x, x[i + 1] = a.y, x[i + 2] = b.x, x[i + 3] = b.y;
+    }
+  }
+}
+template <int D, bool MASK, int PAIRS>
+__device__ __forceinline__ void softmax_tile_keyed(uint32_t s, uint32_t o, bool first, float mult, int see, Row &row,
+                                                   const float *kn, const float *vn, float vmost, uint64_t *half,
+                                                   uint64_t *full) {
   uint32_t buf[2][32];
   float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
   sm100::tmem_ld32(s, buf[0]);
@@ -170,32 +237,16 @@ __device__ __forceinline__ void softmax_tile(uint32_t s, uint32_t o, bool first,
     sm100::tmem_wait_ld();
     sm100::tmem_ld32(s + 32 * ((c + 1) & 3), buf[(c + 1) & 1]);
     float(&x)[32] = reinterpret_cast<float(&)[32]>(buf[c & 1]);
-    columns<MASK, KN>(x, 32 * c, see, kn);
+    keyed_columns<MASK>(x, 32 * c, see, kn);
 #pragma unroll
     for (int i = 0; i < 32; i += 8)
 #pragma unroll
       for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], fmaxf(x[i + k], x[i + 4 + k]));
   }
   const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mult;
-  bool grow = most > row.ref + kSlack || (row.ref == -INFINITY && most > -INFINITY);
-  float scale = row.scale;
-  if constexpr (KN) {
-    scale = fmaxf(scale, exponent_above(vmost));
-    grow |= scale > row.scale;
-  }
   sm100::tmem_wait_ld();
-  if (__any_sync(0xffffffffu, grow)) {
-    float up = scale - row.scale;
-    row.scale = scale;
-    if (most > row.ref) {
-      up += most - row.ref;  // infinite for the first visible keys
-      row.ref = most;
-    }
-    const float f = ex2(-up);
-    row.sum *= f;
-    if (!first) scale_rows<D>(o, f);
-  }
-  const float base = row.ref == -INFINITY ? 0.f : KN ? -(row.ref + row.scale) : -row.ref;
+  move_reference<D>(o, first, most, fmaxf(row.scale, exponent_above(vmost)), row);
+  const float base = row.ref == -INFINITY ? 0.f : -(row.ref + row.scale);
   const float2 m2 = make_float2(mult, mult), b2 = make_float2(base, base);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 2
@@ -203,23 +254,22 @@ __device__ __forceinline__ void softmax_tile(uint32_t s, uint32_t o, bool first,
     sm100::tmem_wait_ld();
     if (c < 3) sm100::tmem_ld32(s + 32 * (c + 1), buf[(c + 1) & 1]);
     float(&x)[32] = reinterpret_cast<float(&)[32]>(buf[c & 1]);
-    columns<MASK, KN>(x, 32 * c, see, kn);
+    keyed_columns<MASK>(x, 32 * c, see, kn);
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float2 e = fma2(make_float2(x[2 * i], x[2 * i + 1]), m2, b2);
       if (i % 8 >= 8 - PAIRS)
-        e = ex2_poly2<BF16>(e);
+        e = ex2_poly2<false>(e);
       else
         e = make_float2(ex2(e.x), ex2(e.y));
       sum[i & 1] = add2(sum[i & 1], e);
-      if constexpr (KN) e = mul2(e, *reinterpret_cast<const float2 *>(vn + 32 * c + 2 * i));
-      w[i] = pack16<BF16>(e);
+      w[i] = pack16<false>(mul2(e, *reinterpret_cast<const float2 *>(vn + 32 * c + 2 * i)));
     }
     sm100::tmem_st16(s + 16 * c, w);
+    if (c & 1) hand_over(c == 1 ? half : full);
   }
   row.sum += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-  sm100::tmem_wait_st();
 }
 
 }  // namespace flash

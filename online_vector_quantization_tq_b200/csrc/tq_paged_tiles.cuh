@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((0u - sm100::smem_u32(smem_raw)) & 1023u);
   float *s_kn = reinterpret_cast<float *>(smem + SM::kKn), *s_vn = reinterpret_cast<float *>(smem + SM::kVn);
-  __shared__ uint64_t full[SM::kSlots], empty[SM::kSlots], q_full[2], s_full[2], p_full[2], merge, merged;
+  __shared__ uint64_t full[SM::kSlots], empty[SM::kSlots], q_full[2], s_full[2], p_half[2], p_full[2], merge, merged;
   __shared__ uint32_t s_tmem;
   __shared__ int64_t s_run[5];
   __shared__ int s_some, s_gap[kNorms][4];
@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
     for (int i = 0; i < 2; ++i) {
       sm100::mbar_init(&q_full[i], kTile);
       sm100::mbar_init(&s_full[i], 1);
+      sm100::mbar_init(&p_half[i], kTile);
       sm100::mbar_init(&p_full[i], kTile);
     }
     sm100::mbar_init(&merge, kTile);
@@ -360,10 +361,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
       const uint32_t iqk = sm100::idesc_f16_f32(kTile, kTile) | (p.scale < 0.f ? 1u << 13 : 0u);  // negate A
       const uint32_t ipv = sm100::idesc_f16_f32(kTile, D) | (1u << 16);
       const uint32_t base = sm100::smem_u32(smem);
-      int nq[2] = {0, 0}, np[2] = {0, 0};  // uses of q_full, p_full so far
+      int nq[2] = {0, 0}, np[2] = {0, 0};  // uses of q_full, of p_half and p_full so far
       bool ok = true;
       auto wait_full = [&](int at) {
-        return sm100::mbar_wait_abort(&full[at % SM::kSlots], (uint32_t)((at / SM::kSlots) & 1), &s_abort, p.err, 122);
+        return sm100::mbar_poll_abort(&full[at % SM::kSlots], (uint32_t)((at / SM::kSlots) & 1), &s_abort, p.err, 122);
       };
       do {
         const Segment g = segment_of<D, IP>(p, cur);
@@ -390,20 +391,26 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
           for (int k = 0; k < SM::kWide; ++k) sm100::mma_commit(&empty[(ring.key(j) + k) % SM::kSlots]);
         };
         auto output = [&](int i, int j, bool fresh) {  // O_i += P_i V_j
-          ok = ok && sm100::mbar_wait_abort(&p_full[i], (uint32_t)(np[i]++ & 1), &s_abort, p.err, 123);
+          ok = ok && sm100::mbar_poll_abort(&p_half[i], (uint32_t)(np[i] & 1), &s_abort, p.err, 123);
           const int at = ring.value(j);
           ok = ok && wait_full(at);
           if (!ok) return;
           sm100::tc_fence_after();
           const uint64_t v = sm100::desc_sw128_mn(base + SM::kRing + (at % SM::kSlots) * SM::kSlot, SM::kHalf, 1024);
 #pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
+          for (int ks = 0; ks < kTile / 16; ++ks) {
+            if (ks == kTile / 32) {  // the weights' second half
+              ok = sm100::mbar_poll_abort(&p_full[i], (uint32_t)(np[i]++ & 1), &s_abort, p.err, 130);
+              if (!ok) return;
+              sm100::tc_fence_after();
+            }
             sm100::mma_f16_ts(tmem + 2 * kTile + kTile * i, tmem + kTile * i + 8 * ks, v + ks * (2048 / 16), ipv,
                               !fresh || ks != 0);
+          }
         };
         auto free_value = [&](int j) { sm100::mma_commit(&empty[(ring.value(j)) % SM::kSlots]); };
         for (int i = 0; i < (g.turns ? 1 : 2) && ok; ++i)
-          ok = sm100::mbar_wait_abort(&q_full[i], (uint32_t)(nq[i]++ & 1), &s_abort, p.err, 124);
+          ok = sm100::mbar_poll_abort(&q_full[i], (uint32_t)(nq[i]++ & 1), &s_abort, p.err, 124);
         sm100::tc_fence_after();
         if (g.turns) {
           for (int j = 0; j < 2 && j < g.tiles && ok; ++j) {
@@ -473,20 +480,19 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
       flash::Row st;
       for (int n = 0; n < cnt; ++n) {
         const int j = g.turns ? 2 * n + i : n, nr = (ring.before + j) % kNorms;
-        ok = sm100::mbar_wait_abort(&s_full[i], (uint32_t)(ns++ & 1), &s_abort, p.err, 125);
+        ok = sm100::mbar_poll_abort(&s_full[i], (uint32_t)(ns++ & 1), &s_abort, p.err, 125);
         if (!ok) break;
         sm100::tc_fence_after();
         const float *kn = s_kn + nr * kTile, *vn = s_vn + nr * kTile;
         const float most = fmaxf(fmaxf(s_vmost[nr][0], s_vmost[nr][1]), fmaxf(s_vmost[nr][2], s_vmost[nr][3]));
         const int end = (g.t0 + j + 1) * kTile;
         if (end > lim_first || (s_gap[nr][0] | s_gap[nr][1] | s_gap[nr][2] | s_gap[nr][3]))
-          flash::softmax_tile<D, false, true, true, 2>(S, O, n == 0, mult, lim - (end - kTile), st, kn, vn, most);
+          flash::softmax_tile_keyed<D, true, 2>(S, O, n == 0, mult, lim - (end - kTile), st, kn, vn, most, &p_half[i],
+                                                &p_full[i]);
         else
-          flash::softmax_tile<D, false, false, true, 2>(S, O, n == 0, mult, 0, st, kn, vn, most);
-        sm100::tc_fence_before();
-        sm100::mbar_arrive(&p_full[i]);
+          flash::softmax_tile_keyed<D, false, 2>(S, O, n == 0, mult, 0, st, kn, vn, most, &p_half[i], &p_full[i]);
       }
-      if (ok && cnt) ok = sm100::mbar_wait_abort(&s_full[i], (uint32_t)(ns++ & 1), &s_abort, p.err, 126);
+      if (ok && cnt) ok = sm100::mbar_poll_abort(&s_full[i], (uint32_t)(ns++ & 1), &s_abort, p.err, 126);
       if (!ok) break;
       sm100::tc_fence_after();
       float M = st.sum != 0.f ? st.ref + st.scale : -INFINITY, L = st.sum, f0 = L != 0.f ? 1.f : 0.f, f1 = 0.f;
@@ -496,7 +502,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
           sm100::tc_fence_before();
           sm100::mbar_arrive(&merge);
         } else {
-          ok = sm100::mbar_wait_abort(&merge, (uint32_t)(nm & 1), &s_abort, p.err, 127);
+          ok = sm100::mbar_poll_abort(&merge, (uint32_t)(nm & 1), &s_abort, p.err, 127);
           if (!ok) break;
           sm100::tc_fence_after();
           const float2 b = s_ml[r];
@@ -543,7 +549,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
         if (i == 0)
           sm100::mbar_arrive(&merged);
         else
-          ok = sm100::mbar_wait_abort(&merged, (uint32_t)(nm & 1), &s_abort, p.err, 128);
+          ok = sm100::mbar_poll_abort(&merged, (uint32_t)(nm & 1), &s_abort, p.err, 128);
         ++nm;
       }
       ring.done();

@@ -37,6 +37,9 @@ namespace {
 constexpr int kTile = 128;  // query rows of a tile, keys of a tile
 constexpr int kStages = 2;  // key tiles and value tiles in flight
 constexpr int kPromptThreads = 384;
+// Registers move to the softmax: a warpgroup's share, whose sum is no more
+// than the block was launched with (launch_prompt checks).
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kGuardWarp = 10;
 
 struct PromptParams {
@@ -164,7 +167,7 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((0u - sm100::smem_u32(smem_raw)) & 1023u);
   __shared__ uint64_t q_full[2], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], t_full[kStages],
-      t_ok[kStages], s_full[2], p_full[2];
+      t_ok[kStages], s_full[2], p_full[2], p_half[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_item[5], s_bad;
   __shared__ volatile int s_abort;
@@ -185,6 +188,7 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       sm100::mbar_init(&q_full[i], 1);
       sm100::mbar_init(&s_full[i], 1);
       sm100::mbar_init(&p_full[i], kTile);
+      sm100::mbar_init(&p_half[i], kTile);
     }
     for (int i = 0; i < kStages; ++i) {
       sm100::mbar_init(&k_full[i], 1);
@@ -220,6 +224,8 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
   const int tiles = max(cnt[0], cnt[1]);
   const int tail = (t0 + 1) / kTile;  // tiles from here on hold keys that some row does not see
 
+  if (warp >= kLoadWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == kLoadWarp) {
     if (lane == 0) {
       const uint32_t qbytes = (uint32_t)p.group * p.tokens * 128 * (D / 64);
@@ -263,6 +269,7 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       const uint32_t iqk = type | (p.negative ? 1u << 13 : 0u);  // negate A
       const uint32_t ipv = (BF16 ? sm100::idesc_bf16_f32(kTile, D) : sm100::idesc_f16_f32(kTile, D)) | (1u << 16);
       const uint32_t base = sm100::smem_u32(smem);
+      bool ok = true;
       auto logits = [&](int i, int j) {
         // (a step along the operand advances the descriptor's address field, in units of 16 bytes)
         const uint64_t q = sm100::desc_sw128(base + SM::kQ + i * SM::kOne);
@@ -277,14 +284,20 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       auto output = [&](int i, int j) {
         const uint64_t v = sm100::desc_sw128_mn(base + SM::kV + (j % kStages) * SM::kOne, SM::kHalf, 1024);
 #pragma unroll
-        for (int ks = 0; ks < kTile / 16; ++ks)
+        for (int ks = 0; ks < kTile / 16; ++ks) {
+          if (ks == kTile / 32) {
+            ok = sm100::mbar_poll_abort(&p_full[i], (uint32_t)(j & 1), &s_abort, p.err, 117);
+            if (!ok) return;
+            sm100::tc_fence_after();
+          }
           sm100::mma_f16_ts(tmem + 2 * kTile + kTile * i, tmem + kTile * i + 8 * ks, v + ks * (2048 / 16), ipv,
                             (j | ks) != 0);
+        }
       };
-      bool ok = sm100::mbar_wait_abort(&k_full[0], 0, &s_abort, p.err, 103);
+      ok = sm100::mbar_poll_abort(&k_full[0], 0, &s_abort, p.err, 103);
       for (int i = 0; i < 2 && ok; ++i)
         if (cnt[i]) {
-          ok = sm100::mbar_wait_abort(&q_full[i], 0, &s_abort, p.err, 104);
+          ok = sm100::mbar_poll_abort(&q_full[i], 0, &s_abort, p.err, 104);
           if (ok) logits(i, 0);
         }
       if (ok) sm100::mma_commit(&k_empty[0]);
@@ -293,18 +306,19 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
         bool have_v = false, have_k = false;
         for (int i = 0; i < 2 && ok; ++i) {
           if (j >= cnt[i]) continue;
-          ok = sm100::mbar_wait_abort(&p_full[i], (uint32_t)(j & 1), &s_abort, p.err, 105);
+          ok = sm100::mbar_poll_abort(&p_half[i], (uint32_t)(j & 1), &s_abort, p.err, 105);
           if (ok && !have_v) {
-            ok = j < tail ? sm100::mbar_wait_abort(&v_full[st], (uint32_t)((j / kStages) & 1), &s_abort, p.err, 106)
-                          : sm100::mbar_wait_abort(&t_ok[(j - tail) % kStages], (uint32_t)(((j - tail) / kStages) & 1),
+            ok = j < tail ? sm100::mbar_poll_abort(&v_full[st], (uint32_t)((j / kStages) & 1), &s_abort, p.err, 106)
+                          : sm100::mbar_poll_abort(&t_ok[(j - tail) % kStages], (uint32_t)(((j - tail) / kStages) & 1),
                                                    &s_abort, p.err, 107);
             have_v = true;
           }
           if (!ok) break;
           sm100::tc_fence_after();
           output(i, j);
+          if (!ok) break;
           if (j + 1 < cnt[i]) {
-            if (!have_k) ok = sm100::mbar_wait_abort(&k_full[nx], (uint32_t)(((j + 1) / kStages) & 1), &s_abort, p.err, 108);
+            if (!have_k) ok = sm100::mbar_poll_abort(&k_full[nx], (uint32_t)(((j + 1) / kStages) & 1), &s_abort, p.err, 108);
             have_k = true;
             if (ok) logits(i, j + 1);
           } else {
@@ -325,7 +339,10 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       guard_values<D, BF16>(smem + SM::kV + st * SM::kOne, j * kTile, t0, n, &s_bad);
       sm100::mbar_arrive(&t_ok[u % kStages]);
     }
-  } else if (cnt[warp >> 2]) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    if (cnt[warp >> 2]) {
     const int i = warp >> 2, r = tid & (kTile - 1);
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s = tmem + kTile * i + lanes, o = tmem + 2 * kTile + kTile * i + lanes;
@@ -333,17 +350,15 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
     flash::Row row;
     bool ok = true;
     for (int j = 0; j < cnt[i]; ++j) {
-      ok = sm100::mbar_wait_abort(&s_full[i], (uint32_t)(j & 1), &s_abort, p.err, 110);
+      ok = sm100::mbar_poll_abort(&s_full[i], (uint32_t)(j & 1), &s_abort, p.err, 110);
       if (!ok) break;
       sm100::tc_fence_after();
       if ((j + 1) * kTile > first + 1)
-        flash::softmax_tile<D, BF16, true, false, 2>(s, o, j == 0, p.mult, token + 1 - j * kTile, row);
+        flash::softmax_tile<D, BF16, true, 2>(s, o, j == 0, p.mult, token + 1 - j * kTile, row, &p_half[i], &p_full[i]);
       else
-        flash::softmax_tile<D, BF16, false, false, 2>(s, o, j == 0, p.mult, 0, row);
-      sm100::tc_fence_before();
-      sm100::mbar_arrive(&p_full[i]);
+        flash::softmax_tile<D, BF16, false, 2>(s, o, j == 0, p.mult, 0, row, &p_half[i], &p_full[i]);
     }
-    if (ok) ok = sm100::mbar_wait_abort(&s_full[i], (uint32_t)(cnt[i] & 1), &s_abort, p.err, 111);
+    if (ok) ok = sm100::mbar_poll_abort(&s_full[i], (uint32_t)(cnt[i] & 1), &s_abort, p.err, 111);
     if (ok) {
       sm100::tc_fence_after();
       const float inv = 1.0f / row.sum;
@@ -380,6 +395,7 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
                          flash::pack16<BF16>(f[4 * k + 2]), flash::pack16<BF16>(f[4 * k + 3]));
       }
     }
+  }
   }
   sm100::tc_fence_before();
   __syncthreads();
@@ -440,6 +456,11 @@ tq_status launch_prompt(const PromptArgs &a, int *err, cudaStream_t st) {
   auto kern = k_attend_prompt<D, BF16>;
   constexpr int smem = PromptSmem<D>::kBytes;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return TQ_ERR_CUDA;
+  // a split beyond what the block holds would wait for ever
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess ||
+      fa.numRegs * kPromptThreads < 128 * (2 * kSoftmaxRegs + kOtherRegs))
+    return TQ_ERR_CUDA;
   kern<<<(unsigned)blocks, kPromptThreads, smem, st>>>(mq, mk, mv, p);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }

@@ -96,6 +96,25 @@ __device__ __forceinline__ bool mbar_wait_abort(uint64_t *bar, uint32_t parity, 
   return false;
 }
 
+// The same for a role on the critical path (issuing products, softmax): it
+// polls instead of sleeping, since a thread that sleeps on a barrier wakes
+// several hundred cycles late.
+__device__ __forceinline__ bool mbar_poll_abort(uint64_t *bar, uint32_t parity, volatile int *abort, int *err,
+                                                int code) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (global_ns() - t0 > kWaitLimitNs) break;
+  }
+  atomicCAS(err, 0, code);
+  *abort = 1;
+  return false;
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
