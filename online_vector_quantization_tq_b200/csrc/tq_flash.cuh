@@ -97,16 +97,14 @@ __device__ __forceinline__ uint32_t pack16(float2 v) {
   return r;
 }
 
-// One row's running softmax state, in base 2: the exponent's reference and
-// the sum of the weights.  Where keys bring factors of their own (the value
-// norms of the paged cache), scale is the power of two above those seen, and
-// weights and sum are relative to ref + scale.
+// One row's running softmax state, in base 2: the exponent's reference, the
+// sum of the weights, and the exponent by which the values of O are scaled down
+// (the paged cache's, whose norms may be of any size).
 struct Row {
   float ref = -INFINITY, sum = 0.f, scale = -100.f;
 };
 
-// Exponent of the power of two above v (v >= 0), kept where neither it nor
-// the weights under it leave fp32
+// Exponent of the power of two above v (v >= 0), within what fp32 factors hold
 __device__ __forceinline__ float exponent_above(float v) {
   return fminf(fmaxf((float)((int)(__float_as_uint(v) >> 23) - 126), -100.f), 100.f);
 }
@@ -133,15 +131,14 @@ template <int D>
 __device__ __forceinline__ void move_reference(uint32_t o, bool first, float most, float scale, Row &row) {
   const bool grow = most > row.ref + kSlack || (row.ref == -INFINITY && most > -INFINITY) || scale > row.scale;
   if (!__any_sync(0xffffffffu, grow)) return;
-  float up = scale - row.scale;
-  row.scale = scale;
+  float up = 0.f;
   if (most > row.ref) {
-    up += most - row.ref;  // infinite for the first visible keys
+    up = most - row.ref;  // infinite for the first visible keys
     row.ref = most;
   }
-  const float f = ex2(-up);
-  row.sum *= f;
-  if (!first) scale_rows<D>(o, f);
+  row.sum *= ex2(-up);
+  if (!first) scale_rows<D>(o, ex2(row.scale - scale - up));
+  row.scale = scale;
 }
 
 // Weights are in TMEM: the product that reads them may start
@@ -201,34 +198,29 @@ __device__ __forceinline__ void softmax_tile(uint32_t s, uint32_t o, bool first,
   row.sum += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
-// The same for keys that bring factors of their own, in shared memory (the
-// norms of the paged cache): kn multiplies the logit (below 0: no such key,
-// looked at under MASK), vn the weight behind the sum; vmost is the largest vn.
-// fp16 weights.  S is read twice, for the maximum and for the weights, 32
-// columns at a time, each read issued before the columns in hand are worked on:
-// the warps that expand operands leave no registers for a row of 128 logits.
-// (P's columns reach no further than S's that are read already.)
+// The same with fp16 weights for the paged cache, whose values come scaled down
+// by 2^scale.  S is read twice, for the maximum and for the weights, 32 columns
+// at a time, each read issued before the columns in hand are worked on: the
+// warps that expand operands leave no registers for a row of 128 logits.  (P's
+// columns reach no further than S's that are read already.)  none: one value a
+// key in shared memory, below 0 where there is no such key; looked at under
+// MASK.
 template <bool MASK>
-__device__ __forceinline__ void keyed_columns(float (&x)[32], int col, int see, const float *kn) {
+__device__ __forceinline__ void hide(float (&x)[32], int col, int see, const float *none) {
+  if constexpr (MASK) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
-    const float4 k = *reinterpret_cast<const float4 *>(kn + col + i);
-    const float2 a = mul2(make_float2(x[i], x[i + 1]), make_float2(k.x, k.y));
-    const float2 b = mul2(make_float2(x[i + 2], x[i + 3]), make_float2(k.z, k.w));
-    if constexpr (MASK) {
-      x[i] = k.x < 0.f || col + i >= see ? -INFINITY : a.x;
-      x[i + 1] = k.y < 0.f || col + i + 1 >= see ? -INFINITY : a.y;
-      x[i + 2] = k.z < 0.f || col + i + 2 >= see ? -INFINITY : b.x;
-      x[i + 3] = k.w < 0.f || col + i + 3 >= see ? -INFINITY : b.y;
-    } else {
-      x[i] = a.x, x[i + 1] = a.y, x[i + 2] = b.x, x[i + 3] = b.y;
+    for (int i = 0; i < 32; i += 4) {
+      const float4 k = *reinterpret_cast<const float4 *>(none + col + i);
+      x[i] = k.x < 0.f || col + i >= see ? -INFINITY : x[i];
+      x[i + 1] = k.y < 0.f || col + i + 1 >= see ? -INFINITY : x[i + 1];
+      x[i + 2] = k.z < 0.f || col + i + 2 >= see ? -INFINITY : x[i + 2];
+      x[i + 3] = k.w < 0.f || col + i + 3 >= see ? -INFINITY : x[i + 3];
     }
   }
 }
 template <int D, bool MASK, int PAIRS>
-__device__ __forceinline__ void softmax_tile_keyed(uint32_t s, uint32_t o, bool first, float mult, int see, Row &row,
-                                                   const float *kn, const float *vn, float vmost, uint64_t *half,
-                                                   uint64_t *full) {
+__device__ __forceinline__ void softmax_tile_twice(uint32_t s, uint32_t o, bool first, float mult, int see, Row &row,
+                                                   const float *none, float scale, uint64_t *half, uint64_t *full) {
   uint32_t buf[2][32];
   float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
   sm100::tmem_ld32(s, buf[0]);
@@ -237,7 +229,7 @@ __device__ __forceinline__ void softmax_tile_keyed(uint32_t s, uint32_t o, bool 
     sm100::tmem_wait_ld();
     sm100::tmem_ld32(s + 32 * ((c + 1) & 3), buf[(c + 1) & 1]);
     float(&x)[32] = reinterpret_cast<float(&)[32]>(buf[c & 1]);
-    keyed_columns<MASK>(x, 32 * c, see, kn);
+    hide<MASK>(x, 32 * c, see, none);
 #pragma unroll
     for (int i = 0; i < 32; i += 8)
 #pragma unroll
@@ -245,8 +237,8 @@ __device__ __forceinline__ void softmax_tile_keyed(uint32_t s, uint32_t o, bool 
   }
   const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mult;
   sm100::tmem_wait_ld();
-  move_reference<D>(o, first, most, fmaxf(row.scale, exponent_above(vmost)), row);
-  const float base = row.ref == -INFINITY ? 0.f : -(row.ref + row.scale);
+  move_reference<D>(o, first, most, fmaxf(row.scale, scale), row);
+  const float base = row.ref == -INFINITY ? 0.f : -row.ref;
   const float2 m2 = make_float2(mult, mult), b2 = make_float2(base, base);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 2
@@ -254,7 +246,7 @@ __device__ __forceinline__ void softmax_tile_keyed(uint32_t s, uint32_t o, bool 
     sm100::tmem_wait_ld();
     if (c < 3) sm100::tmem_ld32(s + 32 * (c + 1), buf[(c + 1) & 1]);
     float(&x)[32] = reinterpret_cast<float(&)[32]>(buf[c & 1]);
-    keyed_columns<MASK>(x, 32 * c, see, kn);
+    hide<MASK>(x, 32 * c, see, none);
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -264,7 +256,7 @@ __device__ __forceinline__ void softmax_tile_keyed(uint32_t s, uint32_t o, bool 
       else
         e = make_float2(ex2(e.x), ex2(e.y));
       sum[i & 1] = add2(sum[i & 1], e);
-      w[i] = pack16<false>(mul2(e, *reinterpret_cast<const float2 *>(vn + 32 * c + 2 * i)));
+      w[i] = pack16<false>(e);
     }
     sm100::tmem_st16(s + 16 * c, w);
     if (c & 1) hand_over(c == 1 ? half : full);

@@ -410,6 +410,8 @@ tq_status attend_paged_launch(const tq_quantizer *qk, const tq_quantizer *qv, co
   for (int i = 0; i < 16; ++i) {
     prm.ck[i] = i < (1 << qk->w) ? double_to_half_bits(qk->centroids[i]) : 0;
     prm.cv[i] = i < (1 << qv->w) ? double_to_half_bits(qv->centroids[i]) : 0;
+    prm.ckf[i] = i < (1 << qk->w) ? (float)qk->centroids[i] : 0.f;
+    prm.cvf[i] = i < (1 << qv->w) ? (float)qv->centroids[i] : 0.f;
   }
   prm.kdiag = qk->kt.diag_bits;
   prm.vdiag = qv->kt.diag_bits;

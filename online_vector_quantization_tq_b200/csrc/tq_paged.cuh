@@ -45,6 +45,7 @@ struct PagedParams {
   int bf16;  // queries and output: bf16, else fp16
   float scale;
   uint16_t ck[16], cv[16];  // fp16 centroids
+  float ckf[16], cvf[16];   // the same in fp32
   const uint32_t *kdiag, *vdiag;
   const uint16_t *qjl;  // d x d fp16 (inner-product keys)
   float kappa;

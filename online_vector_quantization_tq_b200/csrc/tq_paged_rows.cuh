@@ -409,8 +409,13 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float2 kn = *reinterpret_cast<const float2 *>(st + ST::kNormK + (8 * i + kpos) * 8);
+          float2 kn = *reinterpret_cast<const float2 *>(st + ST::kNormK + (8 * i + kpos) * 8);
           vn[i] = *reinterpret_cast<const float *>(st + ST::kNormV + (8 * i + kpos) * 8);
+          // a value that is not finite makes a NaN of every row that sees its key, and of no other
+          if (!(vn[i] < INFINITY)) {
+            kn.x = NAN;
+            vn[i] = 0.f;
+          }
 #pragma unroll
           for (int q = 0; q < NQ; ++q)
 #pragma unroll

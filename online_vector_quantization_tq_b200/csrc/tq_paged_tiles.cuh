@@ -4,9 +4,15 @@
 //
 // As the prompt kernel (tq_flash.cuh has the softmax), with key and value tiles
 // that are expanded from the packed pages instead of copied: both products run
-// on tcgen05 with fp16 operands, and the norms multiply logits and weights as
-// fp32 factors of their column.  Inner-product keys are operands of twice the
-// width, [c | +-64 gamma sqrt(pi/2)/d], against queries [R y | S R y / 64].
+// on tcgen05 with fp16 operands.  A row's operand is its centroids times its
+// norm, scaled down by a power of two that is above all norms of the tile (keys)
+// or of the tiles so far (values) and that the softmax takes back.  Each thread
+// makes a table of its row's 2^w possible values, so that every element is
+// rounded once, and the softmax meets no factors per key.  (As fp32 factors of
+// logits and weights the norms made the softmax the bound: 316 us instead of
+// 287 on 512 new tokens over 16384 keys.)  Inner-product keys are operands of
+// twice the width, [c | +-64 gamma sqrt(pi/2)/d] times the norm, against queries
+// [R y | S R y / 64].
 //
 // One block per SM works off its run of units (PagedCut; a unit is a tile of
 // 128 keys).  Two warpgroups of softmax share the tensor cores:
@@ -41,7 +47,7 @@ constexpr int kTilesThreads = 640;  // warps 17-19 only complete the last warpgr
 // than the block was launched with (launch_tiles checks).
 constexpr int kSoftmaxRegs = 128, kExpandRegs = 72, kMmaRegs = 72;
 constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16;
-constexpr int kNorms = 8;  // tiles whose norms are kept: more than the ring holds
+constexpr int kNorms = 8;  // tiles whose scales are kept: more than the ring holds
 
 template <int D, bool IP>
 struct TileSmem {
@@ -52,8 +58,8 @@ struct TileSmem {
   static constexpr int kQTiles = IP && D == 128 ? 1 : 2;
   static constexpr int kRows = kTile * kQTiles;          // rows of a block
   static constexpr int kQ = 0, kQTile = kSlot * kWide, kRing = kQTiles * kQTile;
-  static constexpr int kKn = kRing + kSlots * kSlot, kVn = kKn + kNorms * kTile * 4;
-  static constexpr int kBytes = kVn + kNorms * kTile * 4 + 1024;
+  static constexpr int kNone = kRing + kSlots * kSlot;  // below 0 for a key on a bad page
+  static constexpr int kBytes = kNone + kNorms * kTile * 4 + 1024;
 };
 
 // Ring positions of key and value tiles: `lead` key tiles first (one where both
@@ -150,18 +156,24 @@ __device__ __forceinline__ void load_words(uint32_t *w, const uint8_t *from) {
   }
 }
 
-// byte tables of the fp16 centroids
-__device__ __forceinline__ void byte_tables(const uint16_t *c, uint32_t (&lo)[4], uint32_t (&hi)[4]) {
+// Byte tables of a row's values: centroids times f, rounded to fp16
+template <int W>
+__device__ __forceinline__ void byte_tables(const float *c, float f, uint32_t (&lo)[4], uint32_t (&hi)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     lo[i] = hi[i] = 0u;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      lo[i] |= (uint32_t)(c[4 * i + k] & 0xFF) << (8 * k);
-      hi[i] |= (uint32_t)(c[4 * i + k] >> 8) << (8 * k);
+    if (4 * i < (1 << W)) {
+      const float2 ff = make_float2(f, f);
+      const uint32_t a = flash::pack16<false>(flash::mul2(make_float2(c[4 * i], c[4 * i + 1]), ff));
+      const uint32_t b = flash::pack16<false>(flash::mul2(make_float2(c[4 * i + 2], c[4 * i + 3]), ff));
+      lo[i] = sm100::prmt(a, b, 0x6420u);
+      hi[i] = sm100::prmt(a, b, 0x7531u);
     }
   }
 }
+
+// A norm's part in its tile's largest: what is not finite has none
+__device__ __forceinline__ float finite_or_0(float v) { return fabsf(v) < INFINITY ? v : 0.f; }
 
 template <int D, bool IP, int WK, int WV>
 __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const __grid_constant__ PagedParams p) {
@@ -169,13 +181,15 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
   constexpr int DQ = IP ? 2 * D : D;  // elements of a query operand's row
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((0u - sm100::smem_u32(smem_raw)) & 1023u);
-  float *s_kn = reinterpret_cast<float *>(smem + SM::kKn), *s_vn = reinterpret_cast<float *>(smem + SM::kVn);
+  float *s_none = reinterpret_cast<float *>(smem + SM::kNone);
   __shared__ uint64_t full[SM::kSlots], empty[SM::kSlots], q_full[2], s_full[2], p_half[2], p_full[2], merge, merged;
   __shared__ uint32_t s_tmem;
   __shared__ int64_t s_run[5];
   __shared__ int s_some, s_gap[kNorms][4];
-  __shared__ float s_vmost[kNorms][4];
+  __shared__ float s_key[kNorms], s_value[kNorms];  // 2^e of a tile's keys, exponent of its values
+  __shared__ float s_top[3][2][4];                  // keys' and values' largest norms, of each warp
   __shared__ float2 s_ml[kTile];
+  __shared__ float s_back;
   __shared__ volatile int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -221,11 +235,23 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
     const bool keys = warp < kValueWarp;
     const int r = tid & (kTile - 1);
     uint32_t tlo[4], thi[4];
-    byte_tables(keys ? p.ck : p.cv, tlo, thi);
     auto wait_slot = [&](int at) {
       return at < SM::kSlots ||
              sm100::mbar_wait_abort(&empty[at % SM::kSlots], (uint32_t)((at / SM::kSlots - 1) & 1), &s_abort, p.err, 121);
     };
+    // Largest of a norm over the warpgroup's threads, put down before `agree`
+    // and read behind it, alternately in two places.  agree: whether any of the
+    // threads gave up (they have to leave together).
+    auto put_top = [&](int what, int turn, float v) {
+      v = finite_or_0(v);  // not below 0: ordered as an integer
+      const int top = __reduce_max_sync(0xffffffffu, __float_as_int(v));
+      if (lane == 0) s_top[what][turn & 1][warp & 3] = __int_as_float(top);
+    };
+    auto top_of = [&](int what, int turn) {
+      const float *t = s_top[what][turn & 1];
+      return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+    };
+    auto agree = [&](bool mine) { return !sm100::named_barrier_or(keys ? 1 : 2, kTile, !mine); };
     constexpr int kBehind = -2;  // a page index: the key lies behind those that are seen
     bool ok = true;
     do {
@@ -274,36 +300,42 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
             n.x = -1.f;
           }
         }
+        float exponent = -100.f;
         for (int j = 0; j < g.tiles; ++j) {
           const int pg = page;
           const int64_t row = pg >= 0 ? row_of(j + 1, pg) : 0;
           page = page_of(j + 2);
-          const int at = ring.key(j);
-          ok = wait_slot(at);
+          const int at = ring.key(j), nr = (ring.before + j) % kNorms;
+          const bool gap = __any_sync(0xffffffffu, n.x < 0.f);
+          const float none = n.x < 0.f ? -1.f : 0.f;
+          put_top(0, j, fmaxf(n.x, 0.f));
+          put_top(1, j, v);
+          ok = agree(wait_slot(at));
           if (!ok) break;
+          const float e = flash::exponent_above(top_of(0, j));
+          exponent = fmaxf(exponent, flash::exponent_above(top_of(1, j)));
+          // a value that is not finite makes a NaN of every row that sees its key, and of no other
+          const float f = fabsf(v) < INFINITY ? fmaxf(n.x, 0.f) * flash::ex2(-e) + 0.f * n.x : NAN;
+          byte_tables<WK>(p.ckf, f, tlo, thi);
           uint8_t *slot = smem + SM::kRing + (at % SM::kSlots) * SM::kSlot;
 #pragma unroll
           for (int q = 0; q < G; ++q) {
             expand_group<WK>(slot, r, q, w[q], tlo, thi);
             if (pg >= 0) load_words<WK>(w[q], p.kcodes + row * (WK * D / 8) + q * (4 * WK));
           }
-          const int nr = (ring.before + j) % kNorms;
-          s_kn[nr * kTile + r] = n.x;
-          s_vn[nr * kTile + r] = v;
-          const bool gap = __any_sync(0xffffffffu, n.x < 0.f);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-          if (lane == 0) {
-            s_gap[nr][warp - kKeyWarp] = gap;
-            s_vmost[nr][warp - kKeyWarp] = v;
+          s_none[nr * kTile + r] = none;
+          if (lane == 0) s_gap[nr][warp - kKeyWarp] = gap;
+          if (r == 0) {
+            s_key[nr] = flash::ex2(e);
+            s_value[nr] = exponent;
           }
           sm100::fence_proxy_async();
           sm100::mbar_arrive(&full[at % SM::kSlots]);
           if constexpr (IP) {
-            ok = wait_slot(at + 1);
+            ok = agree(wait_slot(at + 1));
             if (!ok) break;
             uint8_t *signs = smem + SM::kRing + ((at + 1) % SM::kSlots) * SM::kSlot;
-            const uint32_t h = __half_as_ushort(__float2half_rn(n.y * (64.f * p.kappa)));
+            const uint32_t h = __half_as_ushort(__float2half_rn(f * n.y * (64.f * p.kappa)));
             const uint32_t minus = (h | h << 16) ^ 0x80008000u;
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {  // elements 2 k and 2 k + 1 of a group: bits k and k + 16 of its word
@@ -326,6 +358,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
         }
       } else {
         uint32_t w[G][WV];
+        float v = 0.f, exponent = -100.f;
         {
           const int pg = page_of(0);
           const int64_t row = pg >= 0 ? row_of(0, pg) : 0;
@@ -335,20 +368,26 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
             for (int i = 0; i < WV; ++i) w[q][i] = 0u;
             if (pg >= 0) load_words<WV>(w[q], p.vcodes + row * (WV * D / 8) + q * (4 * WV));
           }
+          if (pg >= 0) v = __ldg(&p.vnorms[row].x);
         }
         for (int j = 0; j < g.tiles; ++j) {
           const int pg = page;
           const int64_t row = pg >= 0 ? row_of(j + 1, pg) : 0;
           page = page_of(j + 2);
           const int at = ring.value(j);
-          ok = wait_slot(at);
+          put_top(2, j, v);
+          ok = agree(wait_slot(at));
           if (!ok) break;
+          exponent = fmaxf(exponent, flash::exponent_above(top_of(2, j)));  // (as the keys' threads find it)
+          byte_tables<WV>(p.cvf, finite_or_0(v) * flash::ex2(-exponent), tlo, thi);
           uint8_t *slot = smem + SM::kRing + (at % SM::kSlots) * SM::kSlot;
 #pragma unroll
           for (int q = 0; q < G; ++q) {
             expand_group<WV>(slot, r, q, w[q], tlo, thi);
             if (pg >= 0) load_words<WV>(w[q], p.vcodes + row * (WV * D / 8) + q * (4 * WV));
           }
+          v = 0.f;
+          if (pg >= 0) v = __ldg(&p.vnorms[row].x);
           sm100::fence_proxy_async();
           sm100::mbar_arrive(&full[at % SM::kSlots]);
         }
@@ -463,8 +502,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
       const bool mine = row < g.rows;
       const int64_t at = (int64_t)(cur.s.start + (mine ? row / p.group : 0)) * p.heads + cur.head * p.group +
                          (mine ? row % p.group : 0);
-      // 0 would turn a masked logit, -inf, into a NaN
-      const float mult = fminf(fmaxf((mine ? __ldg(p.qscale + at) : 1.f) * unit, 1.17549435e-38f), 3.402823466e38f);
+      const float mult = (mine ? __ldg(p.qscale + at) : 1.f) * unit;
       if (i == 0 || !g.turns) {
         uint8_t *q = smem + SM::kQ + i * SM::kQTile;
         const uint4 *from = reinterpret_cast<const uint4 *>(p.qprep + at * DQ);
@@ -483,22 +521,26 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
         ok = sm100::mbar_poll_abort(&s_full[i], (uint32_t)(ns++ & 1), &s_abort, p.err, 125);
         if (!ok) break;
         sm100::tc_fence_after();
-        const float *kn = s_kn + nr * kTile, *vn = s_vn + nr * kTile;
-        const float most = fmaxf(fmaxf(s_vmost[nr][0], s_vmost[nr][1]), fmaxf(s_vmost[nr][2], s_vmost[nr][3]));
+        const float *none = s_none + nr * kTile;
+        // (a factor of 0 would turn a masked logit, -inf, into a NaN)
+        const float m = fminf(fmaxf(mult * s_key[nr], 1.17549435e-38f), 3.402823466e38f), scale = s_value[nr];
         const int end = (g.t0 + j + 1) * kTile;
         if (end > lim_first || (s_gap[nr][0] | s_gap[nr][1] | s_gap[nr][2] | s_gap[nr][3]))
-          flash::softmax_tile_keyed<D, true, 2>(S, O, n == 0, mult, lim - (end - kTile), st, kn, vn, most, &p_half[i],
+          flash::softmax_tile_twice<D, true, 2>(S, O, n == 0, m, lim - (end - kTile), st, none, scale, &p_half[i],
                                                 &p_full[i]);
         else
-          flash::softmax_tile_keyed<D, false, 2>(S, O, n == 0, mult, 0, st, kn, vn, most, &p_half[i], &p_full[i]);
+          flash::softmax_tile_twice<D, false, 2>(S, O, n == 0, m, 0, st, none, scale, &p_half[i], &p_full[i]);
       }
       if (ok && cnt) ok = sm100::mbar_poll_abort(&s_full[i], (uint32_t)(ns++ & 1), &s_abort, p.err, 126);
       if (!ok) break;
       sm100::tc_fence_after();
-      float M = st.sum != 0.f ? st.ref + st.scale : -INFINITY, L = st.sum, f0 = L != 0.f ? 1.f : 0.f, f1 = 0.f;
+      float M = st.sum != 0.f ? st.ref : -INFINITY, L = st.sum, f0 = 0.f, f1 = 0.f;
+      const float back = flash::ex2(st.scale);  // the values' scale
+      if (L != 0.f) f0 = back;
       if (g.turns) {
         if (i == 1) {
           s_ml[r] = make_float2(M, L);
+          if (r == 0) s_back = back;
           sm100::tc_fence_before();
           sm100::mbar_arrive(&merge);
         } else {
@@ -507,9 +549,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
           sm100::tc_fence_after();
           const float2 b = s_ml[r];
           const float top = fmaxf(M, b.x);
-          if (L != 0.f) f0 = flash::ex2(M - top);
-          if (b.y != 0.f) f1 = flash::ex2(b.x - top);
-          L = f0 * L + f1 * b.y;
+          const float a0 = L != 0.f ? flash::ex2(M - top) : 0.f, a1 = b.y != 0.f ? flash::ex2(b.x - top) : 0.f;
+          f0 = a0 * back;
+          f1 = a1 * s_back;
+          L = a0 * L + a1 * b.y;
           M = top;
         }
       }

@@ -29,8 +29,10 @@ def attend(y, limits, scale, ke, tk, ve, tv, dtype, many=False):
     output and, per coordinate, the most that fp16 operands (rotated query and
     its projection, centroids, weights; each rounded once) with fp32 sums and
     one rounding of the output can be off.  many: of the kernel of many rows,
-    whose residual norms are fp16 operands too, whose projections share the
-    query's scale, and some of whose exponentials are polynomials (2^-18.4)."""
+    whose keys' and values' operands are centroids times norms, absolute below
+    2^-14 of the largest norm (at most twice that), whose residual norms are
+    fp16 operands too, whose projections share the query's scale, and some of
+    whose exponentials are polynomials (2^-18.4)."""
     d, n = tk.d, len(ke["norm"])
     yt, p = o.prepare_query(y, tk)
     x = scale * o.score(yt, p, ke, tk)
@@ -50,6 +52,9 @@ def attend(y, limits, scale, ke, tk, ve, tv, dtype, many=False):
         if many:
             err += (g * H + HS / 64) * (ap.sum(1) * (1 + H) + perr.sum(1))[:, None] + g * (128 * top * HS * d)
         size = size + g * ap.sum(1)[:, None]
+    if many:
+        kmost = 2 * ke["norm"].max(initial=0.0) / np.maximum(ke["norm"], 1e-30)[None]
+        err += kmost * HS * (np.abs(yt).sum(1) + (ap.sum(1) / 64 if tk.m else 0.0))[:, None]
     # fp32: the rotation's 21 adds, the MMA's sums, the scaling
     err = (err + size * (d / 8 + 24) * F) * abs(scale) * ke["norm"][None] + np.abs(x) * 4 * F + 2.0 ** -21
     see = np.arange(n)[None] < np.asarray(limits)[:, None]
@@ -68,6 +73,8 @@ def attend(y, limits, scale, ke, tk, ve, tv, dtype, many=False):
     # a weight below 2^-14 of the scale is rounded absolutely; the largest weight is 1 before division by the sum
     small = np.where(see, vtop * HS, 0.0) / np.maximum(total, 1.0)
     e = (w * vn * rel + small) @ np.abs(cv)
+    if many:
+        e += vtop * HS
     bound = e @ np.abs(tv.R)
     r, a = OUT[dtype]
     return out, bound + (np.abs(out) + bound) * r + a

@@ -173,3 +173,31 @@ def test_a_prompt_in_chunks(tq):  # noqa: F811
                             1 / math.sqrt(d), ke, tk, ve, tv, "bf16", True)
         for out in (got, once):
             assert np.all(np.abs(out[:, cols].double().cpu().numpy().reshape(n * group, d) - ref) <= bound)
+
+
+@pytest.mark.parametrize("n,group", [(3, 4), (3, 5), (40, 4), (200, 2)])
+@pytest.mark.parametrize("what", ["key", "value", "value inf"])
+def test_what_a_token_does_not_see(tq, n, group, what):  # noqa: F811
+    """A norm that is not finite, of a token's key or value, makes NaN of the
+    tokens that see it; the tokens before it keep their results, bit for bit."""
+    rng = np.random.default_rng(n)
+    (qk, _), (qv, _) = quantizer(tq, 128, 4, n != 40), quantizer(tq, 128, 4, False, seed=1)
+    kv = n + 150
+    batch = Batch(tq, qk, qv, 1, 16, [kv, 60], rng)
+    y = torch.randn(n + 1, group * 128, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    start = torch.tensor([0, n, n + 1], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([kv, 60], dtype=torch.int32, device="cuda")
+
+    def call():
+        return tq.tq_attend_paged(qk, qv, y, start, *batch.caches, batch.table_dev, lens, n, 0.1)
+    clean = call()
+    for t in (0, 1, n // 2, n - 1):
+        at = kv - n + t
+        norms = batch.caches[what != "key"].norms[batch.table[0, at // 16], 0, at % 16]
+        keep = norms.clone()
+        norms[0] = math.inf if what == "value inf" else math.nan
+        out = call()
+        norms.copy_(keep)
+        assert torch.equal(out[:t], clean[:t]) and torch.equal(out[n:], clean[n:])
+        assert bool(torch.isnan(out[t:n]).all())
+    assert torch.equal(call(), clean)
