@@ -70,201 +70,350 @@ __global__ void __launch_bounds__(256) k_paged_store(const StoreParams p) {
 // kernel of many rows: row (token * heads + head) is R y / U, and for
 // inner-product keys S R y / (64 U) behind it, U a power of two above the row's
 // largest coordinate, which goes to qscale.  Coordinates stand where the
-// expansion of packed codes and signs puts them.  16 rows a block.
+// expansion of packed codes and signs puts them.  One thread a row, 64 rows a
+// block; the projection on the tensor cores, with y~ as two fp16 terms.
+// (16384 rows of d = 128: 6 us, by a warp a row 11 us; 37000 rows with the
+// projection: see the table of rates in the kernel of many rows.)
+constexpr int kQueryRows = 64;
+
 template <int D, bool IP>
-__global__ void __launch_bounds__(128) k_paged_queries(const __grid_constant__ PagedParams p, int w) {
-  constexpr int V = D / 32, DQ = IP ? 2 * D : D;
-  __shared__ __align__(16) uint16_t yh[IP ? 16 * D : 1], yl[IP ? 16 * D : 1];
-  __shared__ __align__(16) uint16_t stage[16 * DQ];
+__global__ void __launch_bounds__(kQueryRows) k_paged_queries(const __grid_constant__ PagedParams p, int w) {
+  constexpr int DQ = IP ? 2 * D : D, LD = D + 8;  // padded rows: fragments of 8 rows fall into different banks
+  __shared__ __align__(16) uint16_t yh[kQueryRows * LD], yl[IP ? kQueryRows * LD : 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t row0 = (int64_t)blockIdx.x * 16, total = p.total_q * p.heads;
-  float v[4][V];
+  const int64_t row0 = (int64_t)blockIdx.x * kQueryRows, total = p.total_q * p.heads, row = row0 + tid;
+  {
+    float v[D];
+    const int64_t at = row < total ? row / p.heads * p.ldy + row % p.heads * D : -1;
+    const uint16_t *from = static_cast<const uint16_t *>(p.y) + at;
+    if (at >= 0 && (p.ldy % 8 | (reinterpret_cast<uintptr_t>(p.y) & 15)) == 0) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t row = row0 + 4 * warp + i;
-    const bool there = row < total;
-    const int64_t at = there ? row / p.heads * p.ldy + row % p.heads * D + lane * V : 0;
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(from) + c);
+        const uint32_t words[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[i][e] = there ? load16(p.y, at + e, p.bf16) : 0.f;
-  }
+        for (int e = 0; e < 8; ++e) v[8 * c + e] = widen16((uint16_t)(words[e / 2] >> (16 * (e & 1))), p.bf16);
+      }
+    } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) warp_rotate<D>(v[i], p.kdiag, lane);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * warp + i;
+      for (int e = 0; e < D; ++e) v[e] = at >= 0 ? widen16(from[e], p.bf16) : 0.f;
+    }
+    thread_rotate<D>(v, p.kdiag);
     float top = 0.f;
 #pragma unroll
-    for (int e = 0; e < V; ++e) top = fmaxf(top, fabsf(v[i][e]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int e = 0; e < D; ++e) top = fmaxf(top, fabsf(v[e]));
     const float up = pow2_above(top), down = 1.0f / up;
-    if (lane == 0 && row0 + r < total) p.qscale[row0 + r] = up;
+    if (at >= 0) p.qscale[row] = up;
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const int j = lane * V + e;
-      const float x = v[i][e] * down;
-      const __half hi = __float2half_rn(x);
-      stage[r * DQ + (w == 1 ? j / 32 * 32 + 8 * (j % 4) + j % 32 / 4 : j)] = __half_as_ushort(hi);
+    for (int e = 0; e < D; e += 2) {
+      const float2 x = make_float2(v[e] * down, v[e + 1] * down);
+      const __half2 hi = __floats2half2_rn(x.x, x.y);
+      *reinterpret_cast<__half2 *>(yh + tid * LD + e) = hi;
       if constexpr (IP) {
-        yh[r * D + j] = __half_as_ushort(hi);
-        yl[r * D + j] = __half_as_ushort(__float2half_rn(x - __half2float(hi)));
+        const float2 h = __half22float2(hi);
+        *reinterpret_cast<__half2 *>(yl + tid * LD + e) = __floats2half2_rn(x.x - h.x, x.y - h.y);
       }
     }
   }
   __syncthreads();
+  float acc[IP ? 2 : 1][IP ? D / 8 : 1][4];  // projections of the warp's 32 rows
   if constexpr (IP) {
-    // p = S y~ with y~ as two fp16 terms; warp w has the 8-column tiles w, w + 4, ..
     const int r = lane >> 2, c = lane & 3;
 #pragma unroll
-    for (int t = warp; t < D / 8; t += 4) {
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      const uint32_t *srow = reinterpret_cast<const uint32_t *>(p.qjl + (t * 8 + r) * D);
+    for (int t = 0; t < D / 8; ++t) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t b0 = __ldg(srow + 8 * k + c), b1 = __ldg(srow + 8 * k + c + 4);
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[m][t][e] = 0.f;
+    }
+#pragma unroll 1
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t a[2][2][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int term = 0; term < 2; ++term) {
-          const uint32_t *ya = reinterpret_cast<const uint32_t *>((term ? yl : yh) + r * D + 16 * k) + c;
-          const uint32_t a[4] = {ya[0], ya[8 * (D / 2)], ya[4], ya[8 * (D / 2) + 4]};
-          mma16816(acc, a, b0, b1);
+          const uint32_t *ya =
+              reinterpret_cast<const uint32_t *>((term ? yl : yh) + (32 * warp + 16 * m + r) * LD + 16 * k) + c;
+          a[m][term][0] = ya[0], a[m][term][1] = ya[8 * (LD / 2)], a[m][term][2] = ya[4], a[m][term][3] = ya[8 * (LD / 2) + 4];
         }
-      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = t * 8 + 2 * c + (e & 1), b = j % 32;  // bits k and k + 16 of a word are neighbours
-        stage[(r + 8 * (e >> 1)) * DQ + D + j / 32 * 32 + (b < 16 ? 2 * b : 2 * (b - 16) + 1)] =
-            __half_as_ushort(__float2half_rn(acc[e] * (1.0f / 64.0f)));
+      for (int t = 0; t < D / 8; ++t) {
+        const uint32_t *srow = reinterpret_cast<const uint32_t *>(p.qjl + (t * 8 + r) * D) + 8 * k + c;
+        const uint32_t b0 = __ldg(srow), b1 = __ldg(srow + 4);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int term = 0; term < 2; ++term) mma16816(acc[m][t], a[m][term], b0, b1);
       }
     }
+    __syncthreads();  // the low terms are read: the projections take their place
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int t = 0; t < D / 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = t * 8 + 2 * c + (e & 1), b = j % 32;  // bits k and k + 16 of a word are neighbours
+          yl[(32 * warp + 16 * m + r + 8 * (e >> 1)) * LD + j / 32 * 32 + (b < 16 ? 2 * b : 2 * (b - 16) + 1)] =
+              __half_as_ushort(__float2half_rn(acc[m][t][e] * (1.0f / 64.0f)));
+        }
     __syncthreads();
   }
-  const int64_t n = min((int64_t)16, total - row0) * (DQ / 8);
+  // 16-byte pieces, neighbours by neighbouring threads
+  const int rows = (int)min((int64_t)kQueryRows, total - row0);
   uint4 *to = reinterpret_cast<uint4 *>(p.qprep + row0 * DQ);
-  for (int i = tid; i < n; i += 128) to[i] = reinterpret_cast<const uint4 *>(stage)[i];
+  for (int i = tid; i < rows * (DQ / 8); i += kQueryRows) {
+    const int r = i / (DQ / 8), c = i % (DQ / 8);
+    uint4 x;
+    if (IP && c >= D / 8) {
+      x = *reinterpret_cast<const uint4 *>(yl + r * LD + (c - D / 8) * 8);
+    } else if (w != 1) {
+      x = *reinterpret_cast<const uint4 *>(yh + r * LD + c * 8);
+    } else {  // one-bit codes: byte 8 (j % 4) + j / 4 of a group is coordinate j
+      uint32_t q[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int b = (8 * c + 2 * e) % 32;  // coordinates of positions b and b + 1
+        const uint16_t *g = yh + r * LD + 8 * c / 32 * 32;
+        q[e] = g[4 * (b % 8) + b / 8] | (uint32_t)g[4 * (b % 8 + 1) + b / 8] << 16;
+      }
+      x = make_uint4(q[0], q[1], q[2], q[3]);
+    }
+    to[i] = x;
+  }
 }
 
 // ---------------------------------------------------------------- join
 
-// Where the result of a token's rows lies: what all heads of it share
+// Where the result of a block of rows lies: runs b0 to b1 have part of it (one
+// run: its normalized rows are in p.whole)
 struct Place {
-  bool there;       // the token belongs to a sequence
-  Seq s;
-  const PagedCut *c;
-  int row0;         // the token's first row in its sequence's KV head
-  int64_t units0;   // first unit of KV head 0's block
-  int64_t head_units, per;
-  int units;        // of the block
+  int b0, b1;
+  bool seen;  // the block has keys
+  __device__ int64_t at(const PagedCut &c, int b) const { return ((int64_t)2 * b + (b == b0 ? 1 : 0)) * c.rows; }
 };
-// By one warp
-__device__ __forceinline__ Place find_token(const PagedParams &p, int64_t token) {
-  const int lane = threadIdx.x & 31;
-  // the last sequence that starts at or before the token
-  int lo = 0, hi = p.nseq;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (__ldg(p.q_start + mid) <= token)
-      lo = mid;
-    else
-      hi = mid;
-  }
+__device__ __forceinline__ Place place_of(const PagedParams &p, const PagedCut &c, const Seq &s, int seq, int head,
+                                          int block) {
   Place f{};
-  f.s = seq_of(p, lo);
-  f.there = token >= f.s.start && token < f.s.start + f.s.n;
-  if (!f.there) return f;
-  const PagedCut &c = f.s.n * p.group <= p.few.upto ? p.few : p.many;
-  f.c = &c;
-  f.row0 = (int)(token - f.s.start) * p.group;
-  f.per = run_units(c, __ldg(c.first + p.nseq));
-  for (int k = lane, n = blocks_of(p, c, f.s); k < n; k += 32) f.head_units += units_of(p, c, f.s, k);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) f.head_units += __shfl_xor_sync(0xffffffffu, f.head_units, o);
-  f.units0 = __ldg(c.first + lo);
+  int64_t before = 0, all = 0;
+  for (int k = 0, n = blocks_of(p, c, s); k < n; ++k) {
+    const int u = units_of(p, c, s, k);
+    all += u;
+    if (k < block) before += u;
+  }
+  const int units = units_of(p, c, s, block);
+  f.seen = units > 0;
+  if (!f.seen) return f;
+  const int64_t u0 = __ldg(c.first + seq) + head * all + before, u1 = u0 + units - 1;
+  const int64_t per = run_units(c, __ldg(c.first + p.nseq));
+  if (u1 < 0x7fffffff) {  // (as in nearly all calls: no 64-bit division)
+    const uint32_t d = (uint32_t)min(per, (int64_t)0x7fffffff);
+    f.b0 = (int)((uint32_t)u0 / d);
+    f.b1 = (int)((uint32_t)u1 / d);
+  } else {
+    f.b0 = (int)(u0 / per);
+    f.b1 = (int)(u1 / per);
+  }
   return f;
 }
 
 // Output rows from the normalized rows of whole blocks, or from the partial
 // results of the runs that share a block (added up in their order), rotated
-// back.  A block of threads takes a token's heads, a warp each; or, where rows
-// are few and shared by many runs, one row with WARPS warps that take its runs
-// in turn, so that their loads overlap.
-template <int D, int WARPS>
+// back.  Many rows: a block of threads takes up to 64 rows of one block, whose
+// place it finds once; each warp has four rows in flight.
+constexpr int kJoinRows = 64, kJoinThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) k_attend_paged_join_many(const __grid_constant__ PagedParams p) {
+  constexpr int V = D / 32, N = 4, kWarps = kJoinThreads / 32;
+  __shared__ int s_item[4];  // sequence (-1: none), KV head, block, part
+  __shared__ Place s_place;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // (by value, field by field: a reference to either would make every use a load from global memory)
+  auto cut_of = [&](const Seq &s) {
+    const bool few = s.n * p.group <= p.few.upto;
+    PagedCut c;
+    c.rows = few ? p.few.rows : p.many.rows;
+    c.unit = few ? p.few.unit : p.many.unit;
+    c.above = few ? p.few.above : p.many.above;
+    c.upto = few ? p.few.upto : p.many.upto;
+    c.grid = few ? p.few.grid : p.many.grid;
+    c.least = few ? p.few.least : p.many.least;
+    c.first = few ? p.few.first : p.many.first;
+    c.part_o = few ? p.few.part_o : p.many.part_o;
+    c.part_ml = few ? p.few.part_ml : p.many.part_ml;
+    return c;
+  };
+  auto parts_of = [&](const PagedCut &c) { return (c.rows + kJoinRows - 1) / kJoinRows; };
+  if (warp == 0) {
+    if (lane == 0) s_item[0] = -1;
+    __syncwarp();
+    int64_t before = 0;
+    for (int i0 = 0; i0 < p.nseq && before <= blockIdx.x; i0 += 32) {
+      int64_t n = 0;
+      if (i0 + lane < p.nseq) {
+        const Seq s = seq_of(p, i0 + lane);
+        const PagedCut c = cut_of(s);
+        n = (int64_t)blocks_of(p, c, s) * parts_of(c) * p.kv_heads;
+      }
+      int64_t in = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t b = __shfl_up_sync(0xffffffffu, in, o);
+        if (lane >= o) in += b;
+      }
+      const int64_t at = blockIdx.x - (before + in - n);
+      if (at >= 0 && at < n) {
+        const Seq s = seq_of(p, i0 + lane);
+        const PagedCut c = cut_of(s);
+        const int per = blocks_of(p, c, s) * parts_of(c), rest = (int)(at % per);
+        s_item[0] = i0 + lane;
+        s_item[1] = (int)(at / per);
+        s_item[2] = rest / parts_of(c);
+        s_item[3] = rest % parts_of(c);
+        s_place = place_of(p, c, s, i0 + lane, s_item[1], s_item[2]);
+      }
+      before += __shfl_sync(0xffffffffu, in, 31);
+    }
+  }
+  __syncthreads();
+  if (s_item[0] < 0) return;
+  const Seq s = seq_of(p, s_item[0]);
+  const PagedCut c = cut_of(s);
+  const Place f = s_place;
+  const int head = s_item[1], first = s_item[2] * c.rows + s_item[3] * kJoinRows;
+  const int rows = min(min(kJoinRows, c.rows), s.n * p.group - first);
+  for (int r0 = warp; r0 < rows; r0 += N * kWarps) {
+    float v[N][V];
+    int64_t out[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int row = min(first + r0 + i * kWarps, first + rows - 1);  // (a row too many repeats the last)
+      const int t = row / p.group, h = head * p.group + row - t * p.group;
+      out[i] = (int64_t)(s.start + t) * p.heads + h;
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[i][e] = 0.f;
+    }
+    if (f.seen && f.b0 == f.b1) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[i][e] = __ldg(p.whole + out[i] * D + lane * V + e);
+    } else if (f.seen) {
+      float M[N], L[N];
+      int64_t in[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        M[i] = -INFINITY;
+        L[i] = 0.f;
+        in[i] = s_item[3] * kJoinRows + min(r0 + i * kWarps, rows - 1);
+      }
+#pragma unroll 2
+      for (int b = f.b0; b <= f.b1; ++b)
+#pragma unroll
+        for (int i = 0; i < N; ++i) M[i] = fmaxf(M[i], __ldg(&c.part_ml[f.at(c, b) + in[i]].x));
+#pragma unroll 2
+      for (int b = f.b0; b <= f.b1; ++b) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int64_t at = f.at(c, b) + in[i];
+          const float2 a = __ldg(c.part_ml + at);
+          float x[V];
+#pragma unroll
+          for (int e = 0; e < V; ++e) x[e] = __ldg(c.part_o + at * D + lane * V + e);
+          if (a.y != 0.f) {  // the row sees some of the run's keys
+            const float g = a.x == -INFINITY ? 0.f : ex2(a.x - M[i]);
+            L[i] = fmaf(g, a.y, L[i]);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[i][e] = fmaf(g, x[e], v[i][e]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float inv = L[i] != 0.f ? 1.0f / L[i] : 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[i][e] *= inv;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) warp_rotate_back<D>(v[i], p.vdiag, lane);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (r0 + i * kWarps >= rows) break;
+      const int64_t token = out[i] / p.heads;
+      write_row<D>(p.out, token * p.ldo + (out[i] - token * p.heads) * D, v[i], lane, p.bf16);
+    }
+  }
+}
+
+// Few rows, each perhaps shared by many runs: four warps a row, which take its
+// runs in turn, so that their loads overlap, and are added up in the order of
+// the warps.
+template <int D>
 __global__ void __launch_bounds__(128) k_attend_paged_join(const __grid_constant__ PagedParams p) {
   constexpr int V = D / 32;
   __shared__ float s_v[4][D], s_l[4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t token = WARPS == 1 ? blockIdx.x : blockIdx.x / p.heads;
-  const Place f = find_token(p, token);
-  if (!f.there) return;
-  const PagedCut &c = *f.c;
-  int block = -1, units = 0;
-  int64_t before = 0;  // units of a KV head's blocks before this one
-  for (int h = WARPS == 1 ? warp : (int)(blockIdx.x % p.heads); h < p.heads; h += WARPS == 1 ? 4 : p.heads) {
-    const int head = h / p.group, row = f.row0 + h % p.group;
-    if (row / c.rows != block) {
-      block = row / c.rows;
-      before = 0;
-      for (int k = lane; k < block; k += 32) before += units_of(p, c, f.s, k);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-      units = units_of(p, c, f.s, block);
-    }
-    float v[V], L = 0.f;
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = 0.f;
-    const int64_t u0 = f.units0 + head * f.head_units + before;
-    // (units of a call that fit 32 bits, as nearly all do, need no 64-bit division)
-    const bool narrow = u0 + units < 0x7fffffff && f.per < 0x7fffffff;
-    const int b0 = narrow ? (int)((uint32_t)u0 / (uint32_t)f.per) : (int)(u0 / f.per);
-    const int64_t u1 = u0 + max(units, 1) - 1;
-    const int b1 = narrow ? (int)((uint32_t)u1 / (uint32_t)f.per) : (int)(u1 / f.per);
-    if (units > 0 && b0 == b1) {
-      if (WARPS == 1 || warp == 0) {
-        const float *from = p.whole + (token * p.heads + h) * D + lane * V;
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = from[e];
-        L = 1.f;
-      }
-    } else if (units > 0) {
-      const int in = row % c.rows;
-      auto at = [&](int b) { return ((int64_t)2 * b + (b == b0 ? 1 : 0)) * c.rows + in; };
-      float M = -INFINITY;
-      for (int b = b0 + lane; b <= b1; b += 32) M = fmaxf(M, c.part_ml[at(b)].x);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-#pragma unroll 4
-      for (int b = b0 + (WARPS == 1 ? 0 : warp); b <= b1; b += WARPS) {
-        const float2 a = c.part_ml[at(b)];
-        const float *po = c.part_o + at(b) * D + lane * V;
-        float x[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) x[e] = po[e];
-        if (a.y != 0.f) {  // the row sees some of the run's keys
-          const float g = a.x == -INFINITY ? 0.f : ex2(a.x - M);
-          L = fmaf(g, a.y, L);
-#pragma unroll
-          for (int e = 0; e < V; ++e) v[e] = fmaf(g, x[e], v[e]);
-        }
-      }
-    }
-    if constexpr (WARPS > 1) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) s_v[warp][lane * V + e] = v[e];
-      if (lane == 0) s_l[warp] = L;
-      __syncthreads();
-      if (warp > 0) return;
-      L = s_l[0] + s_l[1] + s_l[2] + s_l[3];
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const int j = lane * V + e;
-        v[e] = s_v[0][j] + s_v[1][j] + s_v[2][j] + s_v[3][j];
-      }
-    }
-    const float inv = L != 0.f ? 1.0f / L : 0.f;
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] *= inv;
-    warp_rotate_back<D>(v, p.vdiag, lane);
-    write_row<D>(p.out, token * p.ldo + (int64_t)h * D, v, lane, p.bf16);
+  const int64_t token = blockIdx.x / p.heads;
+  const int h = (int)(blockIdx.x % p.heads);
+  int seq = -1;
+  for (int i0 = 0; i0 < p.nseq; i0 += 32) {
+    const uint32_t m = __ballot_sync(0xffffffffu, i0 + lane < p.nseq && __ldg(p.q_start + i0 + lane) <= token);
+    seq += __popc(m);
+    if (m != 0xffffffffu) break;
   }
+  if (seq < 0) return;
+  const Seq s = seq_of(p, seq);
+  if (token < s.start || token >= s.start + s.n) return;
+  const PagedCut &c = p.few;
+  const int row = (int)(token - s.start) * p.group + h % p.group, block = row / c.rows, in = row - block * c.rows;
+  const Place f = place_of(p, c, s, seq, h / p.group, block);
+  float v[V], L = 0.f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) v[e] = 0.f;
+  if (f.seen && f.b0 == f.b1) {
+    if (warp == 0) {
+      const float *from = p.whole + (token * p.heads + h) * D + lane * V;
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] = from[e];
+      L = 1.f;
+    }
+  } else if (f.seen) {
+    float M = -INFINITY;
+    for (int b = f.b0 + lane; b <= f.b1; b += 32) M = fmaxf(M, c.part_ml[f.at(c, b) + in].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll 4
+    for (int b = f.b0 + warp; b <= f.b1; b += 4) {
+      const float2 a = c.part_ml[f.at(c, b) + in];
+      const float *po = c.part_o + (f.at(c, b) + in) * D + lane * V;
+      float x[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[e] = po[e];
+      if (a.y != 0.f) {  // the row sees some of the run's keys
+        const float g = a.x == -INFINITY ? 0.f : ex2(a.x - M);
+        L = fmaf(g, a.y, L);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = fmaf(g, x[e], v[e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) s_v[warp][lane * V + e] = v[e];
+  if (lane == 0) s_l[warp] = L;
+  __syncthreads();
+  if (warp > 0) return;
+  L = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+  const float inv = L != 0.f ? 1.0f / L : 0.f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const int j = lane * V + e;
+    v[e] = (s_v[0][j] + s_v[1][j] + s_v[2][j] + s_v[3][j]) * inv;
+  }
+  warp_rotate_back<D>(v, p.vdiag, lane);
+  write_row<D>(p.out, token * p.ldo + (int64_t)h * D, v, lane, p.bf16);
 }
 
 int device_sms() {
@@ -319,21 +468,26 @@ tq_status launch_paged(const PagedParams &prm, const tq_quantizer *qk, const tq_
   tq_status rc = TQ_OK;
   const int64_t rows = prm.total_q * prm.heads;
   if (prm.many.grid > 0) {
-    const unsigned blocks = (unsigned)((rows + 15) / 16);
+    const unsigned blocks = (unsigned)((rows + kQueryRows - 1) / kQueryRows);
     if (qk->m)
-      k_paged_queries<D, true><<<blocks, 128, 0, st>>>(prm, qk->w);
+      k_paged_queries<D, true><<<blocks, kQueryRows, 0, st>>>(prm, qk->w);
     else
-      k_paged_queries<D, false><<<blocks, 128, 0, st>>>(prm, qk->w);
+      k_paged_queries<D, false><<<blocks, kQueryRows, 0, st>>>(prm, qk->w);
     if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
     rc = qk->m ? paged_tiles_launch<D, true>(prm, qk->w, qv->w, st) : paged_tiles_launch<D, false>(prm, qk->w, qv->w, st);
     if (rc != TQ_OK) return rc;
   }
   rc = qk->m ? paged_rows_launch<D, true>(prm, qk->w, qv->w, st) : paged_rows_launch<D, false>(prm, qk->w, qv->w, st);
   if (rc != TQ_OK) return rc;
-  if (rows >= 16 * (int64_t)prm.few.grid)
-    k_attend_paged_join<D, 1><<<(unsigned)prm.total_q, 128, 0, st>>>(prm);
-  else
-    k_attend_paged_join<D, 4><<<(unsigned)rows, 128, 0, st>>>(prm);
+  if (prm.many.grid > 0 || rows >= 16 * (int64_t)prm.few.grid) {
+    // parts of blocks of rows: at most one that is not whole per sequence and KV head
+    const int64_t per = std::min(kJoinRows, prm.few.rows);
+    const int64_t most = prm.kv_heads * (prm.total_q * prm.group / per + prm.nseq * (prm.many.grid > 0 ? 4 : 1));
+    if (most > 0x7fffffff) return TQ_ERR_TOO_LARGE;
+    k_attend_paged_join_many<D><<<(unsigned)most, kJoinThreads, 0, st>>>(prm);
+  } else {
+    k_attend_paged_join<D><<<(unsigned)rows, 128, 0, st>>>(prm);
+  }
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 

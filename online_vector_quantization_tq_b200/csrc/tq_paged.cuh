@@ -72,9 +72,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float load16(const void *p, int64_t i, int bf16) {
-  const uint16_t v = static_cast<const uint16_t *>(p)[i];
+__device__ __forceinline__ float widen16(uint16_t v, int bf16) {
   return bf16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
+}
+__device__ __forceinline__ float load16(const void *p, int64_t i, int bf16) {
+  return widen16(static_cast<const uint16_t *>(p)[i], bf16);
 }
 __device__ __forceinline__ uint16_t store16(float v, int bf16) {
   return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
@@ -143,6 +145,54 @@ __device__ __forceinline__ void warp_rotate_back(float (&v)[D / 32], const uint3
   const float f = 1.0f / ((float)D * sqrtf((float)D));
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) v[i] *= f;
+}
+
+// The same for a row held by one thread: no data moves between threads, so
+// where there are rows for every thread a transform costs a fifth of the
+// warp's.  The three rounds are one loop (code of one round: 2 KB at D = 64).
+template <int D>
+__device__ __forceinline__ void thread_fwht(float (&v)[D]) {
+#pragma unroll
+  for (int h = 1; h < D; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < D; ++i)
+      if (!(i & h)) {
+        const float a = v[i], b = v[i + h];
+        v[i] = a + b;
+        v[i + h] = a - b;
+      }
+}
+template <int D>
+__device__ __forceinline__ void thread_signs(float (&v)[D], const uint32_t *words) {
+#pragma unroll
+  for (int g = 0; g < D / 32; ++g) {
+    const uint32_t w = __ldg(words + g);
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      v[32 * g + i] = __uint_as_float(__float_as_uint(v[32 * g + i]) ^ ((w << (31 - i)) & 0x80000000u));
+  }
+}
+template <int D>
+__device__ __forceinline__ void thread_rotate(float (&v)[D], const uint32_t *diag) {
+#pragma unroll 1
+  for (int r = 0; r < 3; ++r) {
+    thread_signs<D>(v, diag + r * (D / 32));
+    thread_fwht<D>(v);
+  }
+  const float f = 1.0f / ((float)D * sqrtf((float)D));
+#pragma unroll
+  for (int i = 0; i < D; ++i) v[i] *= f;
+}
+template <int D>
+__device__ __forceinline__ void thread_rotate_back(float (&v)[D], const uint32_t *diag) {
+#pragma unroll 1
+  for (int r = 2; r >= 0; --r) {
+    thread_fwht<D>(v);
+    thread_signs<D>(v, diag + r * (D / 32));
+  }
+  const float f = 1.0f / ((float)D * sqrtf((float)D));
+#pragma unroll
+  for (int i = 0; i < D; ++i) v[i] *= f;
 }
 
 // D/32 consecutive 16-bit values of one row, written by one lane
