@@ -19,9 +19,11 @@
 //
 // Two codes become two fp16 centroids by one shared-memory lookup.  A table
 // of all 256 code pairs, each in 32 copies, gives every lane its own bank; its
-// rows are 256 bytes (keys' pair and values' pair side by side), so a single
-// byte permute forms the address.  A byte-table expansion in registers (PRMT)
-// takes 2.75 ALU instructions per code against 0.5 here plus half a lookup.
+// rows are 256 bytes (keys' pair and values' pair side by side) and it lies at
+// a multiple of 64 KB in shared memory, so that a single byte permute forms the
+// whole address (a table elsewhere took an addition per lookup: 64 of 520
+// instructions of a step).  A byte-table expansion in registers (PRMT) takes
+// 2.75 ALU instructions per code against 0.5 here plus half a lookup.
 #pragma once
 
 #include "tq_paged.cuh"
@@ -35,12 +37,13 @@ using namespace paged;
 constexpr int kBlock = 16;  // keys of a warp's step; a page is a whole number of them
 constexpr int kLutBytes = 256 * 256;
 
-// Shapes of a variant with NQ groups of 8 query rows.  With one group, 16
-// warps of 128 registers; two groups' accumulators need more: 8 warps.
+// Shapes of a variant with NQ groups of 8 query rows.  As many warps as the
+// registers allow: 16 of 128; two groups' accumulators at d = 128 need 168 (12
+// warps), with the projections' operands 255 (8).
 template <int D, bool IP, int WK, int WV, int NQ>
 struct Shape {
   static constexpr int kRows = 8 * NQ;
-  static constexpr int kWarps = NQ == 1 ? 16 : 8;
+  static constexpr int kWarps = NQ == 1 || D == 64 ? 16 : IP ? 8 : 12;
   static constexpr int kThreads = 32 * kWarps;
   // one warp's stage of the ring: the packed rows of kBlock keys
   static constexpr int kRowK = WK * D / 8, kRowV = WV * D / 8, kRowS = IP ? D / 8 : 0;  // bytes of a packed row
@@ -49,15 +52,22 @@ struct Shape {
   static constexpr int kCodeV = kNormK + kBlock * 8;
   static constexpr int kNormV = kCodeV + kBlock * kRowV;
   static constexpr int kBytes = kNormV + kBlock * 8;
-  // queries: y~ and its low terms, and p, of 16 rows (the projection's MMA tile)
+  // The table takes the second 64 KB of the shared window.  The ring lies on
+  // both sides of it: in what is left of the first 64 KB (the first kLow bytes
+  // of the dynamic memory, which starts below kStart: 1 KB that the system has
+  // and this kernel's static arrays), and behind the table, where the
+  // queries (y~ and its low terms, and p, of 16 rows) come first.
+  static constexpr int kStart = 4096, kLow = 65536 - kStart;
   static constexpr int kQuery = 16 * D * 2 * (IP ? 3 : 1);
-  static constexpr int kMerge = kWarps * kRows * D * 4;  // the warps' outputs, over the ring
+  static constexpr int kMerge = kWarps * kRows * D * 4;  // the warps' outputs, behind the queries
+  static constexpr int kHigh = 232448 + 1024 - 131072 - kQuery;  // bytes behind them
+  static constexpr int kLowStages = kLow / kBytes, kFit = (kLowStages + kHigh / kBytes) / kWarps;
   // steps in flight, the one being used among them
-  static constexpr int kFit = (232448 - 4096 - kLutBytes - kQuery) / (kWarps * kBytes);
   static constexpr int kStages = kFit < 4 ? kFit : 4;
-  static constexpr int kRing = kStages * kWarps * kBytes > kMerge ? kStages * kWarps * kBytes : kMerge;
-  static constexpr int kSmem = kLutBytes + kRing + kQuery;
-  static_assert(kStages >= 3 && kSmem <= 232448 - 4096, "shared memory");
+  static constexpr int kHighStages = kStages * kWarps > kLowStages ? kStages * kWarps - kLowStages : 0;
+  static constexpr int kTail = kHighStages * kBytes > kMerge ? kHighStages * kBytes : kMerge;
+  static constexpr int kEnd = 131072 + kQuery + kTail;  // of the shared window's bytes in use
+  static_assert(kStages >= 3 && kTail <= kHigh, "shared memory");
   // 64-byte value rows: 16-byte piece ^= 2 on every second pair of rows, so that four rows fill the banks
   static constexpr bool kSwizzle = kRowV == 64;
 };
@@ -129,11 +139,14 @@ __device__ __forceinline__ void nibble_words(const uint8_t *g, int J0, uint32_t 
   }
 }
 
-// Two fp16 centroids for byte I of a nibble word: address byte 1 is the code
-// pair, byte 0 the lane's copy.
-template <int I>
-__device__ __forceinline__ uint32_t lookup(const uint8_t *lut, uint32_t word, uint32_t lane4) {
-  return *reinterpret_cast<const uint32_t *>(lut + sm100::prmt(word, lane4, 0x6504u | (I << 4)));
+// Two fp16 centroids (of the keys, or AT = 128: of the values) for byte I of a
+// nibble word.  The address: byte 0 is the lane's copy, byte 1 the code pair,
+// byte 2 the table's 64 KB, all but byte 1 from `lane4`.
+template <int I, int AT>
+__device__ __forceinline__ uint32_t lookup(uint32_t word, uint32_t lane4) {
+  uint32_t v;
+  asm("ld.shared.b32 %0, [%1+%2];" : "=r"(v) : "r"(sm100::prmt(word, lane4, 0x6504u | (I << 4))), "n"(AT));
+  return v;
 }
 
 template <int D, bool IP, int WK, int WV, int NQ>
@@ -145,18 +158,33 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
   constexpr int KS = D / 16;      // MMA steps along the head dimension
   constexpr int MT = D / 16;      // 16-coordinate output tiles
   extern __shared__ __align__(256) uint8_t smem[];
-  uint8_t *lut = smem;
-  uint8_t *ring = smem + kLutBytes;
-  uint16_t *yh = reinterpret_cast<uint16_t *>(ring + ST::kRing);  // [16][D], then the low terms, and p
+  const uint32_t start = sm100::smem_u32(smem);
+  uint8_t *lut = smem + (65536 - start);
+  uint16_t *yh = reinterpret_cast<uint16_t *>(lut + kLutBytes);  // [16][D], then the low terms, and p
   uint16_t *yl = yh + 16 * D, *ph = yl + 16 * D;
+  uint8_t *tail = lut + kLutBytes + ST::kQuery;
   __shared__ int64_t s_run[5];
   __shared__ int s_some;
   __shared__ float s_f[2][16];  // factors of the scaled queries y~ and p
   __shared__ int s_pmax[16];
+  __shared__ float s_psum[16];
   __shared__ uint16_t s_c[32];
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_v[kWarps];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+  {
+    uint32_t size;
+    asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(size));
+    if (start > ST::kStart || start + size < ST::kEnd) {  // (not on this architecture: launch_rows sees to it)
+      if (tid == 0) atomicCAS(p.err, 0, 131);
+      return;
+    }
+  }
+  // this warp's stage of the ring
+  auto stage_at = [&](int j) {
+    const int i = (j % kStages) * kWarps + warp;
+    return i < ST::kLowStages ? smem + (ST::kStart - start) + i * ST::kBytes : tail + (i - ST::kLowStages) * ST::kBytes;
+  };
   if (tid < 32) {
     s_c[tid] = tid < 16 ? p.ck[tid] : p.cv[tid - 16];
     const bool some = find_run(p, p.few, s_run);
@@ -171,7 +199,7 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
     const uint32_t v = t[byte & 15] | (uint32_t)t[byte >> 4] << 16;
     *reinterpret_cast<uint4 *>(lut + byte * 256 + part * 16) = make_uint4(v, v, v, v);
   }
-  const uint32_t lane4 = lane * 4;
+  const uint32_t lane4 = lane * 4 | 1u << 8;
   Cursor cur = start_run(p, p.few, s_run);
 
   for (;;) {
@@ -185,9 +213,10 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
     const int32_t *table = p.table + (int64_t)cur.seq * p.ldt;
     const int nblk = (k1 - k0 + kBlock - 1) / kBlock;
     const int mine = nblk > warp ? (nblk - warp + kWarps - 1) / kWarps : 0;  // steps of this warp
+    const int page_rows = p.kv_heads * p.page_size, head_row = head * p.page_size;
     uint32_t okbits = 0;
     auto page_at = [&](int j) -> int {  // page of the warp's step j
-      return j < mine ? __ldg(table + (k0 + (warp + j * kWarps) * kBlock) / p.page_size) : -1;
+      return j < mine ? __ldg(table + p.page_of(k0 + (warp + j * kWarps) * kBlock)) : -1;
     };
     auto copy = [&](int j, int page) {
       if (j < mine) {
@@ -195,8 +224,8 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
         okbits = (okbits & ~(1u << (j & 31))) | ((ok ? 1u : 0u) << (j & 31));
         if (ok) {
           const int key = k0 + (warp + j * kWarps) * kBlock;
-          const int64_t row = ((int64_t)page * p.kv_heads + head) * p.page_size + key % p.page_size;
-          const uint32_t st = sm100::smem_u32(ring + ((j % kStages) * kWarps + warp) * ST::kBytes);
+          const int64_t row = (int64_t)page * page_rows + (head_row + key - p.page_of(key) * p.page_size);
+          const uint32_t st = sm100::smem_u32(stage_at(j));
           const uint8_t *kc = p.kcodes + row * ST::kRowK, *vc = p.vcodes + row * ST::kRowV;
 #pragma unroll
           for (int i = 0; i < ST::kRowK; i += 32)  // kBlock rows = kRowK pieces of 16 bytes
@@ -300,6 +329,16 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
         }
       }
       __syncthreads();
+#pragma unroll
+      for (int i = warp; i < kRows; i += kWarps) {
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) sum += __half2float(__ushort_as_half(ph[i * D + e * 32 + lane]));
+#pragma unroll
+        for (int b = 16; b > 0; b >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, b);
+        if (lane == 0) s_psum[i] = sum;
+      }
+      __syncthreads();
     }
     // the B operands (column r: query row r of a group of 8): step k of a lane
     // pairs the coordinates of its nibble word k / 2, bytes 2 (k % 2) and
@@ -318,11 +357,15 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
             qb[q][k][e] = yh[row * D + j0] | (uint32_t)yh[row * D + j1] << 16;
             if constexpr (IP) {
               const int i = 2 * k + e + (D == 128 ? 0 : 8 * (c & 1));  // sign bits i and i + 16 of the lane's word
-              pb[q][k][e] = ph[row * D + 32 * grp + i] | (uint32_t)ph[row * D + 32 * grp + i + 16] << 16;
+              // times 2^15 over the value of the keys' bit (see there): exact, p is below 1
+              const __half2 up = __float2half2_rn((float)(1 << (15 - i % 8)));
+              const __half2 v = __hmul2(__halves2half2(__ushort_as_half(ph[row * D + 32 * grp + i]),
+                                                       __ushort_as_half(ph[row * D + 32 * grp + i + 16])), up);
+              pb[q][k][e] = *reinterpret_cast<const uint32_t *>(&v);
             }
           }
     }
-    float fy[NQ][2], fp[NQ][2];  // columns 2 c and 2 c + 1 of the accumulators
+    float fy[NQ][2], fp[NQ][2], pc[NQ][2];  // columns 2 c and 2 c + 1 of the accumulators
     int lim[NQ][2];
     const int lim_min = min(s.len, hidden + row0 / p.group);
 #pragma unroll
@@ -331,7 +374,10 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
       for (int e = 0; e < 2; ++e) {
         const int i = 8 * q + 2 * c + e, row = row0 + i;
         fy[q][e] = s_f[0][i] * (p.scale * 1.4426950408889634f);
+        // <p, +-1> = 2 <p, bits> - sum p, and the bits' product comes 2^-9 too small
         fp[q][e] = IP ? s_f[1][i] * (p.scale * 1.4426950408889634f * p.kappa) : 0.f;
+        pc[q][e] = IP ? -s_psum[i] * fp[q][e] : 0.f;
+        fp[q][e] *= 1024.f;
         lim[q][e] = row < rows ? min(hidden + row / p.group, s.len) : s.len;  // (columns of no row are zeros)
       }
 
@@ -358,7 +404,7 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
       copy(j + kStages - 1, next_page);
       next_page = page_at(j + kStages);
       if (!((okbits >> (j & 31)) & 1u)) continue;
-      const uint8_t *st = ring + ((j % kStages) * kWarps + warp) * ST::kBytes;
+      const uint8_t *st = stage_at(j);
       const int key0 = k0 + (warp + j * kWarps) * kBlock;
       // position 8 i + 2 c + e of a step (a row of A, or of B for the values)
       // holds key 8 i + (e ? 4 + (c ^ 1) : c)
@@ -378,10 +424,10 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
                                D == 128 ? 0 : 2 * (c & 1), word[i]);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-          const uint32_t a[4] = {lookup<0>(lut, word[0][w], lane4), lookup<0>(lut, word[1][w], lane4),
-                                 lookup<1>(lut, word[0][w], lane4), lookup<1>(lut, word[1][w], lane4)};
-          const uint32_t b[4] = {lookup<2>(lut, word[0][w], lane4), lookup<2>(lut, word[1][w], lane4),
-                                 lookup<3>(lut, word[0][w], lane4), lookup<3>(lut, word[1][w], lane4)};
+          const uint32_t a[4] = {lookup<0, 0>(word[0][w], lane4), lookup<0, 0>(word[1][w], lane4),
+                                 lookup<1, 0>(word[0][w], lane4), lookup<1, 0>(word[1][w], lane4)};
+          const uint32_t b[4] = {lookup<2, 0>(word[0][w], lane4), lookup<2, 0>(word[1][w], lane4),
+                                 lookup<3, 0>(word[0][w], lane4), lookup<3, 0>(word[1][w], lane4)};
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
             // two chains of sums: the second holds the signs' part, or half of the codes'
@@ -390,19 +436,20 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
           }
         }
         if constexpr (IP) {
-          uint32_t sw[2];
+          uint32_t sw[2], hw[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             sw[i] = *reinterpret_cast<const uint32_t *>(st + ST::kSigns + (8 * i + kpos) * ST::kRowS +
                                                         (D == 128 ? c : c >> 1) * 4);
             if (D == 64) sw[i] >>= 8 * (c & 1);
+            hw[i] = sw[i] >> 8;
           }
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
-            const uint32_t a[4] = {((sw[0] << (15 - 2 * k)) & 0x80008000u) ^ 0xBC00BC00u,
-                                   ((sw[1] << (15 - 2 * k)) & 0x80008000u) ^ 0xBC00BC00u,
-                                   ((sw[0] << (14 - 2 * k)) & 0x80008000u) ^ 0xBC00BC00u,
-                                   ((sw[1] << (14 - 2 * k)) & 0x80008000u) ^ 0xBC00BC00u};
+            // bits i and i + 16 (i = 2 k, then 2 k + 1) where they stand: as fp16, 2^(i % 8 - 24) or 0
+            const uint32_t m0 = 0x00010001u << (2 * k % 8), m1 = 0x00010001u << (2 * k % 8 + 1);
+            const uint32_t *w = 2 * k < 8 ? sw : hw;
+            const uint32_t a[4] = {w[0] & m0, w[1] & m0, w[0] & m1, w[1] & m1};
 #pragma unroll
             for (int q = 0; q < NQ; ++q) mma16816(acc2[q], a, pb[q][k][0], pb[q][k][1]);
           }
@@ -421,7 +468,7 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float a = (IP ? acc[q][2 * i + e] : acc[q][2 * i + e] + acc2[q][2 * i + e]) * fy[q][e];
-              x[q][i][e] = kn.x * (IP ? fmaf(acc2[q][2 * i + e] * fp[q][e], kn.y, a) : a);
+              x[q][i][e] = kn.x * (IP ? fmaf(fmaf(acc2[q][2 * i + e], fp[q][e], pc[q][e]), kn.y, a) : a);
             }
         }
       }
@@ -514,12 +561,11 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
           ev[i] = (n[i][0][w] & 0x0F0F0F0Fu) | ((n[i][1][w] << 4) & 0xF0F0F0F0u);
           od[i] = ((n[i][0][w] >> 4) & 0x0F0F0F0Fu) | (n[i][1][w] & 0xF0F0F0F0u);
         }
-        const uint8_t *vl = lut + 128;
         const uint32_t a[4][4] = {
-            {lookup<0>(vl, ev[0], lane4), lookup<0>(vl, od[0], lane4), lookup<0>(vl, ev[1], lane4), lookup<0>(vl, od[1], lane4)},
-            {lookup<1>(vl, ev[0], lane4), lookup<1>(vl, od[0], lane4), lookup<1>(vl, ev[1], lane4), lookup<1>(vl, od[1], lane4)},
-            {lookup<2>(vl, ev[0], lane4), lookup<2>(vl, od[0], lane4), lookup<2>(vl, ev[1], lane4), lookup<2>(vl, od[1], lane4)},
-            {lookup<3>(vl, ev[0], lane4), lookup<3>(vl, od[0], lane4), lookup<3>(vl, ev[1], lane4), lookup<3>(vl, od[1], lane4)}};
+            {lookup<0, 128>(ev[0], lane4), lookup<0, 128>(od[0], lane4), lookup<0, 128>(ev[1], lane4), lookup<0, 128>(od[1], lane4)},
+            {lookup<1, 128>(ev[0], lane4), lookup<1, 128>(od[0], lane4), lookup<1, 128>(ev[1], lane4), lookup<1, 128>(od[1], lane4)},
+            {lookup<2, 128>(ev[0], lane4), lookup<2, 128>(od[0], lane4), lookup<2, 128>(ev[1], lane4), lookup<2, 128>(od[1], lane4)},
+            {lookup<3, 128>(ev[0], lane4), lookup<3, 128>(od[0], lane4), lookup<3, 128>(ev[1], lane4), lookup<3, 128>(od[1], lane4)}};
 #pragma unroll
         for (int b = 0; b < 4; ++b)
 #pragma unroll
@@ -543,7 +589,7 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
       }
     if (lane == 0) s_v[warp] = vtop;
     __syncthreads();  // every warp is done with the ring
-    float *so = reinterpret_cast<float *>(ring);
+    float *so = reinterpret_cast<float *>(tail);
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
 #pragma unroll
@@ -596,9 +642,12 @@ template <int D, bool IP, int WK, int WV, int NQ>
 tq_status launch_rows(const PagedParams &prm, cudaStream_t st) {
   using ST = Shape<D, IP, WK, WV, NQ>;
   auto kern = k_attend_paged<D, IP, WK, WV, NQ>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ST::kSmem) != cudaSuccess)
-    return TQ_ERR_CUDA;
-  kern<<<(unsigned)prm.few.grid, ST::kThreads, ST::kSmem, st>>>(prm);
+  // dynamic memory starts behind the system's 1 KB and the kernel's static arrays (the kernel checks)
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return TQ_ERR_CUDA;
+  const int smem = ST::kEnd - 1024 - (int)fa.sharedSizeBytes;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return TQ_ERR_CUDA;
+  kern<<<(unsigned)prm.few.grid, ST::kThreads, smem, st>>>(prm);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
