@@ -207,14 +207,8 @@ __device__ __forceinline__ Place place_of(const PagedParams &p, const PagedCut &
   if (!f.seen) return f;
   const int64_t u0 = __ldg(c.first + seq) + head * all + before, u1 = u0 + units - 1;
   const int64_t per = run_units(c, __ldg(c.first + p.nseq));
-  if (u1 < 0x7fffffff) {  // (as in nearly all calls: no 64-bit division)
-    const uint32_t d = (uint32_t)min(per, (int64_t)0x7fffffff);
-    f.b0 = (int)((uint32_t)u0 / d);
-    f.b1 = (int)((uint32_t)u1 / d);
-  } else {
-    f.b0 = (int)(u0 / per);
-    f.b1 = (int)(u1 / per);
-  }
+  f.b0 = (int)divide(u0, per);
+  f.b1 = (int)divide(u1, per);
   return f;
 }
 
@@ -267,9 +261,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_paged_join_many(const _
       if (at >= 0 && at < n) {
         const Seq s = seq_of(p, i0 + lane);
         const PagedCut c = cut_of(s);
-        const int per = blocks_of(p, c, s) * parts_of(c), rest = (int)(at % per);
+        const int per = blocks_of(p, c, s) * parts_of(c), rest = (int)(at - divide(at, per) * per);
         s_item[0] = i0 + lane;
-        s_item[1] = (int)(at / per);
+        s_item[1] = (int)divide(at, per);
         s_item[2] = rest / parts_of(c);
         s_item[3] = rest % parts_of(c);
         s_place = place_of(p, c, s, i0 + lane, s_item[1], s_item[2]);

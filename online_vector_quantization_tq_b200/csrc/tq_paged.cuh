@@ -240,8 +240,13 @@ __device__ __forceinline__ int64_t head_units(const PagedParams &p, const PagedC
   for (int k = 0, n = blocks_of(p, c, s); k < n; ++k) u += units_of(p, c, s, k);
   return u;
 }
+// a / b of non-negative numbers, nearly always of 32 bits (a 64-bit division takes a microsecond)
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
 __device__ __forceinline__ int64_t run_units(const PagedCut &c, int64_t total) {
-  return max((total + c.grid - 1) / c.grid, (int64_t)c.least);
+  return max(divide(total + c.grid - 1, c.grid), (int64_t)c.least);
 }
 
 // Where a run stands: the units [unit, unit + take) of a block of rows.
@@ -318,7 +323,8 @@ __device__ __forceinline__ bool find_run(const PagedParams &p, const PagedCut &c
     }
     const int64_t at = from - (before + in - u);
     if (u > 0 && at >= 0 && at < u) {
-      int64_t rest = at % hu;
+      const int64_t head = divide(at, hu);
+      int64_t rest = at - head * hu;
       int k = 0;
       for (;; ++k) {
         const int n = units_of(p, c, s, k);
@@ -326,7 +332,7 @@ __device__ __forceinline__ bool find_run(const PagedParams &p, const PagedCut &c
         rest -= n;
       }
       found[0] = i0 + lane;
-      found[1] = at / hu;
+      found[1] = head;
       found[2] = k;
       found[3] = rest;
       found[4] = min(per, total - from);

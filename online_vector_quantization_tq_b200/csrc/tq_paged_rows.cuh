@@ -58,14 +58,16 @@ struct Shape {
   // and this kernel's static arrays), and behind the table, where the
   // queries (y~ and its low terms, and p, of 16 rows) come first.
   static constexpr int kStart = 4096, kLow = 65536 - kStart;
-  static constexpr int kQuery = 16 * D * 2 * (IP ? 3 : 1);
-  static constexpr int kMerge = kWarps * kRows * D * 4;  // the warps' outputs, behind the queries
+  static constexpr int kLdq = D + 8;  // elements: 16-byte pieces of 8 rows fall into different banks
+  static constexpr int kQuery = 16 * kLdq * 2 * (IP ? 3 : 1);
+  static constexpr int kLdo = D + 4;                        // floats: accumulators of a warp fall into different banks
+  static constexpr int kMerge = kWarps * kRows * kLdo * 4;  // the warps' outputs, over queries and ring
   static constexpr int kHigh = 232448 + 1024 - 131072 - kQuery;  // bytes behind them
   static constexpr int kLowStages = kLow / kBytes, kFit = (kLowStages + kHigh / kBytes) / kWarps;
   // steps in flight, the one being used among them
   static constexpr int kStages = kFit < 4 ? kFit : 4;
   static constexpr int kHighStages = kStages * kWarps > kLowStages ? kStages * kWarps - kLowStages : 0;
-  static constexpr int kTail = kHighStages * kBytes > kMerge ? kHighStages * kBytes : kMerge;
+  static constexpr int kTail = kHighStages * kBytes > kMerge - kQuery ? kHighStages * kBytes : kMerge - kQuery;
   static constexpr int kEnd = 131072 + kQuery + kTail;  // of the shared window's bytes in use
   static_assert(kStages >= 3 && kTail <= kHigh, "shared memory");
   // 64-byte value rows: 16-byte piece ^= 2 on every second pair of rows, so that four rows fill the banks
@@ -157,11 +159,12 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
   constexpr int NW = D / 32;      // nibble words of a key per lane (a quad holds a key)
   constexpr int KS = D / 16;      // MMA steps along the head dimension
   constexpr int MT = D / 16;      // 16-coordinate output tiles
+  constexpr int LDQ = ST::kLdq, LDO = ST::kLdo;
   extern __shared__ __align__(256) uint8_t smem[];
   const uint32_t start = sm100::smem_u32(smem);
   uint8_t *lut = smem + (65536 - start);
-  uint16_t *yh = reinterpret_cast<uint16_t *>(lut + kLutBytes);  // [16][D], then the low terms, and p
-  uint16_t *yl = yh + 16 * D, *ph = yl + 16 * D;
+  uint16_t *yh = reinterpret_cast<uint16_t *>(lut + kLutBytes);  // [16][LDQ], then the low terms, and p
+  uint16_t *yl = yh + 16 * LDQ, *ph = yl + 16 * LDQ;
   uint8_t *tail = lut + kLutBytes + ST::kQuery;
   __shared__ int64_t s_run[5];
   __shared__ int s_some;
@@ -185,20 +188,42 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
     const int i = (j % kStages) * kWarps + warp;
     return i < ST::kLowStages ? smem + (ST::kStart - start) + i * ST::kBytes : tail + (i - ST::kLowStages) * ST::kBytes;
   };
-  if (tid < 32) {
-    s_c[tid] = tid < 16 ? p.ck[tid] : p.cv[tid - 16];
+  if (tid < 32) s_c[tid] = tid < 16 ? p.ck[tid] : p.cv[tid - 16];
+  // S's fragments of a warp's 8 columns of the projection: loaded long before they are used
+  constexpr int PT = D / 8 > kWarps ? D / 8 / kWarps : 1;  // tiles of 8 columns of a warp: warp, warp + kWarps, ..
+  uint32_t sb[IP ? PT : 1][IP ? KS : 1][2];
+  auto load_projection = [&] {
+    if constexpr (IP) {
+      if (warp < D / 8) {
+#pragma unroll
+        for (int t = 0; t < PT; ++t) {
+          const uint32_t *srow = reinterpret_cast<const uint32_t *>(p.qjl + ((warp + t * kWarps) * 8 + r) * D) + c;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            sb[t][k][0] = __ldg(srow + 8 * k);
+            sb[t][k][1] = __ldg(srow + 8 * k + 4);
+          }
+        }
+      }
+    }
+  };
+  load_projection();
+  __syncthreads();
+  if (warp == 0) {
     const bool some = find_run(p, p.few, s_run);
-    if (tid == 0) s_some = some;
+    if (lane == 0) s_some = some;
+  } else {
+    for (int i = tid - 32; i < 256 * 16; i += kThreads - 32) {  // 16-byte pieces: 4 copies
+      const int byte = i >> 4, part = i & 15;
+      const uint16_t *t = s_c + (part < 8 ? 0 : 16);
+      const uint32_t v = t[byte & 15] | (uint32_t)t[byte >> 4] << 16;
+      *reinterpret_cast<uint4 *>(lut + byte * 256 + part * 16) = make_uint4(v, v, v, v);
+    }
+    for (int i = tid - 32; i < ST::kQuery / 16; i += kThreads - 32)
+      reinterpret_cast<uint4 *>(yh)[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-  for (int i = tid; i < ST::kQuery / 16; i += kThreads) reinterpret_cast<uint4 *>(yh)[i] = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();
   if (!s_some) return;
-  for (int i = tid; i < 256 * 16; i += kThreads) {  // 16-byte pieces: 4 copies
-    const int byte = i >> 4, part = i & 15;
-    const uint16_t *t = s_c + (part < 8 ? 0 : 16);
-    const uint32_t v = t[byte & 15] | (uint32_t)t[byte >> 4] << 16;
-    *reinterpret_cast<uint4 *>(lut + byte * 256 + part * 16) = make_uint4(v, v, v, v);
-  }
   const uint32_t lane4 = lane * 4 | 1u << 8;
   Cursor cur = start_run(p, p.few, s_run);
 
@@ -282,35 +307,31 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
       for (int e = 0; e < D / 32; ++e) {
         const float x = v[e] * down;
         const __half hi = __float2half_rn(x);
-        yh[i * D + lane * (D / 32) + e] = __half_as_ushort(hi);
-        if (IP) yl[i * D + lane * (D / 32) + e] = __half_as_ushort(__float2half_rn(x - __half2float(hi)));
+        yh[i * LDQ + lane * (D / 32) + e] = __half_as_ushort(hi);
+        if (IP) yl[i * LDQ + lane * (D / 32) + e] = __half_as_ushort(__float2half_rn(x - __half2float(hi)));
       }
     }
     __syncthreads();
     if constexpr (IP) {
-      // p[row][i] = sum_j S[i][j] y~[row][j]; warp w has the 8-column tiles w, w + kWarps, ..
-      constexpr int T = D / 8 > kWarps ? D / 8 / kWarps : 1;
-      float acc[T][4];
+      // p[row][i] = sum_j S[i][j] y~[row][j]
+      float acc[PT][4];
       if (warp < D / 8) {
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
+        for (int t = 0; t < PT; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
-          const uint32_t *srow = reinterpret_cast<const uint32_t *>(p.qjl + ((warp + t * kWarps) * 8 + r) * D);
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            const uint32_t b0 = __ldg(srow + 8 * k + c), b1 = __ldg(srow + 8 * k + c + 4);
+        for (int k = 0; k < KS; ++k)
 #pragma unroll
-            for (int term = 0; term < 2; ++term) {
-              const uint32_t *ya = reinterpret_cast<const uint32_t *>((term ? yl : yh) + r * D + 16 * k) + c;
-              const uint32_t a[4] = {ya[0], ya[8 * (D / 2)], ya[4], ya[8 * (D / 2) + 4]};
-              mma16816(acc[t], a, b0, b1);
-            }
+          for (int term = 0; term < 2; ++term) {
+            const uint32_t *ya = reinterpret_cast<const uint32_t *>((term ? yl : yh) + r * LDQ + 16 * k) + c;
+            const uint32_t a[4] = {ya[0], ya[8 * (LDQ / 2)], ya[4], ya[8 * (LDQ / 2) + 4]};
+#pragma unroll
+            for (int t = 0; t < PT; ++t) mma16816(acc[t], a, sb[t][k][0], sb[t][k][1]);
           }
-        }
         float top[2] = {0.f, 0.f};
 #pragma unroll
-        for (int t = 0; t < T; ++t)
+        for (int t = 0; t < PT; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], fabsf(acc[t][e]));
 #pragma unroll
@@ -323,9 +344,13 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
           const float up = pow2_above(__int_as_float(s_pmax[r + 8 * h])), down = 1.0f / up;
           if (warp == 0 && c == 0) s_f[1][r + 8 * h] = up * s_f[0][r + 8 * h];
 #pragma unroll
-          for (int t = 0; t < T; ++t)
-            reinterpret_cast<__half2 *>(ph + (r + 8 * h) * D + (warp + t * kWarps) * 8)[c] =
-                __floats2half2_rn(acc[t][2 * h] * down, acc[t][2 * h + 1] * down);
+          for (int t = 0; t < PT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int j = (warp + t * kWarps) * 8 + 2 * c + e, b = j % 32;  // coordinates k and k + 16 side by side
+              ph[(r + 8 * h) * LDQ + j / 32 * 32 + (b < 16 ? 2 * b : 2 * (b - 16) + 1)] =
+                  __half_as_ushort(__float2half_rn(acc[t][2 * h + e] * down));
+            }
         }
       }
       __syncthreads();
@@ -333,7 +358,7 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
       for (int i = warp; i < kRows; i += kWarps) {
         float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) sum += __half2float(__ushort_as_half(ph[i * D + e * 32 + lane]));
+        for (int e = 0; e < D / 32; ++e) sum += __half2float(__ushort_as_half(ph[i * LDQ + e * 32 + lane]));
 #pragma unroll
         for (int b = 16; b > 0; b >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, b);
         if (lane == 0) s_psum[i] = sum;
@@ -349,21 +374,31 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+        for (int k = 0; k < KS; k += 2) {  // a nibble word
+          const uint16_t *y = yh + (8 * q + r) * LDQ + 32 * grp;
+          const int J = jo + (k >> 1);
+          if constexpr (WK != 1) {  // eight neighbours
+            const uint4 v = *reinterpret_cast<const uint4 *>(y + 8 * J);
+            qb[q][k][0] = v.x, qb[q][k][1] = v.y, qb[q][k + 1][0] = v.z, qb[q][k + 1][1] = v.w;
+          } else {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int row = 8 * q + r, byte = 2 * (k & 1) + e, J = jo + (k >> 1);
-            const int j0 = 32 * grp + nibble_coord<WK>(J, 2 * byte), j1 = 32 * grp + nibble_coord<WK>(J, 2 * byte + 1);
-            qb[q][k][e] = yh[row * D + j0] | (uint32_t)yh[row * D + j1] << 16;
-            if constexpr (IP) {
-              const int i = 2 * k + e + (D == 128 ? 0 : 8 * (c & 1));  // sign bits i and i + 16 of the lane's word
-              // times 2^15 over the value of the keys' bit (see there): exact, p is below 1
-              const __half2 up = __float2half2_rn((float)(1 << (15 - i % 8)));
-              const __half2 v = __hmul2(__halves2half2(__ushort_as_half(ph[row * D + 32 * grp + i]),
-                                                       __ushort_as_half(ph[row * D + 32 * grp + i + 16])), up);
-              pb[q][k][e] = *reinterpret_cast<const uint32_t *>(&v);
+            for (int e = 0; e < 4; ++e)
+              qb[q][k + (e >> 1)][e & 1] = y[nibble_coord<WK>(J, 2 * e)] | (uint32_t)y[nibble_coord<WK>(J, 2 * e + 1)] << 16;
+          }
+          if constexpr (IP) {
+            // sign bits i and i + 16 of the lane's word, i = 2 k .. 2 k + 3, times 2^15 over the value of the keys'
+            // bit (see there): exact, p is below 1
+            const int i0 = 2 * k + (D == 128 ? 0 : 8 * (c & 1));
+            const uint4 v = *reinterpret_cast<const uint4 *>(ph + (8 * q + r) * LDQ + 32 * grp + 2 * i0);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __half2 u = __hmul2(*reinterpret_cast<const __half2 *>(w + e),
+                                        __float2half2_rn((float)(1 << (15 - (2 * k + e) % 8))));
+              pb[q][k + (e >> 1)][e & 1] = *reinterpret_cast<const uint32_t *>(&u);
             }
           }
+        }
     }
     float fy[NQ][2], fp[NQ][2], pc[NQ][2];  // columns 2 c and 2 c + 1 of the accumulators
     int lim[NQ][2];
@@ -589,18 +624,16 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
       }
     if (lane == 0) s_v[warp] = vtop;
     __syncthreads();  // every warp is done with the ring
-    float *so = reinterpret_cast<float *>(tail);
+    load_projection();  // (for the next block of rows)
+    // coordinate (D / 8) r + i of a row, i = 2 t + (e >> 1), stands at 8 i + r
+    float *so = reinterpret_cast<float *>(yh);
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // tile t: word t / 4, byte t % 4, its low (rows 0-7) or high nibble, of lane group r's piece
-          const int J = (D == 128 ? 2 * (r & 1) : r & 3) + (t >> 2);
-          const int j = 32 * (D == 128 ? r >> 1 : r >> 2) + 8 * J + 2 * (t & 3) + (e >> 1);
-          so[(warp * kRows + 8 * q + 2 * c + (e & 1)) * D + j] = o[q][t][e];
-        }
+        for (int e = 0; e < 4; ++e)
+          so[(warp * kRows + 8 * q + 2 * c + (e & 1)) * LDO + 8 * (2 * t + (e >> 1)) + r] = o[q][t][e];
     __syncthreads();
     for (int i = warp; i < kRows; i += kWarps) {
       const int row = row0 + i;
@@ -616,7 +649,7 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
         if (s_l[w][i] != 0.f) {  // the row sees some of the warp's keys
           L += f * s_l[w][i];
 #pragma unroll
-          for (int e = 0; e < D / 32; ++e) v[e] += f * s_v[w] * so[(w * kRows + i) * D + lane * (D / 32) + e];
+          for (int e = 0; e < D / 32; ++e) v[e] += f * s_v[w] * so[(w * kRows + i) * LDO + lane * (D / 32) + e];
         }
       }
       float *to;
@@ -631,10 +664,13 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
         to = p.few.part_o + at * D;
       }
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) to[lane * (D / 32) + e] = v[e];
+      for (int e = 0; e < D / 32; ++e) {
+        const int at = lane * (D / 32) + e;
+        to[(D / 8) * (at & 7) + (at >> 3)] = v[e];
+      }
     }
     if (!cur.next(p, p.few)) break;
-    __syncthreads();  // the ring is free
+    __syncthreads();  // the ring and the queries' place are free
   }
 }
 
