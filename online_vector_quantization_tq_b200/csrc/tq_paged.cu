@@ -529,7 +529,8 @@ tq_status attend_paged_launch(const tq_quantizer *qk, const tq_quantizer *qv, co
   const int64_t group = a.heads / a.kv_heads;
   const Plan L = plan_of(qk, a.total_q, a.nseq, a.heads, a.kv_heads, a.max_new, device_sms());
   if (!a.workspace || a.workspace_bytes < L.total) return TQ_ERR_WORKSPACE;
-  if (a.total_q * a.heads > 0x7fffffff) return TQ_ERR_TOO_LARGE;
+  if (a.total_q * a.heads > 0x7fffffff || a.npages > (int64_t)0xffffffff / (a.kv_heads * a.page_size))
+    return TQ_ERR_TOO_LARGE;
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(a.workspace) + 255) & ~uintptr_t(255));
   prm.y = a.y;
   prm.ldy = a.ldy;

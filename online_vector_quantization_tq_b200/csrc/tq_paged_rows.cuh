@@ -183,11 +183,6 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
       return;
     }
   }
-  // this warp's stage of the ring
-  auto stage_at = [&](int j) {
-    const int i = (j % kStages) * kWarps + warp;
-    return i < ST::kLowStages ? smem + (ST::kStart - start) + i * ST::kBytes : tail + (i - ST::kLowStages) * ST::kBytes;
-  };
   if (tid < 32) s_c[tid] = tid < 16 ? p.ck[tid] : p.cv[tid - 16];
   // S's fragments of a warp's 8 columns of the projection: loaded long before they are used
   constexpr int PT = D / 8 > kWarps ? D / 8 / kWarps : 1;  // tiles of 8 columns of a warp: warp, warp + kWarps, ..
@@ -236,52 +231,56 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
 
     // ---- the ring: each warp copies its own steps, kStages - 1 ahead
     const int32_t *table = p.table + (int64_t)cur.seq * p.ldt;
-    const int nblk = (k1 - k0 + kBlock - 1) / kBlock;
-    const int mine = nblk > warp ? (nblk - warp + kWarps - 1) / kWarps : 0;  // steps of this warp
-    const int page_rows = p.kv_heads * p.page_size, head_row = head * p.page_size;
-    uint32_t okbits = 0;
-    auto page_at = [&](int j) -> int {  // page of the warp's step j
-      return j < mine ? __ldg(table + p.page_of(k0 + (warp + j * kWarps) * kBlock)) : -1;
-    };
-    auto copy = [&](int j, int page) {
-      if (j < mine) {
-        const bool ok = page >= 0 && page < p.npages;
-        okbits = (okbits & ~(1u << (j & 31))) | ((ok ? 1u : 0u) << (j & 31));
-        if (ok) {
-          const int key = k0 + (warp + j * kWarps) * kBlock;
-          const int64_t row = (int64_t)page * page_rows + (head_row + key - p.page_of(key) * p.page_size);
-          const uint32_t st = sm100::smem_u32(stage_at(j));
-          const uint8_t *kc = p.kcodes + row * ST::kRowK, *vc = p.vcodes + row * ST::kRowV;
+    const uint32_t page_rows = p.kv_heads * p.page_size, head_row = head * p.page_size;
+    uint32_t okbits = 0;  // bit i: whether the i-th last copied step has a page
+    // stages: [0] the next to be copied into; they move up with every step
+    uint32_t stage[kStages];
 #pragma unroll
-          for (int i = 0; i < ST::kRowK; i += 32)  // kBlock rows = kRowK pieces of 16 bytes
-            if (i + 32 <= ST::kRowK || lane < ST::kRowK - i) cp_async16(st + (i + lane) * 16, kc + (i + lane) * 16);
+    for (int i = 0; i < kStages; ++i) {
+      const int at = i * kWarps + warp;
+      stage[i] = at < ST::kLowStages ? ST::kStart + at * ST::kBytes
+                                     : 131072 + ST::kQuery + (at - ST::kLowStages) * ST::kBytes;
+    }
+    const uint8_t *const kbase = p.kcodes + lane * 16, *const vbase = p.vcodes + lane * 16;
+    const uint8_t *const nbase = reinterpret_cast<const uint8_t *>((lane & 8) ? p.vnorms : p.knorms) + (lane & 7) * 16;
+    const uint32_t nto = ((lane & 8) ? ST::kNormV : ST::kNormK) + (lane & 7) * 16;
+    auto page_at = [&](int key) -> int { return key < k1 ? __ldg(table + p.page_of(key)) : -1; };
+    auto copy = [&](int key, int page) {  // of the step that starts at `key`
+      const bool ok = page >= 0 && page < p.npages;  // (-1 behind the last key)
+      okbits = okbits << 1 | (ok ? 1u : 0u);
+      const uint32_t st = stage[0];
 #pragma unroll
-          for (int i = 0; i < ST::kRowV; i += 32)
-            if (i + 32 <= ST::kRowV || lane < ST::kRowV - i) {
-              const int to = ST::kSwizzle ? (i + lane) ^ (((lane >> 3) & 1) << 1) : i + lane;
-              cp_async16(st + ST::kCodeV + to * 16, vc + (i + lane) * 16);
-            }
-          if (IP && lane < ST::kRowS)
-            cp_async16(st + ST::kSigns + lane * 16, p.ksigns + row * ST::kRowS + lane * 16);
-          if (lane >= 16) {
-            const int i = lane & 7;
-            if (lane < 24)
-              cp_async16(st + ST::kNormK + i * 16, reinterpret_cast<const uint8_t *>(p.knorms + row) + i * 16);
-            else
-              cp_async16(st + ST::kNormV + i * 16, reinterpret_cast<const uint8_t *>(p.vnorms + row) + i * 16);
+      for (int i = 0; i + 1 < kStages; ++i) stage[i] = stage[i + 1];
+      stage[kStages - 1] = st;
+      if (ok) {
+        // (rows of a cache fit 32 bits: the host checks)
+        const uint32_t row = (uint32_t)page * page_rows + (head_row + key - p.page_of(key) * p.page_size);
+        const uint8_t *kc = kbase + (uint64_t)row * (uint32_t)ST::kRowK, *vc = vbase + (uint64_t)row * (uint32_t)ST::kRowV;
+#pragma unroll
+        for (int i = 0; i < ST::kRowK; i += 32)  // kBlock rows = kRowK pieces of 16 bytes
+          if (i + 32 <= ST::kRowK || lane < ST::kRowK - i) cp_async16(st + (i + lane) * 16, kc + i * 16);
+#pragma unroll
+        for (int i = 0; i < ST::kRowV; i += 32)
+          if (i + 32 <= ST::kRowV || lane < ST::kRowV - i) {
+            const int to = ST::kSwizzle ? (i + lane) ^ (((lane >> 3) & 1) << 1) : i + lane;
+            cp_async16(st + ST::kCodeV + to * 16, vc + i * 16);
           }
-        }
+        if (IP && lane < ST::kRowS)
+          cp_async16(st + ST::kSigns + lane * 16, p.ksigns + lane * 16 + (uint64_t)row * (uint32_t)ST::kRowS);
+        if (lane >= 16) cp_async16(st + nto, nbase + (uint64_t)row * 8u);
       }
       cp_async_commit();
     };
+    constexpr int kStep = kWarps * kBlock;
+    int ahead = k0 + warp * kBlock;  // first key of the step to be copied next
     {
       int pages[kStages - 1];
 #pragma unroll
-      for (int j = 0; j < kStages - 1; ++j) pages[j] = page_at(j);
+      for (int j = 0; j < kStages - 1; ++j) pages[j] = page_at(ahead + j * kStep);
 #pragma unroll
-      for (int j = 0; j < kStages - 1; ++j) copy(j, pages[j]);
+      for (int j = 0; j < kStages - 1; ++j, ahead += kStep) copy(ahead, pages[j]);
     }
-    int next_page = page_at(kStages - 1);
+    int next_page = page_at(ahead);
 
     // ---- queries: y~ = R y, scaled by a power of two to below 1 as fp16; for
     // inner-product keys also p = S y~ on the tensor cores (y~ as two fp16 terms)
@@ -425,33 +424,31 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[q][t][e] = 0.f;
     float m[NQ][2], l[NQ][2];
+    float limit[NQ][2], base[NQ][2];  // m + 8; m, or 0 while no key was seen
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m[q][e] = -INFINITY;
-        l[q][e] = 0.f;
+        m[q][e] = limit[q][e] = -INFINITY;
+        l[q][e] = base[q][e] = 0.f;
       }
     float vtop = pow2_above(0.f), vinv = 1.0f / vtop;  // power of two above the value norms seen; weights carry 1 / it
-    for (int j = 0; j < mine; ++j) {
+    for (int key0 = k0 + warp * kBlock; key0 < k1; key0 += kStep) {
       cp_async_wait<kStages - 2>();
       __syncwarp();
-      copy(j + kStages - 1, next_page);
-      next_page = page_at(j + kStages);
-      if (!((okbits >> (j & 31)) & 1u)) continue;
-      const uint8_t *st = stage_at(j);
-      const int key0 = k0 + (warp + j * kWarps) * kBlock;
+      copy(ahead, next_page);
+      ahead += kStep;
+      next_page = page_at(ahead);
+      if (!((okbits >> (kStages - 1)) & 1u)) continue;
+      // the step's stage: the one that the next copy will take
+      const uint8_t *st = smem + (stage[0] - start);
       // position 8 i + 2 c + e of a step (a row of A, or of B for the values)
       // holds key 8 i + (e ? 4 + (c ^ 1) : c)
       const int kpos = (r & 1) ? 4 + ((r >> 1) ^ 1) : r >> 1;
       float x[NQ][2][2];  // [key half][column]
       float vn[2];
       {
-        float acc[NQ][4], acc2[NQ][4];
-#pragma unroll
-        for (int q = 0; q < NQ; ++q)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[q][e] = acc2[q][e] = 0.f;
+        float acc[NQ][4], acc2[IP ? NQ : 1][4];  // codes' part, signs' part
         uint32_t word[2][NW];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -465,9 +462,11 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
                                  lookup<3, 0>(word[0][w], lane4), lookup<3, 0>(word[1][w], lane4)};
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
-            // two chains of sums: the second holds the signs' part, or half of the codes'
-            mma16816(acc[q], a, qb[q][2 * w][0], qb[q][2 * w][1]);
-            mma16816(IP ? acc[q] : acc2[q], b, qb[q][2 * w + 1][0], qb[q][2 * w + 1][1]);
+            if (w == 0)
+              mma16816_new(acc[q], a, qb[q][0][0], qb[q][0][1]);
+            else
+              mma16816(acc[q], a, qb[q][2 * w][0], qb[q][2 * w][1]);
+            mma16816(acc[q], b, qb[q][2 * w + 1][0], qb[q][2 * w + 1][1]);
           }
         }
         if constexpr (IP) {
@@ -486,7 +485,11 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
             const uint32_t *w = 2 * k < 8 ? sw : hw;
             const uint32_t a[4] = {w[0] & m0, w[1] & m0, w[0] & m1, w[1] & m1};
 #pragma unroll
-            for (int q = 0; q < NQ; ++q) mma16816(acc2[q], a, pb[q][k][0], pb[q][k][1]);
+            for (int q = 0; q < NQ; ++q)
+              if (k == 0)
+                mma16816_new(acc2[q], a, pb[q][k][0], pb[q][k][1]);
+              else
+                mma16816(acc2[q], a, pb[q][k][0], pb[q][k][1]);
           }
         }
 #pragma unroll
@@ -502,8 +505,8 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
           for (int q = 0; q < NQ; ++q)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float a = (IP ? acc[q][2 * i + e] : acc[q][2 * i + e] + acc2[q][2 * i + e]) * fy[q][e];
-              x[q][i][e] = kn.x * (IP ? fmaf(fmaf(acc2[q][2 * i + e], fp[q][e], pc[q][e]), kn.y, a) : a);
+              const float a = acc[q][2 * i + e] * fy[q][e];
+              x[q][i][e] = kn.x * (IP ? fmaf(fmaf(acc2[IP ? q : 0][2 * i + e], fp[q][e], pc[q][e]), kn.y, a) : a);
             }
         }
       }
@@ -528,7 +531,7 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float t = fmaxf(x[q][0][e], x[q][1][e]);
-          grow |= t > m[q][e] + 8.f || (m[q][e] == -INFINITY && t > -INFINITY);
+          grow |= t > limit[q][e];
         }
       if (__any_sync(0xffffffffu, grow)) {
         float vt = fmaxf(vn[0], vn[1]);
@@ -548,7 +551,8 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
             float f = 1.f;
             if (t > m[q][e]) {
               f = ex2(m[q][e] - t);
-              m[q][e] = t;
+              m[q][e] = base[q][e] = t;
+              limit[q][e] = t + 8.f;
             }
             l[q][e] *= f;
 #pragma unroll
@@ -564,9 +568,8 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
         float w[2][2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float base = m[q][e] == -INFINITY ? 0.f : m[q][e];  // no key seen so far: every weight is 0
 #pragma unroll
-          for (int i = 0; i < 2; ++i) w[i][e] = ex2(x[q][i][e] - base);
+          for (int i = 0; i < 2; ++i) w[i][e] = ex2(x[q][i][e] - base[q][e]);
           l[q][e] += w[0][e] + w[1][e];
         }
 #pragma unroll
