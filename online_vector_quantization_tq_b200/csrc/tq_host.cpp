@@ -591,6 +591,18 @@ static tq_status build_quantizer(int d, int b, int m, uint64_t seed, tq_rotation
       q->score_ch[k] = (int8_t)hi;
       q->score_cl[k] = (int8_t)(v - 256 * hi);
     }
+    // fp16 centroids under a common factor in [1, 2) chosen so that their
+    // largest relative rounding error is least: 2^-13 to 2^-15 instead of 2^-12
+    double best = 1.0, least = 1e300;
+    for (int i = 0; i < 1024; ++i) {
+      const double f = 1.0 + i / 1024.0;
+      double worst = 0.0;
+      for (double c : q->centroids)
+        if (c != 0.0) worst = std::max(worst, std::fabs(half_bits_to_double(double_to_half_bits(c * f)) / (c * f) - 1.0));
+      if (worst < least) least = worst, best = f;
+    }
+    for (int k = 0; k < L; ++k) q->attend_c[k] = double_to_half_bits(q->centroids[k] * best);
+    q->attend_unit = (float)(1.0 / best);
   }
   KernelTables &kt = q->kt;
   kt.d = d;

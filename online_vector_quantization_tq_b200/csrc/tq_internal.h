@@ -63,6 +63,9 @@ struct tq_quantizer {
   // integer scorer: centroid c_k ~ (256 * ch[k] + cl[k]) * 2^-score_cexp
   int8_t score_ch[tq::kMaxLevels] = {}, score_cl[tq::kMaxLevels] = {};
   int score_cexp = 0;
+  // attention over pages: centroid c_k ~ attend_c[k] (fp16 bits) * attend_unit
+  uint16_t attend_c[tq::kMaxLevels] = {};
+  float attend_unit = 1.f;
   tq::KernelTables kt{};
 };
 

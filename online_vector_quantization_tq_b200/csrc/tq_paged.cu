@@ -427,15 +427,19 @@ struct Plan {
   size_t few_o, few_ml, few_first, many_o, many_ml, many_first, whole, qprep, qscale, total;
 };
 
-Plan plan_of(const tq_quantizer *qk, int64_t total_q, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t max_new,
-             int sms) {
+// f16: of the queries
+Plan plan_of(const tq_quantizer *qk, bool f16, int64_t total_q, int64_t nseq, int64_t heads, int64_t kv_heads,
+             int64_t max_new, int sms) {
   Plan L{};
   const int d = qk->d;
   const bool ip = qk->m > 0;
   const int64_t most = std::min(max_new, total_q) * (heads / kv_heads);
   const bool many = most > kFewRows;
-  // 8 rows a block where that is all there is: twice the warps on an SM
-  L.few = PagedCut{most <= 8 ? 8 : 16, 6, 0, many ? kFewRows : 0x7fffffff, sms, 4, nullptr, nullptr, nullptr};
+  // 8 rows a block where that is all there is: more warps on an SM.  24 where
+  // two blocks of 16 would expand every key twice (5 drafted tokens of 4 heads,
+  // 16 sequences, d = 64); at d = 128 its registers do not suffice.
+  const int rows = most <= 8 && !(f16 && d == 128) ? 8 : d == 64 && most > 16 && most <= 24 ? 24 : 16;
+  L.few = PagedCut{rows, 6, 0, many ? kFewRows : 0x7fffffff, sms, 4, nullptr, nullptr, nullptr};
   if (many) L.many = PagedCut{ip && d == 128 ? 128 : 256, 7, kFewRows, 0x7fffffff, sms, 2, nullptr, nullptr, nullptr};
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -521,13 +525,15 @@ bool attend_paged_supported(const tq_quantizer *qk, const tq_quantizer *qv) {
 
 size_t attend_paged_ws_bytes(const tq_quantizer *qk, int64_t total_q, int64_t nseq, int64_t heads, int64_t kv_heads,
                              int64_t max_new) {
-  return plan_of(qk, total_q, nseq, heads, kv_heads, max_new, device_sms()).total;
+  const int sms = device_sms();
+  return std::max(plan_of(qk, false, total_q, nseq, heads, kv_heads, max_new, sms).total,
+                  plan_of(qk, true, total_q, nseq, heads, kv_heads, max_new, sms).total);
 }
 
 tq_status attend_paged_launch(const tq_quantizer *qk, const tq_quantizer *qv, const PagedArgs &a, cudaStream_t st) {
   PagedParams prm{};
   const int64_t group = a.heads / a.kv_heads;
-  const Plan L = plan_of(qk, a.total_q, a.nseq, a.heads, a.kv_heads, a.max_new, device_sms());
+  const Plan L = plan_of(qk, a.dtype == TQ_F16, a.total_q, a.nseq, a.heads, a.kv_heads, a.max_new, device_sms());
   if (!a.workspace || a.workspace_bytes < L.total) return TQ_ERR_WORKSPACE;
   if (a.total_q * a.heads > 0x7fffffff || a.npages > (int64_t)0xffffffff / (a.kv_heads * a.page_size))
     return TQ_ERR_TOO_LARGE;
@@ -557,11 +563,13 @@ tq_status attend_paged_launch(const tq_quantizer *qk, const tq_quantizer *qv, co
   prm.bf16 = a.dtype == TQ_BF16;
   prm.scale = a.scale;
   for (int i = 0; i < 16; ++i) {
-    prm.ck[i] = i < (1 << qk->w) ? double_to_half_bits(qk->centroids[i]) : 0;
-    prm.cv[i] = i < (1 << qv->w) ? double_to_half_bits(qv->centroids[i]) : 0;
+    prm.ck[i] = i < (1 << qk->w) ? qk->attend_c[i] : 0;
+    prm.cv[i] = i < (1 << qv->w) ? qv->attend_c[i] : 0;
     prm.ckf[i] = i < (1 << qk->w) ? (float)qk->centroids[i] : 0.f;
     prm.cvf[i] = i < (1 << qv->w) ? (float)qv->centroids[i] : 0.f;
   }
+  prm.kunit = qk->attend_unit;
+  prm.vunit = qv->attend_unit;
   prm.kdiag = qk->kt.diag_bits;
   prm.vdiag = qv->kt.diag_bits;
   prm.qjl = qk->kt.qjl16;

@@ -44,7 +44,8 @@ struct PagedParams {
   const float2 *knorms, *vnorms;
   int bf16;  // queries and output: bf16, else fp16
   float scale;
-  uint16_t ck[16], cv[16];  // fp16 centroids
+  uint16_t ck[16], cv[16];  // fp16 centroids, in units of kunit and vunit
+  float kunit, vunit;
   float ckf[16], cvf[16];   // the same in fp32
   const uint32_t *kdiag, *vdiag;
   const uint16_t *qjl;  // d x d fp16 (inner-product keys)

@@ -39,11 +39,12 @@ constexpr int kLutBytes = 256 * 256;
 
 // Shapes of a variant with NQ groups of 8 query rows.  As many warps as the
 // registers allow: 16 of 128; two groups' accumulators at d = 128 need 168 (12
-// warps), with the projections' operands 255 (8).
+// warps), with the projections' operands 255 (8), and so do three groups'
+// (d = 64).
 template <int D, bool IP, int WK, int WV, int NQ>
 struct Shape {
   static constexpr int kRows = 8 * NQ;
-  static constexpr int kWarps = NQ == 1 || D == 64 ? 16 : IP ? 8 : 12;
+  static constexpr int kWarps = NQ == 1 || (D == 64 && NQ == 2) ? 16 : IP || NQ == 3 ? 8 : 12;
   static constexpr int kThreads = 32 * kWarps;
   // one warp's stage of the ring: the packed rows of kBlock keys
   static constexpr int kRowK = WK * D / 8, kRowV = WV * D / 8, kRowS = IP ? D / 8 : 0;  // bytes of a packed row
@@ -56,10 +57,11 @@ struct Shape {
   // both sides of it: in what is left of the first 64 KB (the first kLow bytes
   // of the dynamic memory, which starts below kStart: 1 KB that the system has
   // and this kernel's static arrays), and behind the table, where the
-  // queries (y~ and its low terms, and p, of 16 rows) come first.
+  // queries (y~, its low terms, and p) come first.
   static constexpr int kStart = 4096, kLow = 65536 - kStart;
   static constexpr int kLdq = D + 8;  // elements: 16-byte pieces of 8 rows fall into different banks
-  static constexpr int kQuery = 16 * kLdq * 2 * (IP ? 3 : 1);
+  static constexpr int kQueryRows = kRows < 16 ? 16 : (kRows + 15) / 16 * 16;  // whole tiles of the projection's MMA
+  static constexpr int kQuery = kQueryRows * kLdq * 2 * (IP ? 3 : 2);
   static constexpr int kLdo = D + 4;                        // floats: accumulators of a warp fall into different banks
   static constexpr int kMerge = kWarps * kRows * kLdo * 4;  // the warps' outputs, over queries and ring
   static constexpr int kHigh = 232448 + 1024 - 131072 - kQuery;  // bytes behind them
@@ -150,6 +152,13 @@ __device__ __forceinline__ uint32_t lookup(uint32_t word, uint32_t lane4) {
   asm("ld.shared.b32 %0, [%1+%2];" : "=r"(v) : "r"(sm100::prmt(word, lane4, 0x6504u | (I << 4))), "n"(AT));
   return v;
 }
+// The same, not to be merged with an earlier one (whose result would have to be kept)
+template <int I>
+__device__ __forceinline__ uint32_t lookup_again(uint32_t word, uint32_t lane4) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(sm100::prmt(word, lane4, 0x6504u | (I << 4))));
+  return v;
+}
 
 template <int D, bool IP, int WK, int WV, int NQ>
 __global__ void __launch_bounds__((Shape<D, IP, WK, WV, NQ>::kThreads), 1)
@@ -163,14 +172,14 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
   extern __shared__ __align__(256) uint8_t smem[];
   const uint32_t start = sm100::smem_u32(smem);
   uint8_t *lut = smem + (65536 - start);
-  uint16_t *yh = reinterpret_cast<uint16_t *>(lut + kLutBytes);  // [16][LDQ], then the low terms, and p
-  uint16_t *yl = yh + 16 * LDQ, *ph = yl + 16 * LDQ;
+  uint16_t *yh = reinterpret_cast<uint16_t *>(lut + kLutBytes);  // [kQueryRows][LDQ], then the low terms, and p
+  uint16_t *yl = yh + ST::kQueryRows * LDQ, *ph = yl + ST::kQueryRows * LDQ;
   uint8_t *tail = lut + kLutBytes + ST::kQuery;
   __shared__ int64_t s_run[5];
   __shared__ int s_some;
-  __shared__ float s_f[2][16];  // factors of the scaled queries y~ and p
-  __shared__ int s_pmax[16];
-  __shared__ float s_psum[16];
+  __shared__ float s_f[2][ST::kQueryRows];  // factors of the scaled queries y~ and p
+  __shared__ int s_pmax[ST::kQueryRows];
+  __shared__ float s_psum[ST::kQueryRows];
   __shared__ uint16_t s_c[32];
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_v[kWarps];
 
@@ -220,6 +229,11 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
   __syncthreads();
   if (!s_some) return;
   const uint32_t lane4 = lane * 4 | 1u << 8;
+  // fp16 results are precise enough to show the rounding of the rotated
+  // queries to fp16: their low terms are multiplied too, from shared memory.
+  // (Not by the variant of 8 rows at d = 128, which the code alone made 5 %
+  // slower: fp16 queries take the one of 16 rows there.)
+  const bool low = !p.bf16;
   Cursor cur = start_run(p, p.few, s_run);
 
   for (;;) {
@@ -284,7 +298,7 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
 
     // ---- queries: y~ = R y, scaled by a power of two to below 1 as fp16; for
     // inner-product keys also p = S y~ on the tensor cores (y~ as two fp16 terms)
-    if (IP && tid < 16) s_pmax[tid] = 0;
+    if (IP && tid < ST::kQueryRows) s_pmax[tid] = 0;
 #pragma unroll
     for (int i = warp; i < kRows; i += kWarps) {
       float v[D / 32];
@@ -307,50 +321,59 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
         const float x = v[e] * down;
         const __half hi = __float2half_rn(x);
         yh[i * LDQ + lane * (D / 32) + e] = __half_as_ushort(hi);
-        if (IP) yl[i * LDQ + lane * (D / 32) + e] = __half_as_ushort(__float2half_rn(x - __half2float(hi)));
+        yl[i * LDQ + lane * (D / 32) + e] = __half_as_ushort(__float2half_rn(x - __half2float(hi)));
       }
     }
     __syncthreads();
     if constexpr (IP) {
       // p[row][i] = sum_j S[i][j] y~[row][j]
-      float acc[PT][4];
+      constexpr int RT = ST::kQueryRows / 16;
+      float acc[RT][PT][4];
       if (warp < D / 8) {
 #pragma unroll
-        for (int t = 0; t < PT; ++t)
+        for (int u = 0; u < RT; ++u) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+          for (int t = 0; t < PT; ++t)
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+            for (int e = 0; e < 4; ++e) acc[u][t][e] = 0.f;
 #pragma unroll
-          for (int term = 0; term < 2; ++term) {
-            const uint32_t *ya = reinterpret_cast<const uint32_t *>((term ? yl : yh) + r * LDQ + 16 * k) + c;
-            const uint32_t a[4] = {ya[0], ya[8 * (LDQ / 2)], ya[4], ya[8 * (LDQ / 2) + 4]};
+          for (int k = 0; k < KS; ++k)
 #pragma unroll
-            for (int t = 0; t < PT; ++t) mma16816(acc[t], a, sb[t][k][0], sb[t][k][1]);
-          }
-        float top[2] = {0.f, 0.f};
+            for (int term = 0; term < 2; ++term) {
+              const uint32_t *ya =
+                  reinterpret_cast<const uint32_t *>((term ? yl : yh) + (16 * u + r) * LDQ + 16 * k) + c;
+              const uint32_t a[4] = {ya[0], ya[8 * (LDQ / 2)], ya[4], ya[8 * (LDQ / 2) + 4]};
 #pragma unroll
-        for (int t = 0; t < PT; ++t)
+              for (int t = 0; t < PT; ++t) mma16816(acc[u][t], a, sb[t][k][0], sb[t][k][1]);
+            }
+          float top[2] = {0.f, 0.f};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], fabsf(acc[t][e]));
+          for (int t = 0; t < PT; ++t)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) atomicMax(&s_pmax[r + 8 * h], __float_as_int(top[h]));  // non-negative floats
+            for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], fabsf(acc[u][t][e]));
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            atomicMax(&s_pmax[16 * u + r + 8 * h], __float_as_int(top[h]));  // non-negative floats
+        }
       }
       __syncthreads();
       if (warp < D / 8) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float up = pow2_above(__int_as_float(s_pmax[r + 8 * h])), down = 1.0f / up;
-          if (warp == 0 && c == 0) s_f[1][r + 8 * h] = up * s_f[0][r + 8 * h];
+        for (int u = 0; u < RT; ++u)
 #pragma unroll
-          for (int t = 0; t < PT; ++t)
+          for (int h = 0; h < 2; ++h) {
+            const int i = 16 * u + r + 8 * h;
+            const float up = pow2_above(__int_as_float(s_pmax[i])), down = 1.0f / up;
+            if (warp == 0 && c == 0) s_f[1][i] = up * s_f[0][i];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int j = (warp + t * kWarps) * 8 + 2 * c + e, b = j % 32;  // coordinates k and k + 16 side by side
-              ph[(r + 8 * h) * LDQ + j / 32 * 32 + (b < 16 ? 2 * b : 2 * (b - 16) + 1)] =
-                  __half_as_ushort(__float2half_rn(acc[t][2 * h + e] * down));
-            }
-        }
+            for (int t = 0; t < PT; ++t)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int j = (warp + t * kWarps) * 8 + 2 * c + e, b = j % 32;  // coordinates k and k + 16 side by side
+                ph[i * LDQ + j / 32 * 32 + (b < 16 ? 2 * b : 2 * (b - 16) + 1)] =
+                    __half_as_ushort(__float2half_rn(acc[u][t][2 * h + e] * down));
+              }
+          }
       }
       __syncthreads();
 #pragma unroll
@@ -364,26 +387,32 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
       }
       __syncthreads();
     }
+    // the four operand registers of nibble word `w` of this lane, from a row of queries
+    auto word_of = [&](const uint16_t *row, int w, uint32_t(&v)[4]) {
+      const uint16_t *y = row + 32 * (D == 128 ? c : c >> 1);
+      const int J = (D == 128 ? 0 : 2 * (c & 1)) + w;
+      if constexpr (WK != 1) {  // eight neighbours
+        const uint4 x = *reinterpret_cast<const uint4 *>(y + 8 * J);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] = y[nibble_coord<WK>(J, 2 * e)] | (uint32_t)y[nibble_coord<WK>(J, 2 * e + 1)] << 16;
+      }
+    };
     // the B operands (column r: query row r of a group of 8): step k of a lane
     // pairs the coordinates of its nibble word k / 2, bytes 2 (k % 2) and
     // 2 (k % 2) + 1, as the keys' operands do
     uint32_t qb[NQ][KS][2], pb[IP ? NQ : 1][IP ? KS : 1][2];
     {
-      const int grp = D == 128 ? c : c >> 1, jo = D == 128 ? 0 : 2 * (c & 1);
+      const int grp = D == 128 ? c : c >> 1;
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
 #pragma unroll
         for (int k = 0; k < KS; k += 2) {  // a nibble word
-          const uint16_t *y = yh + (8 * q + r) * LDQ + 32 * grp;
-          const int J = jo + (k >> 1);
-          if constexpr (WK != 1) {  // eight neighbours
-            const uint4 v = *reinterpret_cast<const uint4 *>(y + 8 * J);
-            qb[q][k][0] = v.x, qb[q][k][1] = v.y, qb[q][k + 1][0] = v.z, qb[q][k + 1][1] = v.w;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              qb[q][k + (e >> 1)][e & 1] = y[nibble_coord<WK>(J, 2 * e)] | (uint32_t)y[nibble_coord<WK>(J, 2 * e + 1)] << 16;
-          }
+          uint32_t v4[4];
+          word_of(yh + (8 * q + r) * LDQ, k >> 1, v4);
+          qb[q][k][0] = v4[0], qb[q][k][1] = v4[1], qb[q][k + 1][0] = v4[2], qb[q][k + 1][1] = v4[3];
           if constexpr (IP) {
             // sign bits i and i + 16 of the lane's word, i = 2 k .. 2 k + 3, times 2^15 over the value of the keys'
             // bit (see there): exact, p is below 1
@@ -407,7 +436,7 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int i = 8 * q + 2 * c + e, row = row0 + i;
-        fy[q][e] = s_f[0][i] * (p.scale * 1.4426950408889634f);
+        fy[q][e] = s_f[0][i] * (p.scale * 1.4426950408889634f * p.kunit);
         // <p, +-1> = 2 <p, bits> - sum p, and the bits' product comes 2^-9 too small
         fp[q][e] = IP ? s_f[1][i] * (p.scale * 1.4426950408889634f * p.kappa) : 0.f;
         pc[q][e] = IP ? -s_psum[i] * fp[q][e] : 0.f;
@@ -467,6 +496,28 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
             else
               mma16816(acc[q], a, qb[q][2 * w][0], qb[q][2 * w][1]);
             mma16816(acc[q], b, qb[q][2 * w + 1][0], qb[q][2 * w + 1][1]);
+            if (D == 64 && low) {
+              uint32_t l[4];
+              word_of(yl + (8 * q + r) * LDQ, w, l);
+              mma16816(acc[q], a, l[0], l[1]);
+              mma16816(acc[q], b, l[2], l[3]);
+            }
+          }
+        }
+        if (D == 128 && NQ > 1 && low) {  // (with lookups of its own, which cost the others less)
+#pragma unroll
+          for (int w = 0; w < NW; ++w) {
+            const uint32_t a[4] = {lookup_again<0>(word[0][w], lane4), lookup_again<0>(word[1][w], lane4),
+                                   lookup_again<1>(word[0][w], lane4), lookup_again<1>(word[1][w], lane4)};
+            const uint32_t b[4] = {lookup_again<2>(word[0][w], lane4), lookup_again<2>(word[1][w], lane4),
+                                   lookup_again<3>(word[0][w], lane4), lookup_again<3>(word[1][w], lane4)};
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+              uint32_t l[4];
+              word_of(yl + (8 * q + r) * LDQ, w, l);
+              mma16816(acc[q], a, l[0], l[1]);
+              mma16816(acc[q], b, l[2], l[3]);
+            }
           }
         }
         if constexpr (IP) {
@@ -652,7 +703,7 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
         if (s_l[w][i] != 0.f) {  // the row sees some of the warp's keys
           L += f * s_l[w][i];
 #pragma unroll
-          for (int e = 0; e < D / 32; ++e) v[e] += f * s_v[w] * so[(w * kRows + i) * LDO + lane * (D / 32) + e];
+          for (int e = 0; e < D / 32; ++e) v[e] += f * (s_v[w] * p.vunit) * so[(w * kRows + i) * LDO + lane * (D / 32) + e];
         }
       }
       float *to;
@@ -692,6 +743,9 @@ tq_status launch_rows(const PagedParams &prm, cudaStream_t st) {
 
 template <int D, bool IP, int WK, int WV>
 tq_status launch_rows_nq(const PagedParams &prm, cudaStream_t st) {
+  if constexpr (D == 64) {
+    if (prm.few.rows == 24) return launch_rows<D, IP, WK, WV, 3>(prm, st);
+  }
   return prm.few.rows == 8 ? launch_rows<D, IP, WK, WV, 1>(prm, st) : launch_rows<D, IP, WK, WV, 2>(prm, st);
 }
 
