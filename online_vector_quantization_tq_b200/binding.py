@@ -151,6 +151,13 @@ class Encoded:
         return self
 
 
+def _packed(name: str, t: torch.Tensor, dtype, shape: tuple):
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {shape} (got {t.dtype} {tuple(t.shape)})")
+    if not t.is_contiguous() and t.numel():
+        raise ValueError(f"{name} must be contiguous (got strides {t.stride()})")
+
+
 @dataclass
 class PagedCache:
     """Packed rows of a cache's keys, or of its values, in pages (include/tq.h:
@@ -164,16 +171,11 @@ class PagedCache:
         writes whole rows of q's quantizer."""
         if self.codes.dim() != 4:
             raise ValueError(f"PagedCache.codes must have 4 dimensions (got {self.codes.dim()})")
-        lead = tuple(self.codes.shape[:3])
-        for name, t, dtype, row in (("codes", self.codes, torch.uint8, q.code_bytes),
-                                    ("signs", self.signs, torch.uint8, q.sign_bytes),
-                                    ("norms", self.norms, torch.float32, 2)):
-            if t is None and row == 0:
-                continue
-            if t.dtype != dtype or tuple(t.shape) != lead + (row,):
-                raise ValueError(f"PagedCache.{name} must be {dtype} {lead + (row,)} (got {t.dtype} {tuple(t.shape)})")
-            if t.numel() and not t.is_contiguous():
-                raise ValueError(f"PagedCache.{name} must be contiguous (got strides {t.stride()})")
+        lead = self.codes.shape[:3]
+        _packed("PagedCache.codes", self.codes, torch.uint8, (*lead, q.code_bytes))
+        if q.sign_bytes or self.signs is not None:
+            _packed("PagedCache.signs", self.signs, torch.uint8, (*lead, q.sign_bytes))
+        _packed("PagedCache.norms", self.norms, torch.float32, (*lead, 2))
         return self
 
 
@@ -392,12 +394,39 @@ def _dtype16(x: torch.Tensor) -> int:
 
 def _ld_rows(x: torch.Tensor) -> int:
     """_ld, but a single row's stride (which torch leaves open) does not count."""
-    ld = _ld(x)
-    return ld if x.shape[0] > 1 else x.shape[1]
+    if x.shape[0] == 1 and x.dim() == 2:
+        if x.stride(1) == 1 or x.shape[1] <= 1:
+            return x.shape[1]
+    return _ld(x)
 
 
 def _rows(t) -> _Rows:
-    return _Rows(t.codes.data_ptr(), 0 if t.signs is None else t.signs.data_ptr(), t.norms.data_ptr())
+    signs = t.signs
+    return _Rows(t.codes.data_ptr(), 0 if signs is None else signs.data_ptr(), t.norms.data_ptr())
+
+
+def _one_device(q: Quantizer, names: str, *tensors) -> int:
+    """The device of the tensors (None among them passes), which has to be a
+    CUDA device, the same for all that are not empty, and the quantizer's."""
+    found = -1
+    for i, t in enumerate(tensors):
+        if t is None:
+            continue
+        dev = t.get_device()
+        if dev != found and t.numel():
+            if dev < 0 or found >= 0:
+                raise ValueError(f"{names.split()[i]} must be a CUDA tensor" + (f" of device {found}" if found >= 0 else ""))
+            found = dev
+    if found >= 0 and found != q.device_index and q.device_index >= 0:
+        raise ValueError(f"the tensors are on device {found}, the quantizer on device {q.device_index}")
+    return found
+
+
+def _raw_stream(stream, device: int):
+    """`stream`, or the current one of the tensors' device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device) if device >= 0 else None
 
 
 def _vector(t: torch.Tensor, dtype, name: str, length: int | None = None) -> torch.Tensor:
@@ -408,20 +437,16 @@ def _vector(t: torch.Tensor, dtype, name: str, length: int | None = None) -> tor
     return t
 
 
-def _cuda(**tensors):
-    for name, t in tensors.items():
-        if t is not None and t.numel() and not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-
-
 def _check_caches(qk: Quantizer, qv: Quantizer, kcache: PagedCache, vcache: PagedCache):
     """(npages, kv_heads, page_size) that both arrays agree on."""
     kcache.check(qk)
     vcache.check(qv)
-    if kcache.codes.shape[:3] != vcache.codes.shape[:3]:
+    lead = kcache.codes.shape[:3]
+    if lead != vcache.codes.shape[:3]:
         raise ValueError("kcache and vcache must have the same pages, KV heads and page size")
-    _cuda(kcache=kcache.codes, vcache=vcache.codes)
-    return kcache.codes.shape[:3]
+    if kcache.codes.get_device() < 0 and kcache.codes.numel():
+        raise ValueError("kcache must be CUDA tensors")
+    return lead
 
 
 def tq_attend_prompt(q: Quantizer, y: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -431,25 +456,26 @@ def tq_attend_prompt(q: Quantizer, y: torch.Tensor, k: torch.Tensor, v: torch.Te
     will do), sequence i the tokens cu_seqlens[i] to cu_seqlens[i+1] (int32).
     q, any quantizer, gives d and the device.  Rows of out for tokens of no
     sequence are not written."""
-    total = y.shape[0]
-    if y.dim() != 2 or k.dim() != 2 or k.shape != v.shape or k.shape[0] != total:
+    if y.dim() != 2 or k.dim() != 2 or k.shape != v.shape or k.shape[0] != y.shape[0]:
         raise ValueError("y, k and v must be 2-D with the same tokens, k and v of one shape")
-    if k.shape[1] == 0 or k.shape[1] % q.d != 0 or y.shape[1] == 0 or y.shape[1] % k.shape[1] != 0:
-        raise ValueError(f"y must have a whole number of heads of {q.d} for each KV head of k and v")
-    if k.dtype != y.dtype or v.dtype != y.dtype:
+    (total, wide), narrow, d, dtype = y.shape, k.shape[1], q.d, y.dtype
+    if narrow == 0 or narrow % d != 0 or wide == 0 or wide % narrow != 0:
+        raise ValueError(f"y must have a whole number of heads of {d} for each KV head of k and v")
+    if k.dtype != dtype or v.dtype != dtype:
         raise TypeError("y, k and v must have one type")
     _vector(cu_seqlens, torch.int32, "cu_seqlens")
-    if cu_seqlens.numel() < 1:
+    nseq = cu_seqlens.shape[0] - 1
+    if nseq < 0:
         raise ValueError("cu_seqlens must have one entry more than there are sequences")
     if out is None:
-        out = torch.empty((total, y.shape[1]), dtype=y.dtype, device=y.device)
-    elif out.dtype != y.dtype or out.shape != y.shape:
+        out = torch.empty_like(y, memory_format=torch.contiguous_format)
+    elif out.dtype != dtype or out.shape != y.shape:
         raise ValueError("out must have y's shape and type")
-    _cuda(y=y, k=k, v=v, cu_seqlens=cu_seqlens, out=out)
+    device = _one_device(q, "y k v cu_seqlens out", y, k, v, cu_seqlens, out)
     _check("tq_attend_prompt", lib().tq_attend_prompt(
-        q.handle, _dtype16(y), _ptr(y), _ld_rows(y), _ptr(k), _ld_rows(k), _ptr(v), _ld_rows(v), total,
-        _ptr(cu_seqlens), cu_seqlens.numel() - 1, y.shape[1] // q.d, k.shape[1] // q.d, float(scale), _ptr(out),
-        _ld_rows(out), _stream(stream)))
+        q.handle, _dtype16(y), y.data_ptr(), _ld_rows(y), k.data_ptr(), _ld_rows(k), v.data_ptr(), _ld_rows(v), total,
+        cu_seqlens.data_ptr(), nseq, wide // d, narrow // d, scale, out.data_ptr(), _ld_rows(out),
+        _raw_stream(stream, device)))
     return out
 
 
@@ -460,16 +486,20 @@ def tq_paged_store(qk: Quantizer, qv: Quantizer, kenc: Encoded, venc: Encoded, s
     offset (int64; a slot outside the cache stores nothing)."""
     npages, kv_heads, page_size = _check_caches(qk, qv, kcache, vcache)
     _vector(slots, torch.int64, "slots")
-    tokens = slots.numel()
+    tokens = slots.shape[0]
+    n = tokens * kv_heads
     for q, e, name in ((qk, kenc, "kenc"), (qv, venc, "venc")):
-        e.check()
-        want = (tokens * kv_heads, q.code_bytes)
-        if tuple(e.codes.shape) != want or e.norms.shape[0] != want[0] or (q.m and e.signs.shape[0] != want[0]):
-            raise ValueError(f"{name} must have {want[0]} rows of {want[1]} code bytes (got {tuple(e.codes.shape)})")
-    _cuda(kenc=kenc.codes, venc=venc.codes, slots=slots)
+        _packed(name + ".codes", e.codes, torch.uint8, (n, q.code_bytes))
+        if q.sign_bytes:
+            _packed(name + ".signs", e.signs, torch.uint8, (n, q.sign_bytes))
+        _packed(name + ".norms", e.norms, torch.float32, (n, 2))
+    device = _one_device(qk, "slots kenc.codes kenc.norms venc.codes venc.norms kcache.codes kcache.norms vcache.codes "
+                             "vcache.norms kenc.signs kcache.signs venc.signs vcache.signs", slots, kenc.codes,
+                         kenc.norms, venc.codes, venc.norms, kcache.codes, kcache.norms, vcache.codes, vcache.norms,
+                         kenc.signs, kcache.signs, venc.signs, vcache.signs)
     _check("tq_paged_store", lib().tq_paged_store(
-        qk.handle, qv.handle, _rows(kenc), _rows(venc), _ptr(slots), tokens, kv_heads, _rows(kcache), _rows(vcache),
-        npages, page_size, _stream(stream)))
+        qk.handle, qv.handle, _rows(kenc), _rows(venc), slots.data_ptr(), tokens, kv_heads, _rows(kcache),
+        _rows(vcache), npages, page_size, _raw_stream(stream, device)))
 
 
 def attend_paged_workspace(qk: Quantizer, qv: Quantizer, total_q: int, nseq: int, heads: int, kv_heads: int,
@@ -487,28 +517,32 @@ def tq_attend_paged(qk: Quantizer, qv: Quantizer, y: torch.Tensor, q_start: torc
     (at most max_new), its pages page_table[i], its keys kv_len[i] (the new
     tokens' last among them)."""
     npages, kv_heads, page_size = _check_caches(qk, qv, kcache, vcache)
-    total_q, ldy = y.shape[0], _ld_rows(y)
-    if y.shape[1] % (qk.d * kv_heads) != 0:
-        raise ValueError(f"y must have a whole number of heads of {qk.d} for each of {kv_heads} KV heads")
-    heads = y.shape[1] // qk.d
-    nseq = kv_len.numel()
-    _vector(q_start, torch.int32, "q_start", nseq + 1)
+    ldy, d = _ld_rows(y), qk.d
+    total_q, wide = y.shape
+    if wide % (d * kv_heads) != 0:
+        raise ValueError(f"y must have a whole number of heads of {d} for each of {kv_heads} KV heads")
+    heads = wide // d
     _vector(kv_len, torch.int32, "kv_len")
+    nseq = kv_len.shape[0]
+    _vector(q_start, torch.int32, "q_start", nseq + 1)
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != nseq:
         raise TypeError(f"page_table must be an int32 tensor of {nseq} rows")
     if out is None:
-        out = torch.empty((total_q, y.shape[1]), dtype=y.dtype, device=y.device)
+        out = torch.empty_like(y, memory_format=torch.contiguous_format)
     elif out.dtype != y.dtype or out.shape != y.shape:
         raise ValueError("out must have y's shape and type")
     max_pages = page_table.shape[1]
     if workspace is None:
         workspace = attend_paged_workspace(qk, qv, total_q, nseq, heads, kv_heads, max_new, max_pages, page_size,
                                            y.device)
-    _cuda(y=y, q_start=q_start, page_table=page_table, kv_len=kv_len, out=out, workspace=workspace)
+    device = _one_device(qk, "y q_start kv_len page_table out workspace kcache.codes kcache.norms vcache.codes "
+                             "vcache.norms kcache.signs", y, q_start, kv_len, page_table, out, workspace, kcache.codes,
+                         kcache.norms, vcache.codes, vcache.norms, kcache.signs)
     _check("tq_attend_paged", lib().tq_attend_paged(
-        qk.handle, qv.handle, _dtype16(y), _ptr(y), ldy, total_q, _ptr(q_start), nseq, max_new, heads, kv_heads,
-        _rows(kcache), _rows(vcache), npages, page_size, _ptr(page_table), _ld_rows(page_table), max_pages, _ptr(kv_len),
-        float(scale), _ptr(out), _ld_rows(out), _ptr(workspace), workspace.numel(), _stream(stream)))
+        qk.handle, qv.handle, _dtype16(y), y.data_ptr(), ldy, total_q, q_start.data_ptr(), nseq, max_new, heads,
+        kv_heads, _rows(kcache), _rows(vcache), npages, page_size, page_table.data_ptr(), _ld_rows(page_table),
+        max_pages, kv_len.data_ptr(), scale, out.data_ptr(), _ld_rows(out), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _raw_stream(stream, device)))
     return out
 
 

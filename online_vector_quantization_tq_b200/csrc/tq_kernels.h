@@ -1,6 +1,7 @@
 // Internal kernel entry points of libtq (called by the C ABI in tq_api.cu).
 #pragma once
 
+#include <atomic>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
@@ -64,6 +65,20 @@ size_t attend_ws_bytes(int64_t groups, int64_t G, int d, int64_t nkeys);
 tq_status attend_launch(const tq_quantizer *qv, const float *logits, int64_t ldl, int64_t groups, int64_t G,
                         float scale, const void *vcodes, const float *vnorms, int64_t kpg, int64_t key_base,
                         int64_t nkeys, float *out, int64_t ldo, void *ws, size_t ws_bytes, cudaStream_t st);
+// What a kernel needs set once per device before its first launch (calls that
+// cost as much as a launch): `set` runs until it has succeeded on the current
+// device.
+template <typename F>
+tq_status once_per_device(std::atomic<uint64_t> &done, F set) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return TQ_ERR_CUDA;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return TQ_OK;
+  if (!set()) return TQ_ERR_CUDA;
+  done.fetch_or(bit, std::memory_order_release);
+  return TQ_OK;
+}
+
 // attention of whole prompts on raw queries, keys and values
 struct PromptArgs {
   tq_dtype dtype;

@@ -15,6 +15,7 @@
 // once, the output is rotated back once, and in between every packed row is
 // read once and expanded into fp16 MMA operands in registers.
 #include <algorithm>
+#include <atomic>
 
 #include "tq_kernels.h"
 #include "tq_paged.cuh"
@@ -30,36 +31,89 @@ using namespace paged;
 struct StoreArray {
   const uint8_t *src;
   uint8_t *dst;
-  int row;  // bytes of a row, a multiple of 4 (0: absent)
+  int row;   // bytes of a row, a multiple of 4
+  int size;  // bytes of a piece: 16, 8 or 4, dividing the row and aligned at both ends
 };
 struct StoreParams {
   StoreArray a[6];  // codes, signs, norms of the keys, then of the values
+  int arrays, pieces;  // pieces of a token, over all arrays and heads
   const int64_t *slots;
   int64_t tokens, slots_total;  // npages * page_size
   int kv_heads, page_size;
-  int words;  // 32-bit words of all six rows together
 };
 
-// One thread moves one 32-bit word of one (token, head): the six rows of a
-// (token, head) are neighbours in the index, so a warp reads whole rows.
-__global__ void __launch_bounds__(256) k_paged_store(const StoreParams p) {
-  const int64_t n = p.tokens * p.kv_heads * p.words;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t row = i / p.words;  // token * kv_heads + head
-    int w = (int)(i - row * p.words);
-    const int64_t token = row / p.kv_heads;
-    const int head = (int)(row - token * p.kv_heads);
-    const int64_t slot = p.slots[token];
-    if (slot < 0 || slot >= p.slots_total) continue;
-    const int64_t page = slot / p.page_size;
-    const int64_t to = (page * p.kv_heads + head) * p.page_size + (slot - page * p.page_size);
+constexpr int kStorePieces = 4;  // of a lane and token
+
+// A warp takes a token at a time, its lanes the same pieces of every token (up
+// to 16 bytes of a row each), so that where a piece lies within a token's rows
+// is found once; blockIdx.y takes further pieces of the same tokens.  Bound by
+// DRAM (16384 tokens of 8 heads: see the comment at the launch), and for few
+// tokens by one chain of loads.
+__global__ void __launch_bounds__(256) k_paged_store(const __grid_constant__ StoreParams p) {
+  const int lane = threadIdx.x & 31;
+  const uint8_t *src[kStorePieces];
+  uint8_t *dst[kStorePieces];
+  int row[kStorePieces], size[kStorePieces];
+#pragma unroll
+  for (int i = 0; i < kStorePieces; ++i) {
+    int n = (blockIdx.y * kStorePieces + i) * 32 + lane;
+    size[i] = row[i] = 0;
+    src[i] = nullptr;
+    dst[i] = nullptr;
 #pragma unroll
     for (int k = 0; k < 6; ++k) {
-      const int rw = p.a[k].row >> 2;
-      if (w >= 0 && w < rw)
-        reinterpret_cast<uint32_t *>(p.a[k].dst + to * p.a[k].row)[w] =
-            __ldg(reinterpret_cast<const uint32_t *>(p.a[k].src + row * p.a[k].row) + w);
-      w -= rw;
+      if (k >= p.arrays) break;
+      const int per = p.a[k].row / p.a[k].size, all = per * p.kv_heads;
+      if (n >= 0 && n < all) {
+        const int head = n / per, at = (n - head * per) * p.a[k].size;
+        size[i] = p.a[k].size;
+        row[i] = p.a[k].row;
+        src[i] = p.a[k].src + (int64_t)head * p.a[k].row + at;
+        dst[i] = p.a[k].dst + (int64_t)head * p.page_size * p.a[k].row + at;
+      }
+      n -= all;
+    }
+  }
+  const int64_t warps = (int64_t)gridDim.x * 8;
+  // two tokens in flight
+  for (int64_t token = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); token < p.tokens; token += 2 * warps) {
+    int64_t slot[2];
+    uint4 v[2][kStorePieces];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      slot[u] = token + u * warps < p.tokens ? __ldg(p.slots + token + u * warps) : -1;
+      if (slot[u] >= p.slots_total) slot[u] = -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (slot[u] < 0) continue;
+      const int64_t from = (token + u * warps) * p.kv_heads;
+#pragma unroll
+      for (int i = 0; i < kStorePieces; ++i) {
+        const uint8_t *s = src[i] + from * row[i];
+        if (size[i] == 16)
+          v[u][i] = __ldg(reinterpret_cast<const uint4 *>(s));
+        else if (size[i] == 8)
+          *reinterpret_cast<uint2 *>(&v[u][i]) = __ldg(reinterpret_cast<const uint2 *>(s));
+        else if (size[i] == 4)
+          v[u][i].x = __ldg(reinterpret_cast<const uint32_t *>(s));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (slot[u] < 0) continue;
+      const int64_t page = divide(slot[u], p.page_size);
+      const int64_t to = (page * p.kv_heads - page) * p.page_size + slot[u];  // page * heads * page_size + offset
+#pragma unroll
+      for (int i = 0; i < kStorePieces; ++i) {
+        uint8_t *d = dst[i] + to * row[i];
+        if (size[i] == 16)
+          *reinterpret_cast<uint4 *>(d) = v[u][i];
+        else if (size[i] == 8)
+          *reinterpret_cast<uint2 *>(d) = *reinterpret_cast<const uint2 *>(&v[u][i]);
+        else if (size[i] == 4)
+          *reinterpret_cast<uint32_t *>(d) = v[u][i].x;
+      }
     }
   }
 }
@@ -411,10 +465,14 @@ __global__ void __launch_bounds__(128) k_attend_paged_join(const __grid_constant
 }
 
 int device_sms() {
+  static std::atomic<int> known[64];
   int dev = 0, sms = 0;
   cudaGetDevice(&dev);
+  if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms > 0 ? sms : 1;
+  if (sms < 1) sms = 1;
+  if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
 }
 
 // Sequences of more rows go to the kernel of many rows, whose blocks of 128
@@ -503,8 +561,11 @@ tq_status paged_store_launch(const tq_quantizer *qk, const tq_quantizer *qv, con
     const void *src[3] = {from[i]->codes, from[i]->signs, from[i]->norms};
     void *dst[3] = {to[i]->codes, to[i]->signs, to[i]->norms};
     for (int k = 0; k < 3; ++k) {
-      p.a[3 * i + k] = {static_cast<const uint8_t *>(src[k]), static_cast<uint8_t *>(dst[k]), row[k]};
-      p.words += row[k] / 4;
+      if (row[k] == 0) continue;
+      int size = 16;  // (the cache's arrays are 16-byte aligned)
+      while (row[k] % size != 0 || reinterpret_cast<uintptr_t>(src[k]) % size != 0) size /= 2;
+      p.a[p.arrays++] = {static_cast<const uint8_t *>(src[k]), static_cast<uint8_t *>(dst[k]), row[k], size};
+      p.pieces += row[k] / size * kv_heads;
     }
   }
   p.slots = slots;
@@ -512,9 +573,10 @@ tq_status paged_store_launch(const tq_quantizer *qk, const tq_quantizer *qv, con
   p.slots_total = npages * page_size;
   p.kv_heads = kv_heads;
   p.page_size = page_size;
-  const int64_t n = tokens * kv_heads * p.words;
-  const int64_t blocks = std::min<int64_t>((n + 255) / 256, 8 * (int64_t)device_sms());
-  k_paged_store<<<(unsigned)blocks, 256, 0, st>>>(p);
+  const int64_t blocks = std::min<int64_t>((tokens + 7) / 8, 8 * (int64_t)device_sms());
+  const dim3 grid((unsigned)blocks, (unsigned)((p.pieces + 32 * kStorePieces - 1) / (32 * kStorePieces)));
+  if (grid.y > 65535) return TQ_ERR_TOO_LARGE;
+  k_paged_store<<<grid, 256, 0, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 

@@ -733,10 +733,17 @@ tq_status launch_rows(const PagedParams &prm, cudaStream_t st) {
   using ST = Shape<D, IP, WK, WV, NQ>;
   auto kern = k_attend_paged<D, IP, WK, WV, NQ>;
   // dynamic memory starts behind the system's 1 KB and the kernel's static arrays (the kernel checks)
-  cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return TQ_ERR_CUDA;
-  const int smem = ST::kEnd - 1024 - (int)fa.sharedSizeBytes;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return TQ_ERR_CUDA;
+  static std::atomic<uint64_t> ready{0};
+  static std::atomic<int> dynamic{0};
+  const tq_status rc = once_per_device(ready, [&] {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return false;
+    const int n = ST::kEnd - 1024 - (int)fa.sharedSizeBytes;
+    dynamic.store(n);
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, n) == cudaSuccess;
+  });
+  if (rc != TQ_OK) return rc;
+  const int smem = dynamic.load();
   kern<<<(unsigned)prm.few.grid, ST::kThreads, smem, st>>>(prm);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }

@@ -620,12 +620,14 @@ tq_status launch_tiles(const PagedParams &prm, cudaStream_t st) {
   auto kern = k_attend_paged_tiles<D, IP, WK, WV>;
   constexpr int smem = TileSmem<D, IP>::kBytes;
   static_assert(smem <= 232448 - 8192, "shared memory");
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return TQ_ERR_CUDA;
-  // a split beyond what the block holds would wait for ever
-  cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess ||
-      fa.numRegs * kTilesThreads < 128 * (2 * kSoftmaxRegs + 2 * kExpandRegs + kMmaRegs))
-    return TQ_ERR_CUDA;
+  static std::atomic<uint64_t> ready{0};
+  const tq_status rc = once_per_device(ready, [&] {
+    cudaFuncAttributes fa;  // (a split of registers beyond what the block holds would wait for ever)
+    return cudaFuncGetAttributes(&fa, kern) == cudaSuccess &&
+           fa.numRegs * kTilesThreads >= 128 * (2 * kSoftmaxRegs + 2 * kExpandRegs + kMmaRegs) &&
+           cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
+  });
+  if (rc != TQ_OK) return rc;
   kern<<<(unsigned)prm.many.grid, kTilesThreads, smem, st>>>(prm);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }

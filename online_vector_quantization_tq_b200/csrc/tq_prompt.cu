@@ -455,12 +455,14 @@ tq_status launch_prompt(const PromptArgs &a, int *err, cudaStream_t st) {
   if (blocks > 0x7fffffff) return TQ_ERR_TOO_LARGE;
   auto kern = k_attend_prompt<D, BF16>;
   constexpr int smem = PromptSmem<D>::kBytes;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return TQ_ERR_CUDA;
-  // a split beyond what the block holds would wait for ever
-  cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess ||
-      fa.numRegs * kPromptThreads < 128 * (2 * kSoftmaxRegs + kOtherRegs))
-    return TQ_ERR_CUDA;
+  static std::atomic<uint64_t> ready{0};
+  const tq_status rc = once_per_device(ready, [&] {
+    cudaFuncAttributes fa;  // (a split of registers beyond what the block holds would wait for ever)
+    return cudaFuncGetAttributes(&fa, kern) == cudaSuccess &&
+           fa.numRegs * kPromptThreads >= 128 * (2 * kSoftmaxRegs + kOtherRegs) &&
+           cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
+  });
+  if (rc != TQ_OK) return rc;
   kern<<<(unsigned)blocks, kPromptThreads, smem, st>>>(mq, mk, mv, p);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
