@@ -413,7 +413,7 @@ def _one_device(q: Quantizer, names: str, *tensors) -> int:
         if t is None:
             continue
         dev = t.get_device()
-        if dev != found and t.numel():
+        if (dev != found or dev < 0) and t.numel():
             if dev < 0 or found >= 0:
                 raise ValueError(f"{names.split()[i]} must be a CUDA tensor" + (f" of device {found}" if found >= 0 else ""))
             found = dev

@@ -344,3 +344,73 @@ def test_argument_checks(tq):
     none = torch.empty(0, 1024, dtype=torch.bfloat16, device="cuda")
     assert tq.tq_attend_paged(qk, qv, none, torch.zeros(1, dtype=torch.int32, device="cuda"), kc, vc, table[:0],
                               lens[:0], 1, 0.1).shape == (0, 1024)
+
+
+@pytest.mark.parametrize("d,kb,ip,vb", [(128, 4, False, 4), (128, 3, True, 3), (128, 2, True, 4), (128, 1, False, 2),
+                                        (64, 4, True, 4), (64, 3, False, 3), (64, 1, False, 2), (64, 2, True, 2)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_every_block_height(tq, d, kb, ip, vb, dtype):
+    """Calls of up to 8, 16, 24 and 32 rows a sequence and KV head, in both
+    types (fp16 queries keep their low terms)."""
+    for n, group in ((1, 7), (2, 8), (5, 4), (3, 8), (4, 8)):
+        run_case(tq, d, kb, ip, vb, 2, group, 16, [(n, 333), (n, n), (1, 70), (0, 5), (n, n + 64)], dtype,
+                 seed=d + 7 * n + group, q_scale=3.0)
+
+
+def test_fp16_results_are_as_good_as_their_type(tq):
+    """With sharp heads, where the rounding of the rotated queries to fp16 would
+    show: the error against fp64 stays below 2^-11 of the result (its own
+    rounding among it), 2-norm over 2-norm."""
+    d, n, heads = 128, 2000, 16
+    rng = np.random.default_rng(31)
+    (qk, tk), (qv, tv) = quantizer(tq, d, 4, False), quantizer(tq, d, 4, False, seed=1)
+    batch = Batch(tq, qk, qv, 1, 16, [n], rng)
+    y = torch.from_numpy(rng.standard_normal((1, heads * d)).astype(np.float32)).half().cuda()
+    out = tq.tq_attend_paged(qk, qv, y, torch.tensor([0, 1], dtype=torch.int32, device="cuda"), *batch.caches,
+                             batch.table_dev, torch.tensor([n], dtype=torch.int32, device="cuda"), 1, 1 / math.sqrt(d))
+    ref, _ = attend(y.double().cpu().numpy().reshape(heads, d), [n] * heads, 1 / math.sqrt(d),
+                    unpack(batch.rows[0][0][0], tk), tk, unpack(batch.rows[1][0][0], tv), tv, "f16")
+    got = out.double().cpu().numpy().reshape(heads, d)
+    assert np.linalg.norm(got - ref) <= 2.0 ** -11 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("kv_heads,shift", [(1, 1), (5, 2), (40, 0), (40, 3)])
+def test_store_of_any_alignment(tq, kv_heads, shift):
+    """Rows that start at any 4-byte boundary (norms: 8), and more heads than
+    one pass of a warp takes."""
+    d, page, tokens = 128, 16, 37
+    rng = np.random.default_rng(kv_heads + shift)
+    qk, qv = quantizer(tq, d, 4, True)[0], quantizer(tq, d, 4, False, seed=1)[0]
+    slots = torch.from_numpy(rng.permutation(5 * page)[:tokens].astype(np.int64)).cuda()
+    encs, caches = [], []
+    for q in (qk, qv):
+        parts = []
+        for p, step in zip(random_rows(q, tokens * kv_heads, rng), (4, 4, 2)):
+            flat = torch.zeros(p.size + 64, dtype=torch.from_numpy(p).dtype, device="cuda")
+            at = flat[step * shift: step * shift + p.size]
+            at.copy_(torch.from_numpy(p).view(-1))
+            parts.append(at.view(p.shape))
+        encs.append(tq.Encoded(*parts))
+        caches.append(q.empty_paged(5, kv_heads, page))
+    tq.tq_paged_store(qk, qv, *encs, slots, *caches)
+    for e, c in zip(encs, caches):
+        for src, dst in ((e.codes, c.codes), (e.signs, c.signs), (e.norms, c.norms)):
+            got = dst[slots // page, :, slots % page].reshape(src.shape)
+            assert torch.equal(got, src)
+
+
+def test_arrays_of_the_wrong_shape_are_refused(tq):
+    """Encoded rows that are narrower than the quantizer's, or of another type."""
+    qk, qv = quantizer(tq, 128, 4, True)[0], quantizer(tq, 128, 4, False, seed=1)[0]
+    kc, vc = qk.empty_paged(2, 1, 16), qv.empty_paged(2, 1, 16)
+    ke, ve = qk.empty_encoded(3), qv.empty_encoded(3)
+    slots = torch.arange(3, device="cuda")
+    tq.tq_paged_store(qk, qv, ke, ve, slots, kc, vc)
+    E = tq.Encoded
+    for bad in (E(ke.codes, ke.signs[:, :8].contiguous(), ke.norms), E(ke.codes, ke.signs, ke.norms[:, :1].contiguous()),
+                E(ke.codes.view(torch.int8), ke.signs, ke.norms), E(ke.codes, ke.signs, ke.norms.half()),
+                E(ke.codes[:2], ke.signs, ke.norms)):
+        with pytest.raises(ValueError):
+            tq.tq_paged_store(qk, qv, bad, ve, slots, kc, vc)
+    with pytest.raises(ValueError):
+        tq.tq_paged_store(qk, qv, ke, ve, slots.cpu(), kc, vc)

@@ -91,3 +91,25 @@ def test_cache_shapes_are_checked(tq):
     with pytest.raises(ValueError):
         tq.tq_paged_store(q, q, tq.Encoded(torch.zeros(2, 48, dtype=torch.uint8), torch.zeros(2, 16, dtype=torch.uint8),
                                            torch.zeros(2, 2)), None, torch.zeros(1, dtype=torch.int64), good, good)
+
+
+def test_host_tensors_are_refused(tq):
+    """Before any launch, wherever among the arguments they stand."""
+    from online_vector_quantization_tq_b200.binding import _one_device
+    q = tq.tq_codebook_host(128, 4)
+    none, some = torch.empty(0), torch.empty(3)
+    assert _one_device(q, "a b", none, None) == -1
+    for tensors in ((some, none), (none, some), (some, some), (None, some)):
+        with pytest.raises(ValueError):
+            _one_device(q, "a b", *tensors)
+
+
+def test_attention_of_host_tensors_is_refused(tq):
+    q, v = tq.tq_codebook_host(128, 4), tq.tq_codebook_mse_host(128, 4)
+    y, cu = torch.zeros(4, 256, dtype=torch.bfloat16), torch.tensor([0, 4], dtype=torch.int32)
+    with pytest.raises(ValueError):
+        tq.tq_attend_prompt(v, y, y, y, cu, 0.1)
+    kc, vc = q.empty_paged(3, 2, 16, device="cpu"), v.empty_paged(3, 2, 16, device="cpu")
+    table, lens = torch.zeros(1, 2, dtype=torch.int32), torch.tensor([4], dtype=torch.int32)
+    with pytest.raises(ValueError):
+        tq.tq_attend_paged(q, v, y, cu, kc, vc, table, lens, 4, 0.1, workspace=torch.empty(64, dtype=torch.uint8))
