@@ -79,6 +79,18 @@ tq_status once_per_device(std::atomic<uint64_t> &done, F set) {
   return TQ_OK;
 }
 
+// SMs of the current device
+inline int current_sms() {
+  static std::atomic<int> known[64];
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (sms < 1) sms = 1;
+  if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
+}
+
 // attention of whole prompts on raw queries, keys and values
 struct PromptArgs {
   tq_dtype dtype;

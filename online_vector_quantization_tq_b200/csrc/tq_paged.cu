@@ -464,17 +464,6 @@ __global__ void __launch_bounds__(128) k_attend_paged_join(const __grid_constant
   write_row<D>(p.out, token * p.ldo + (int64_t)h * D, v, lane, p.bf16);
 }
 
-int device_sms() {
-  static std::atomic<int> known[64];
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (sms < 1) sms = 1;
-  if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
-  return sms;
-}
-
 // Sequences of more rows go to the kernel of many rows, whose blocks of 128
 // or 256 rows cost the same however few of their rows are there.
 constexpr int kFewRows = 32;
@@ -573,7 +562,7 @@ tq_status paged_store_launch(const tq_quantizer *qk, const tq_quantizer *qv, con
   p.slots_total = npages * page_size;
   p.kv_heads = kv_heads;
   p.page_size = page_size;
-  const int64_t blocks = std::min<int64_t>((tokens + 7) / 8, 8 * (int64_t)device_sms());
+  const int64_t blocks = std::min<int64_t>((tokens + 7) / 8, 8 * (int64_t)current_sms());
   const dim3 grid((unsigned)blocks, (unsigned)((p.pieces + 32 * kStorePieces - 1) / (32 * kStorePieces)));
   if (grid.y > 65535) return TQ_ERR_TOO_LARGE;
   k_paged_store<<<grid, 256, 0, st>>>(p);
@@ -587,7 +576,7 @@ bool attend_paged_supported(const tq_quantizer *qk, const tq_quantizer *qv) {
 
 size_t attend_paged_ws_bytes(const tq_quantizer *qk, int64_t total_q, int64_t nseq, int64_t heads, int64_t kv_heads,
                              int64_t max_new) {
-  const int sms = device_sms();
+  const int sms = current_sms();
   return std::max(plan_of(qk, false, total_q, nseq, heads, kv_heads, max_new, sms).total,
                   plan_of(qk, true, total_q, nseq, heads, kv_heads, max_new, sms).total);
 }
@@ -595,7 +584,7 @@ size_t attend_paged_ws_bytes(const tq_quantizer *qk, int64_t total_q, int64_t ns
 tq_status attend_paged_launch(const tq_quantizer *qk, const tq_quantizer *qv, const PagedArgs &a, cudaStream_t st) {
   PagedParams prm{};
   const int64_t group = a.heads / a.kv_heads;
-  const Plan L = plan_of(qk, a.dtype == TQ_F16, a.total_q, a.nseq, a.heads, a.kv_heads, a.max_new, device_sms());
+  const Plan L = plan_of(qk, a.dtype == TQ_F16, a.total_q, a.nseq, a.heads, a.kv_heads, a.max_new, current_sms());
   if (!a.workspace || a.workspace_bytes < L.total) return TQ_ERR_WORKSPACE;
   if (a.total_q * a.heads > 0x7fffffff || a.npages > (int64_t)0xffffffff / (a.kv_heads * a.page_size))
     return TQ_ERR_TOO_LARGE;

@@ -4,23 +4,30 @@
 //
 //   o_t = sum_{j <= t} softmax_j(scale <q_t, k_j>) v_j,  sequence by sequence
 //
-// A block (one per SM: it uses all of TMEM) takes two tiles of 128 query rows
-// of one sequence and KV head.  A row is a (token, query head of the group)
-// pair, so a tile of a group of g heads covers 128 / g tokens (rounded down):
-// with grouped heads a short prompt still fills its tiles, the keys behind the
-// diagonal that a tile computes for nothing are fewer, and each key tile is
-// fetched once for all heads of its group.  The two tiles share the key and
-// value tiles and take turns on the tensor cores: while one tile's logits
-// pass through its softmax warps, the other's products run.
+// A work item is two tiles of 128 query rows of one sequence and KV head.  A
+// row is a (token, query head of the group) pair, so a tile of a group of g
+// heads covers 128 / g tokens (rounded down): with grouped heads a short prompt
+// still fills its tiles, the keys behind the diagonal that a tile computes for
+// nothing are fewer, and each key tile is fetched once for all heads of its
+// group.  The two tiles share the key and value tiles and take turns on the
+// tensor cores: while one tile's logits pass through its softmax warps, the
+// other's products run.
+//
+// One block per SM stays for the whole call (it uses all of TMEM) and takes
+// items in turn, longest first and in alternating order from round to round, so
+// that the blocks' sums come out nearly equal: the number of key tiles grows
+// with the position in the sequence.  Each role goes on to the next item as
+// soon as its part of one is done: the next queries and keys are fetched, and
+// their logits computed, while the last outputs are written.  (A block per item
+// took 332 us instead of 262 on 16 ragged prompts of up to 2011 tokens.)
 //
 //   warps 0-3, 4-7  softmax of tile 0 and 1 (tq_flash.cuh), and their output
-//   warp 8          TMA: queries, then key and value tiles of 128 keys
+//   warp 8          finds the items; TMA: queries, then key and value tiles of
+//                   128 keys
 //   warp 9          tcgen05: S = Q K^T from shared memory, O += P V with P in
 //                   TMEM and V (keys x D) as an MN-major operand
-//   warps 10-11     the tail of a value tile: see guard_values
+//   warps 10-11     look at value tiles before they are used: see guard_values
 //
-// Work is handed out longest first (blocks start in the order of their
-// index): the number of key tiles grows with the position in the sequence.
 // Bound by the tensor cores and, equally, the exponentials.
 #include <algorithm>
 #include <cfloat>
@@ -62,52 +69,79 @@ struct PromptSmem {
   static constexpr int kBytes = kV + kStages * kOne + 1024;
 };
 
-// Item of a block, longest first.  A sequence of n tokens has ceil(n / 256
-// rows) levels; level L sees about L + 1 times the keys of level 0.  Items are
-// ordered by falling level, then sequence, then KV head.  Called by one warp.
-__device__ bool find_item(const PromptParams &p, int64_t index, int &seq, int &level, int &head, int &start, int &n) {
-  const int lane = threadIdx.x & 31;
-  head = (int)(index % p.kv_heads);
-  const int64_t rank = index / p.kv_heads;
-  const int span = 2 * p.tokens;
-  auto length = [&](int i) {
-    const int64_t a = min(max((int64_t)__ldg(p.cu + i), (int64_t)0), p.total);
-    return (int)(min(max((int64_t)__ldg(p.cu + i + 1), a), p.total) - a);
-  };
-  auto at_least = [&](int L) {  // items per head of level >= L
+// The items, longest first.  A sequence of n tokens has ceil(n / span) levels
+// (span: the tokens of two tiles); level L sees about L + 1 times the keys of
+// level 0.  Items are ordered by falling level, then sequence, then KV head.
+// Used by one warp, each lane of which keeps the levels of its sequence if
+// there are no more than 32.
+struct Items {
+  int levels;  // of sequence `lane`
+
+  static __device__ int start_of(const PromptParams &p, int i) {
+    return (int)min(max((int64_t)__ldg(p.cu + i), (int64_t)0), p.total);
+  }
+  static __device__ int length(const PromptParams &p, int i) {
+    const int a = start_of(p, i);
+    return (int)(min(max((int64_t)__ldg(p.cu + i + 1), (int64_t)a), p.total) - a);
+  }
+  static __device__ int levels_of(const PromptParams &p, int i) {
+    const int span = 2 * p.tokens;
+    return i < p.nseq ? (length(p, i) + span - 1) / span : 0;
+  }
+  __device__ int mine(const PromptParams &p, int i0) const {
+    return i0 == 0 ? levels : levels_of(p, i0 + (threadIdx.x & 31));
+  }
+  // items per head of level >= L
+  __device__ int64_t at_least(const PromptParams &p, int L) const {
     int64_t c = 0;
-    for (int i = lane; i < p.nseq; i += 32) c += max(0, (length(i) + span - 1) / span - L);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    for (int i0 = 0; i0 < p.nseq; i0 += 32)
+      c += (int64_t)__reduce_add_sync(0xffffffffu, (unsigned)max(0, mine(p, i0) - L));
     return c;
-  };
-  int top = 0;
-  for (int i = lane; i < p.nseq; i += 32) top = max(top, (length(i) + span - 1) / span);
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (rank >= at_least(0)) return false;
-  int lo = 0, hi = top;  // at_least(lo) > rank >= at_least(hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (at_least(mid) > rank)
-      lo = mid;
-    else
-      hi = mid;
   }
-  level = lo;
-  int64_t left = rank - at_least(lo + 1);  // which of the sequences that have level lo
-  for (int i0 = 0; i0 < p.nseq; i0 += 32) {
-    const bool has = i0 + lane < p.nseq && (length(i0 + lane) + span - 1) / span > lo;
-    const uint32_t m = __ballot_sync(0xffffffffu, has);
-    if (left < __popc(m)) {
-      seq = i0 + __fns(m, 0, (int)left + 1);
-      start = (int)min(max((int64_t)__ldg(p.cu + seq), (int64_t)0), p.total);
-      n = length(seq);
-      return true;
+  // item (level, KV head, first token and length of its sequence); false behind the last
+  __device__ bool find(const PromptParams &p, int64_t index, int4 &item) const {
+    const int64_t rank = index < 0x7fffffff ? (uint32_t)index / (uint32_t)p.kv_heads : index / p.kv_heads;
+    item.y = (int)(index - rank * p.kv_heads);
+    if (rank >= at_least(p, 0)) return false;
+    int lo = 0, hi = 0;  // at_least(lo) > rank >= at_least(hi)
+    for (int i0 = 0; i0 < p.nseq; i0 += 32) hi = max(hi, (int)__reduce_max_sync(0xffffffffu, (unsigned)mine(p, i0)));
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (at_least(p, mid) > rank)
+        lo = mid;
+      else
+        hi = mid;
     }
-    left -= __popc(m);
+    item.x = lo;
+    int64_t left = rank - at_least(p, lo + 1);  // which of the sequences that have level lo
+    for (int i0 = 0; i0 < p.nseq; i0 += 32) {
+      const uint32_t m = __ballot_sync(0xffffffffu, mine(p, i0) > lo);
+      if (left < __popc(m)) {
+        const int seq = i0 + __fns(m, 0, (int)left + 1);
+        item.z = start_of(p, seq);
+        item.w = length(p, seq);
+        return true;
+      }
+      left -= __popc(m);
+    }
+    return false;
   }
-  return false;
-}
+};
+
+// What the roles need to know of an item
+struct Work {
+  int head, start, n;
+  int t0;             // first token, in the sequence
+  int cnt[2], tiles;  // key tiles of the two query tiles (the second may lie behind the end), the larger
+  int tail;           // tiles from here on hold keys that some row does not see
+  __device__ Work(const PromptParams &p, int4 item) : head(item.y), start(item.z), n(item.w) {
+    t0 = item.x * 2 * p.tokens;
+    cnt[0] = (min(t0 + p.tokens, n) + kTile - 1) / kTile;
+    cnt[1] = t0 + p.tokens < n ? (min(t0 + 2 * p.tokens, n) + kTile - 1) / kTile : 0;
+    tiles = max(cnt[0], cnt[1]);
+    tail = (t0 + 1) / kTile;
+  }
+};
 
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar) {
   asm volatile(
@@ -124,10 +158,10 @@ __device__ __forceinline__ bool finite16(uint32_t v) {
 }
 
 // A product with a weight of 0 is a NaN where the value is infinite or NaN.
-// So in the tiles that some row does not see whole, rows behind the end of the
+// So in the tiles that some row of the item does not see whole, rows behind the end of the
 // sequence (another sequence's) are cleared, and values that are not finite
 // are cleared with *bad set; the rows that do see them add them at the end.
-// Rows up to and including `first` are seen by every query row of the block.
+// Rows up to and including `first` are seen by every query row of the item.
 template <int D, bool BF16>
 __device__ void guard_values(uint8_t *tile, int key0, int first, int n, int *bad) {
   const int t = threadIdx.x - 32 * kGuardWarp;
@@ -166,49 +200,40 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
   using SM = PromptSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((0u - sm100::smem_u32(smem_raw)) & 1023u);
-  __shared__ uint64_t q_full[2], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], t_full[kStages],
-      t_ok[kStages], s_full[2], p_full[2], p_half[2];
+  __shared__ uint64_t q_full[2], q_empty[2], k_full[kStages], k_empty[kStages], v_full[kStages], v_ok[kStages],
+      v_empty[kStages], s_full[2], p_half[2], p_full[2], item_full[2], item_empty[2];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_item[5], s_bad;
+  __shared__ int4 s_item[2];  // x < 0: no more
+  // whether an item's values had to be cleared; the guard is at most two items ahead of the softmax
+  __shared__ int s_bad[8];
   __shared__ volatile int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  if (warp == 0) {
-    int seq = 0, level = 0, head = 0, start = 0, n = 0;
-    const bool some = find_item(p, blockIdx.x, seq, level, head, start, n);
-    if (lane == 0) {
-      s_item[0] = some;
-      s_item[1] = level;
-      s_item[2] = head;
-      s_item[3] = start;
-      s_item[4] = n;
-    }
-  } else if (warp == 1 && lane == 0) {
+  if (warp == 0 && lane == 0) {
     for (int i = 0; i < 2; ++i) {
       sm100::mbar_init(&q_full[i], 1);
+      sm100::mbar_init(&q_empty[i], 1);
       sm100::mbar_init(&s_full[i], 1);
-      sm100::mbar_init(&p_full[i], kTile);
       sm100::mbar_init(&p_half[i], kTile);
+      sm100::mbar_init(&p_full[i], kTile);
+      sm100::mbar_init(&item_full[i], 1);
+      sm100::mbar_init(&item_empty[i], 2 * kTile + 64 + 1);
     }
     for (int i = 0; i < kStages; ++i) {
       sm100::mbar_init(&k_full[i], 1);
       sm100::mbar_init(&k_empty[i], 1);
       sm100::mbar_init(&v_full[i], 1);
+      sm100::mbar_init(&v_ok[i], 64);
       sm100::mbar_init(&v_empty[i], 1);
-      sm100::mbar_init(&t_full[i], 1);
-      sm100::mbar_init(&t_ok[i], 64);
     }
+    for (int i = 0; i < 8; ++i) s_bad[i] = 0;
     s_abort = 0;
-    s_bad = 0;
     sm100::fence_barrier_init();
   } else if (warp == kLoadWarp && lane == 0) {
     sm100::prefetch_tmap(&mq);
     sm100::prefetch_tmap(&mk);
     sm100::prefetch_tmap(&mv);
-  }
-  __syncthreads();
-  if (!s_item[0]) return;
-  if (warp == kMmaWarp) {
+  } else if (warp == kMmaWarp) {
     sm100::tmem_alloc(&s_tmem, 512);
     sm100::tmem_relinquish();
   }
@@ -216,156 +241,192 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
   __syncthreads();
   sm100::tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const int head = s_item[2], start = s_item[3], n = s_item[4];
-  const int t0 = s_item[1] * 2 * p.tokens;  // the block's first token
-  // key tiles of the two query tiles (the second may lie behind the end)
-  const int cnt[2] = {(min(t0 + p.tokens, n) + kTile - 1) / kTile,
-                      t0 + p.tokens < n ? (min(t0 + 2 * p.tokens, n) + kTile - 1) / kTile : 0};
-  const int tiles = max(cnt[0], cnt[1]);
-  const int tail = (t0 + 1) / kTile;  // tiles from here on hold keys that some row does not see
+  // The items of the block as its roles take them: item k is in s_item[k & 1];
+  // a tile's position counts the key tiles of all items.
+  auto take = [&](int k, int4 &item) {
+    if (!sm100::mbar_wait_abort(&item_full[k & 1], (uint32_t)((k >> 1) & 1), &s_abort, p.err, 118)) return false;
+    item = s_item[k & 1];
+    sm100::mbar_arrive(&item_empty[k & 1]);
+    return item.x >= 0;
+  };
+  auto phase = [](int pos) { return (uint32_t)((pos / kStages) & 1); };
 
   if (warp >= kLoadWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp == kLoadWarp) {
-    if (lane == 0) {
+    if (warp == kLoadWarp) {
       const uint32_t qbytes = (uint32_t)p.group * p.tokens * 128 * (D / 64);
-      auto load_q = [&](int i) {
-        sm100::mbar_expect_tx(&q_full[i], qbytes);
-        for (int h = 0; h < D / 64; ++h)
-          tma_load_3d(smem + SM::kQ + i * SM::kOne + h * SM::kHalf, &mq, 64 * h, head * p.group,
-                      start + t0 + i * p.tokens, &q_full[i]);
-      };
-      auto load_kv = [&](uint8_t *dst, const CUtensorMap *m, int j, uint64_t *bar) {
-        sm100::mbar_expect_tx(bar, SM::kOne);
-        for (int h = 0; h < D / 64; ++h) tma_load_3d(dst + h * SM::kHalf, m, 64 * h, head, start + j * kTile, bar);
-      };
-      int keys = 0, values = 0;  // copies issued
-      for (int j = 0; j < tiles; ++j) {
-        const int st = j % kStages;
-        const uint32_t ph = (uint32_t)((j / kStages - 1) & 1);
-        if (j >= kStages && !sm100::mbar_wait_abort(&k_empty[st], ph, &s_abort, p.err, 101)) break;
-        load_kv(smem + SM::kK + st * SM::kOne, &mk, j, &k_full[st]);
-        ++keys;
-        if (j == 0) {
-          load_q(0);
-          if (cnt[1]) load_q(1);
+      const Items items{Items::levels_of(p, lane)};
+      int keys = 0, values = 0, queries[2] = {0, 0};  // copies issued
+      for (int k = 0;; ++k) {
+        const int64_t round = (int64_t)k * gridDim.x;
+        int4 item = make_int4(-1, 0, 0, 0);
+        const bool some = items.find(p, round + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x), item);
+        if (!some) item.x = -1;
+        bool ok = true;
+        if (lane == 0) {
+          if (k >= 2) ok = sm100::mbar_wait_abort(&item_empty[k & 1], (uint32_t)(((k >> 1) - 1) & 1), &s_abort, p.err, 119);
+          if (ok) {
+            s_item[k & 1] = item;
+            sm100::mbar_arrive(&item_full[k & 1]);
+          }
+          if (ok && some) {
+            const Work w(p, item);
+            auto load_kv = [&](uint8_t *dst, const CUtensorMap *m, int j, uint64_t *bar) {
+              sm100::mbar_expect_tx(bar, SM::kOne);
+              for (int h = 0; h < D / 64; ++h)
+                tma_load_3d(dst + h * SM::kHalf, m, 64 * h, w.head, w.start + j * kTile, bar);
+            };
+            for (int j = 0; j < w.tiles && ok; ++j) {
+              const int st = keys % kStages;
+              if (keys >= kStages) ok = sm100::mbar_wait_abort(&k_empty[st], phase(keys - kStages), &s_abort, p.err, 101);
+              if (!ok) break;
+              load_kv(smem + SM::kK + st * SM::kOne, &mk, j, &k_full[st]);
+              ++keys;
+              for (int i = 0; i < 2 && j == 0 && ok; ++i) {
+                if (!w.cnt[i]) continue;
+                if (queries[i])
+                  ok = sm100::mbar_wait_abort(&q_empty[i], (uint32_t)((queries[i] - 1) & 1), &s_abort, p.err, 120);
+                if (!ok) break;
+                sm100::mbar_expect_tx(&q_full[i], qbytes);
+                for (int h = 0; h < D / 64; ++h)
+                  tma_load_3d(smem + SM::kQ + i * SM::kOne + h * SM::kHalf, &mq, 64 * h, w.head * p.group,
+                              w.start + w.t0 + i * p.tokens, &q_full[i]);
+                ++queries[i];
+              }
+              if (ok && values >= kStages)
+                ok = sm100::mbar_wait_abort(&v_empty[st], phase(values - kStages), &s_abort, p.err, 102);
+              if (!ok) break;
+              load_kv(smem + SM::kV + st * SM::kOne, &mv, j, &v_full[st]);
+              ++values;
+            }
+          }
         }
-        if (j >= kStages && !sm100::mbar_wait_abort(&v_empty[st], ph, &s_abort, p.err, 102)) break;
-        load_kv(smem + SM::kV + st * SM::kOne, &mv, j, j < tail ? &v_full[st] : &t_full[st]);
-        ++values;
+        if (!some || __shfl_sync(0xffffffffu, (int)ok, 0) == 0) break;
       }
       // no copy is in flight when the block ends, whichever role gave up
-      for (int i = 0; i < kStages; ++i) {
-        const int k = keys - 1 - i, u = values - 1 - i;
-        if (k >= 0) sm100::mbar_wait(&k_full[k % kStages], (uint32_t)((k / kStages) & 1), p.err, 113);
-        if (u >= tail) sm100::mbar_wait(&t_full[u % kStages], (uint32_t)(((u - tail) / kStages) & 1), p.err, 114);
-        if (u >= 0 && u < tail) sm100::mbar_wait(&v_full[u % kStages], (uint32_t)((u / kStages) & 1), p.err, 115);
-        if (keys > 0 && cnt[i]) sm100::mbar_wait(&q_full[i], 0, p.err, 116);
+      if (lane == 0)
+        for (int i = 1; i <= kStages; ++i) {
+          if (keys >= i) sm100::mbar_wait(&k_full[(keys - i) % kStages], phase(keys - i), p.err, 113);
+          if (values >= i) sm100::mbar_wait(&v_full[(values - i) % kStages], phase(values - i), p.err, 114);
+          if (queries[i - 1]) sm100::mbar_wait(&q_full[i - 1], (uint32_t)((queries[i - 1] - 1) & 1), p.err, 116);
+        }
+    } else if (warp == kMmaWarp) {
+      if (sm100::elect_one()) {
+        const uint32_t type = BF16 ? sm100::idesc_bf16_f32(kTile, kTile) : sm100::idesc_f16_f32(kTile, kTile);
+        const uint32_t iqk = type | (p.negative ? 1u << 13 : 0u);  // negate A
+        const uint32_t ipv = (BF16 ? sm100::idesc_bf16_f32(kTile, D) : sm100::idesc_f16_f32(kTile, D)) | (1u << 16);
+        const uint32_t base = sm100::smem_u32(smem);
+        int nq[2] = {0, 0}, np[2] = {0, 0};  // uses of q_full, of p_half and p_full so far
+        bool ok = true;
+        auto logits = [&](int i, int pos, bool last) {
+          // (a step along the operand advances the descriptor's address field, in units of 16 bytes)
+          const uint64_t q = sm100::desc_sw128(base + SM::kQ + i * SM::kOne);
+          const uint64_t k = sm100::desc_sw128(base + SM::kK + (pos % kStages) * SM::kOne);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = ((ks / 4) * SM::kHalf + (ks % 4) * 32) / 16;
+            sm100::mma_f16(tmem + kTile * i, q + off, k + off, iqk, ks != 0);
+          }
+          sm100::mma_commit(&s_full[i]);
+          if (last) sm100::mma_commit(&q_empty[i]);
+        };
+        auto output = [&](int i, int pos, bool fresh) {
+          const uint64_t v = sm100::desc_sw128_mn(base + SM::kV + (pos % kStages) * SM::kOne, SM::kHalf, 1024);
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks) {
+            if (ks == kTile / 32) {  // the weights' second half
+              ok = sm100::mbar_poll_abort(&p_full[i], (uint32_t)(np[i]++ & 1), &s_abort, p.err, 117);
+              if (!ok) return;
+              sm100::tc_fence_after();
+            }
+            sm100::mma_f16_ts(tmem + 2 * kTile + kTile * i, tmem + kTile * i + 8 * ks, v + ks * (2048 / 16), ipv,
+                              !fresh || ks != 0);
+          }
+        };
+        int4 item;
+        for (int k = 0, pos = 0; ok && take(k, item); ++k) {
+          const Work w(p, item);
+          ok = sm100::mbar_poll_abort(&k_full[pos % kStages], phase(pos), &s_abort, p.err, 103);
+          for (int i = 0; i < 2 && ok; ++i)
+            if (w.cnt[i]) {
+              ok = sm100::mbar_poll_abort(&q_full[i], (uint32_t)(nq[i]++ & 1), &s_abort, p.err, 104);
+              if (ok) logits(i, pos, w.cnt[i] == 1);
+            }
+          if (ok) sm100::mma_commit(&k_empty[pos % kStages]);
+          for (int j = 0; j < w.tiles && ok; ++j, ++pos) {
+            bool have_v = false, have_k = false;
+            for (int i = 0; i < 2 && ok; ++i) {
+              if (j >= w.cnt[i]) continue;
+              ok = sm100::mbar_poll_abort(&p_half[i], (uint32_t)(np[i] & 1), &s_abort, p.err, 105);
+              if (ok && !have_v) ok = sm100::mbar_poll_abort(&v_ok[pos % kStages], phase(pos), &s_abort, p.err, 107);
+              have_v = true;
+              if (!ok) break;
+              sm100::tc_fence_after();
+              output(i, pos, j == 0);
+              if (!ok) break;
+              if (j + 1 < w.cnt[i]) {
+                if (!have_k)
+                  ok = sm100::mbar_poll_abort(&k_full[(pos + 1) % kStages], phase(pos + 1), &s_abort, p.err, 108);
+                have_k = true;
+                if (ok) logits(i, pos + 1, j + 2 == w.cnt[i]);
+              } else {
+                sm100::mma_commit(&s_full[i]);  // the tile's output is complete
+              }
+            }
+            if (!ok) break;
+            sm100::mma_commit(&v_empty[pos % kStages]);
+            if (j + 1 < w.tiles) sm100::mma_commit(&k_empty[(pos + 1) % kStages]);
+          }
+        }
       }
-    }
-  } else if (warp == kMmaWarp) {
-    if (sm100::elect_one()) {
-      const uint32_t type = BF16 ? sm100::idesc_bf16_f32(kTile, kTile) : sm100::idesc_f16_f32(kTile, kTile);
-      const uint32_t iqk = type | (p.negative ? 1u << 13 : 0u);  // negate A
-      const uint32_t ipv = (BF16 ? sm100::idesc_bf16_f32(kTile, D) : sm100::idesc_f16_f32(kTile, D)) | (1u << 16);
-      const uint32_t base = sm100::smem_u32(smem);
+    } else {
+      int4 item;
       bool ok = true;
-      auto logits = [&](int i, int j) {
-        // (a step along the operand advances the descriptor's address field, in units of 16 bytes)
-        const uint64_t q = sm100::desc_sw128(base + SM::kQ + i * SM::kOne);
-        const uint64_t k = sm100::desc_sw128(base + SM::kK + (j % kStages) * SM::kOne);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = ((ks / 4) * SM::kHalf + (ks % 4) * 32) / 16;
-          sm100::mma_f16(tmem + kTile * i, q + off, k + off, iqk, ks != 0);
-        }
-        sm100::mma_commit(&s_full[i]);
-      };
-      auto output = [&](int i, int j) {
-        const uint64_t v = sm100::desc_sw128_mn(base + SM::kV + (j % kStages) * SM::kOne, SM::kHalf, 1024);
-#pragma unroll
-        for (int ks = 0; ks < kTile / 16; ++ks) {
-          if (ks == kTile / 32) {
-            ok = sm100::mbar_poll_abort(&p_full[i], (uint32_t)(j & 1), &s_abort, p.err, 117);
-            if (!ok) return;
-            sm100::tc_fence_after();
-          }
-          sm100::mma_f16_ts(tmem + 2 * kTile + kTile * i, tmem + kTile * i + 8 * ks, v + ks * (2048 / 16), ipv,
-                            (j | ks) != 0);
-        }
-      };
-      ok = sm100::mbar_poll_abort(&k_full[0], 0, &s_abort, p.err, 103);
-      for (int i = 0; i < 2 && ok; ++i)
-        if (cnt[i]) {
-          ok = sm100::mbar_poll_abort(&q_full[i], 0, &s_abort, p.err, 104);
-          if (ok) logits(i, 0);
-        }
-      if (ok) sm100::mma_commit(&k_empty[0]);
-      for (int j = 0; j < tiles && ok; ++j) {
-        const int st = j % kStages, nx = (j + 1) % kStages;
-        bool have_v = false, have_k = false;
-        for (int i = 0; i < 2 && ok; ++i) {
-          if (j >= cnt[i]) continue;
-          ok = sm100::mbar_poll_abort(&p_half[i], (uint32_t)(j & 1), &s_abort, p.err, 105);
-          if (ok && !have_v) {
-            ok = j < tail ? sm100::mbar_poll_abort(&v_full[st], (uint32_t)((j / kStages) & 1), &s_abort, p.err, 106)
-                          : sm100::mbar_poll_abort(&t_ok[(j - tail) % kStages], (uint32_t)(((j - tail) / kStages) & 1),
-                                                   &s_abort, p.err, 107);
-            have_v = true;
-          }
+      for (int k = 0, pos = 0; ok && take(k, item); ++k) {
+        const Work w(p, item);
+        if (tid == 32 * kGuardWarp) s_bad[(k + 4) & 7] = 0;
+        for (int j = 0; j < w.tiles; ++j, ++pos) {
+          const int st = pos % kStages;
+          ok = sm100::mbar_wait_abort(&v_full[st], phase(pos), &s_abort, p.err, 109);
           if (!ok) break;
-          sm100::tc_fence_after();
-          output(i, j);
-          if (!ok) break;
-          if (j + 1 < cnt[i]) {
-            if (!have_k) ok = sm100::mbar_poll_abort(&k_full[nx], (uint32_t)(((j + 1) / kStages) & 1), &s_abort, p.err, 108);
-            have_k = true;
-            if (ok) logits(i, j + 1);
-          } else {
-            sm100::mma_commit(&s_full[i]);  // the tile's output is complete
-          }
+          if (j >= w.tail)
+            guard_values<D, BF16>(smem + SM::kV + st * SM::kOne, j * kTile, w.t0, w.n, &s_bad[k & 7]);
+          sm100::mbar_arrive(&v_ok[st]);
         }
-        if (!ok) break;
-        sm100::mma_commit(&v_empty[st]);
-        if (j + 1 < tiles) sm100::mma_commit(&k_empty[nx]);
       }
     }
-  } else if (warp >= kGuardWarp) {
-    // the tail's stage s of t_full is the stage its tile lies in; t_ok counts
-    // tail tiles from 0
-    for (int j = tail; j < tiles; ++j) {
-      const int st = j % kStages, u = j - tail;
-      if (!sm100::mbar_wait_abort(&t_full[st], (uint32_t)((u / kStages) & 1), &s_abort, p.err, 109)) break;
-      guard_values<D, BF16>(smem + SM::kV + st * SM::kOne, j * kTile, t0, n, &s_bad);
-      sm100::mbar_arrive(&t_ok[u % kStages]);
-    }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    if (cnt[warp >> 2]) {
     const int i = warp >> 2, r = tid & (kTile - 1);
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s = tmem + kTile * i + lanes, o = tmem + 2 * kTile + kTile * i + lanes;
-    const int first = t0 + i * p.tokens, token = first + r / p.group;
-    flash::Row row;
+    int ns = 0;  // uses of s_full
+    int4 item;
     bool ok = true;
-    for (int j = 0; j < cnt[i]; ++j) {
-      ok = sm100::mbar_poll_abort(&s_full[i], (uint32_t)(j & 1), &s_abort, p.err, 110);
+    for (int k = 0; ok && take(k, item); ++k) {
+      const Work w(p, item);
+      const int cnt = i ? w.cnt[1] : w.cnt[0];
+      if (!cnt) continue;
+      const int first = w.t0 + i * p.tokens, token = first + r / p.group;
+      flash::Row row;
+      for (int j = 0; j < cnt; ++j) {
+        ok = sm100::mbar_poll_abort(&s_full[i], (uint32_t)(ns++ & 1), &s_abort, p.err, 110);
+        if (!ok) break;
+        sm100::tc_fence_after();
+        if ((j + 1) * kTile > first + 1)
+          flash::softmax_tile<D, BF16, true, 2>(s, o, j == 0, p.mult, token + 1 - j * kTile, row, &p_half[i],
+                                                &p_full[i]);
+        else
+          flash::softmax_tile<D, BF16, false, 2>(s, o, j == 0, p.mult, 0, row, &p_half[i], &p_full[i]);
+      }
+      if (ok) ok = sm100::mbar_poll_abort(&s_full[i], (uint32_t)(ns++ & 1), &s_abort, p.err, 111);
       if (!ok) break;
       sm100::tc_fence_after();
-      if ((j + 1) * kTile > first + 1)
-        flash::softmax_tile<D, BF16, true, 2>(s, o, j == 0, p.mult, token + 1 - j * kTile, row, &p_half[i], &p_full[i]);
-      else
-        flash::softmax_tile<D, BF16, false, 2>(s, o, j == 0, p.mult, 0, row, &p_half[i], &p_full[i]);
-    }
-    if (ok) ok = sm100::mbar_poll_abort(&s_full[i], (uint32_t)(cnt[i] & 1), &s_abort, p.err, 111);
-    if (ok) {
-      sm100::tc_fence_after();
       const float inv = 1.0f / row.sum;
-      const bool mine = r < p.tokens * p.group && token < n;
-      const bool bad = *(volatile int *)&s_bad != 0;
-      uint16_t *to = static_cast<uint16_t *>(p.out) + (int64_t)(start + token) * p.ldo +
-                     (int64_t)(head * p.group + r % p.group) * D;
+      const bool mine = r < p.tokens * p.group && token < w.n;
+      const bool bad = *(volatile int *)&s_bad[k & 7] != 0;
+      uint16_t *to = static_cast<uint16_t *>(p.out) + (int64_t)(w.start + token) * p.ldo +
+                     (int64_t)(w.head * p.group + r % p.group) * D;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t v[32];
@@ -374,28 +435,27 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
         if (!mine) continue;
         float2 *f = reinterpret_cast<float2 *>(v);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) f[k] = flash::mul2(f[k], make_float2(inv, inv));
+        for (int e = 0; e < 16; ++e) f[e] = flash::mul2(f[e], make_float2(inv, inv));
         if (bad) {  // add what guard_values took out, where this row sees it
-          for (int key = t0 + 1; key <= token; ++key) {
-            const uint16_t *vr = p.v + (int64_t)(start + key) * p.ldv + (int64_t)head * D + c;
+          for (int key = w.t0 + 1; key <= token; ++key) {
+            const uint16_t *vr = p.v + (int64_t)(w.start + key) * p.ldv + (int64_t)w.head * D + c;
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const uint32_t b = vr[k];
+            for (int e = 0; e < 32; ++e) {
+              const uint32_t b = vr[e];
               if (!finite16<BF16>(b)) {
-                const float a = BF16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((uint16_t)b));
-                v[k] = __float_as_uint(__uint_as_float(v[k]) + a);
+                const float x = BF16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((uint16_t)b));
+                v[e] = __float_as_uint(__uint_as_float(v[e]) + x);
               }
             }
           }
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<uint4 *>(to + c + 8 * k) =
-              make_uint4(flash::pack16<BF16>(f[4 * k]), flash::pack16<BF16>(f[4 * k + 1]),
-                         flash::pack16<BF16>(f[4 * k + 2]), flash::pack16<BF16>(f[4 * k + 3]));
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint4 *>(to + c + 8 * e) =
+              make_uint4(flash::pack16<BF16>(f[4 * e]), flash::pack16<BF16>(f[4 * e + 1]),
+                         flash::pack16<BF16>(f[4 * e + 2]), flash::pack16<BF16>(f[4 * e + 3]));
       }
     }
-  }
   }
   sm100::tc_fence_before();
   __syncthreads();
@@ -451,8 +511,8 @@ tq_status launch_prompt(const PromptArgs &a, int *err, cudaStream_t st) {
   p.out = a.out;
   p.err = err;
   // at most one started span per sequence beside the whole ones
-  const int64_t blocks = (a.total / (2 * tokens) + std::min(a.nseq, a.total)) * a.kv_heads;
-  if (blocks > 0x7fffffff) return TQ_ERR_TOO_LARGE;
+  const int64_t most = (a.total / (2 * tokens) + std::min(a.nseq, a.total)) * a.kv_heads;
+  const int64_t blocks = std::min<int64_t>(most, current_sms());
   auto kern = k_attend_prompt<D, BF16>;
   constexpr int smem = PromptSmem<D>::kBytes;
   static std::atomic<uint64_t> ready{0};

@@ -254,3 +254,31 @@ def test_argument_checks(tq):
     assert bool((out == 3.0).all())
     none = torch.empty(0, 4 * d, dtype=torch.bfloat16, device="cuda")
     assert tq.tq_attend_prompt(q, none, none[:, : 2 * d], none[:, : 2 * d], cu[:1], 0.1).shape == (0, 4 * d)
+
+
+@pytest.mark.parametrize("d,kv_heads,group", [(64, 8, 1), (128, 8, 2), (64, 5, 7)])
+def test_more_items_than_blocks(tq, d, kv_heads, group):
+    """Several rounds of work items to a block, of one and of two tiles."""
+    run_case(tq, d, kv_heads, group, [1 + (97 * i) % 640 for i in range(24)], "bf16", seed=41 + d)
+
+
+def test_bad_values_among_many_items(tq):
+    """Infinities and NaN in some sequences of a batch that takes several rounds:
+    every other sequence, and every earlier token, keeps its result, bit for bit."""
+    d, heads = 64, 8
+    lens = [(53 * i) % 400 + 1 for i in range(30)]
+    starts = [sum(lens[:i]) for i in range(len(lens) + 1)]
+    y, k, v = make(starts[-1], heads, heads, d, "bf16", 43)
+    cu = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    q = handle(tq, d)
+    clean = tq.tq_attend_prompt(q, y, k, v, cu, 0.125)
+    same = torch.ones(starts[-1], dtype=torch.bool, device="cuda")
+    v2 = v.clone()
+    for i in range(0, 30, 4):
+        at = starts[i] + lens[i] // 2
+        v2[at] = math.nan if i % 8 else math.inf
+        same[at: starts[i + 1]] = False
+    for _ in range(3):
+        out = tq.tq_attend_prompt(q, y, k, v2, cu, 0.125)
+        assert torch.equal(out[same], clean[same])
+        assert not bool(torch.isfinite(out[~same]).any())
