@@ -205,7 +205,8 @@ tq_status tq_attend(const tq_quantizer *qv, const float *logits, int64_t ldl, in
  * products and sums in fp32, the weights rounded to `dtype` (up to 2^8, before
  * the division by their fp32 sum).  What a token does not see does not reach
  * its output, whatever it holds.  Takes no workspace; lengths are read on the
- * device, so a captured call can be replayed with others.
+ * device, so a captured call can be replayed with others.  A bounded wait that
+ * ran out is reported by tq_sync_check(q).
  * total == 0 or nseq == 0: no-op. */
 tq_status tq_attend_prompt(const tq_quantizer *q, tq_dtype dtype, const void *y, int64_t ldy, const void *k,
                            int64_t ldk, const void *v, int64_t ldv, int64_t total,
@@ -271,13 +272,22 @@ tq_status tq_paged_store(const tq_quantizer *qk, const tq_quantizer *qv, const t
  *       share it with another that may run at the same time.
  * out_h = sum_k softmax_k(scale s_hk) v^_k with s_hk the estimate of tq_score
  * (or, without sign bits, <y, x^_k>) and v^_k = ||v_k|| R^T c[codes_k].  The
- * rotated queries, the centroids and the weights are fp16 operands (each
- * rounded to within 2^-11, the queries and weights under a power-of-two
- * scale), products are accumulated in fp32 and the softmax is fp32: out is
- * within about 2^-9 sum_k softmax_k ||v_k|| / sqrt(d) of the exact value per
- * coordinate beside its own rounding, for scaled logits up to about 30.
+ * rotated queries, the centroids (times their norms, for sequences of more
+ * than 32 query rows per KV head) and the weights are fp16 operands (each
+ * rounded to within 2^-11, under power-of-two scales), products are
+ * accumulated in fp32 and the softmax is fp32: out is within about
+ * 2^-9 sum_k softmax_k ||v_k|| / sqrt(d) of the exact value per coordinate
+ * beside its own rounding, for scaled logits up to about 30.  With up to 32
+ * rows the centroids' common factor leaves them within 2^-13 and fp16 queries
+ * keep 22 bits.  Value norms up to 2^100.  A key or value norm that is not
+ * finite makes NaN of the tokens that see it, and of no other.
  * Lengths and tables are read on the device: the call can be captured in a
- * graph and replayed with other values in the same buffers.
+ * graph and replayed with other values in the same buffers.  A bounded wait
+ * that ran out is reported by tq_sync_check(qk).  max_pages*page_size is at
+ * most 2^29, npages*kv_heads*page_size below 2^32, total_q*heads below 2^31.
+ * The workspace holds 4 d bytes per query row (token x head), twice that and
+ * more where max_new rows need the kernel of many rows, and per SM the partial
+ * results of two blocks of rows.
  * nseq == 0, total_q == 0 or max_new == 0: no-op. */
 size_t tq_attend_paged_workspace_bytes(const tq_quantizer *qk, const tq_quantizer *qv, int64_t total_q,
                                        int64_t nseq, int64_t heads, int64_t kv_heads, int64_t max_new,
