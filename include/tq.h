@@ -273,11 +273,11 @@ tq_status tq_paged_store(const tq_quantizer *qk, const tq_quantizer *qv, const t
  * out_h = sum_k softmax_k(scale s_hk) v^_k with s_hk the estimate of tq_score
  * (or, without sign bits, <y, x^_k>) and v^_k = ||v_k|| R^T c[codes_k].  The
  * rotated queries, the centroids (times their norms, for sequences of more
- * than 32 query rows per KV head) and the weights are fp16 operands (each
+ * than 64 query rows per KV head) and the weights are fp16 operands (each
  * rounded to within 2^-11, under power-of-two scales), products are
  * accumulated in fp32 and the softmax is fp32: out is within about
  * 2^-9 sum_k softmax_k ||v_k|| / sqrt(d) of the exact value per coordinate
- * beside its own rounding, for scaled logits up to about 30.  With up to 32
+ * beside its own rounding, for scaled logits up to about 30.  With up to 64
  * rows the centroids' common factor leaves them within 2^-13 and fp16 queries
  * keep 22 bits.  Value norms up to 2^100.  A key or value norm that is not
  * finite makes NaN of the tokens that see it, and of no other.

@@ -151,8 +151,8 @@ __device__ __forceinline__ void hand_over(uint64_t *bar) {
 // One tile of 128 keys: S at `s` -> P over it, handed over by halves (64 keys
 // each) on two barriers.  mult >= 0 turns logits into base-2 exponents.  MASK:
 // the row sees the tile's first `see` keys alone.  PAIRS of eight pairs of
-// exponentials run on the FMA pipe (prompt of 8192 tokens, d = 128, us: 0 1030,
-// 2 968, 3 992, 4 992).  The row's 128 logits stay in registers: reading S
+// exponentials run on the FMA pipe (prompts of 8192 tokens, d = 128: with 2 968
+// us, with 3 or 4 992).  The row's 128 logits stay in registers: reading S
 // twice, 32 columns at a time, took 1040 us instead of 968.
 template <int D, bool BF16, bool MASK, int PAIRS>
 __device__ __forceinline__ void softmax_tile(uint32_t s, uint32_t o, bool first, float mult, int see, Row &row,

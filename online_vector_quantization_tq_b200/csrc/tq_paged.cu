@@ -16,6 +16,8 @@
 // read once and expanded into fp16 MMA operands in registers.
 #include <algorithm>
 #include <atomic>
+#include <cstring>
+#include <type_traits>
 
 #include "tq_kernels.h"
 #include "tq_paged.cuh"
@@ -46,9 +48,9 @@ constexpr int kStorePieces = 4;  // of a lane and token
 
 // A warp takes a token at a time, its lanes the same pieces of every token (up
 // to 16 bytes of a row each), so that where a piece lies within a token's rows
-// is found once; blockIdx.y takes further pieces of the same tokens.  Bound by
-// DRAM (16384 tokens of 8 heads: see the comment at the launch), and for few
-// tokens by one chain of loads.
+// is found once; blockIdx.y takes further pieces of the same tokens.  Bound by the
+// latency of slot, load and store (16384 tokens of 8 heads: 23 us, 1.6 TB/s; by
+// 4-byte words 54 us).
 __global__ void __launch_bounds__(256) k_paged_store(const __grid_constant__ StoreParams p) {
   const int lane = threadIdx.x & 31;
   const uint8_t *src[kStorePieces];
@@ -126,8 +128,8 @@ __global__ void __launch_bounds__(256) k_paged_store(const __grid_constant__ Sto
 // largest coordinate, which goes to qscale.  Coordinates stand where the
 // expansion of packed codes and signs puts them.  One thread a row, 64 rows a
 // block; the projection on the tensor cores, with y~ as two fp16 terms.
-// (16384 rows of d = 128: 6 us, by a warp a row 11 us; 37000 rows with the
-// projection: see the table of rates in the kernel of many rows.)
+// (37000 rows of d = 128 with the projection: 30 us; by a warp a row, 16 rows a
+// block, 115 us.)
 constexpr int kQueryRows = 64;
 
 template <int D, bool IP>
@@ -268,13 +270,14 @@ __device__ __forceinline__ Place place_of(const PagedParams &p, const PagedCut &
 
 // Output rows from the normalized rows of whole blocks, or from the partial
 // results of the runs that share a block (added up in their order), rotated
-// back.  Many rows: a block of threads takes up to 64 rows of one block, whose
-// place it finds once; each warp has four rows in flight.
-constexpr int kJoinRows = 64, kJoinThreads = 256;
+// back.  Many rows: a block of threads takes up to 16 rows of one block, whose
+// place it finds once; each warp has two rows and four runs of each in flight.
+// (64 rows a block, a run at a time: 92 us for 1024 rows of 17 runs each.)
+constexpr int kJoinRows = 16, kJoinThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) k_attend_paged_join_many(const __grid_constant__ PagedParams p) {
-  constexpr int V = D / 32, N = 4, kWarps = kJoinThreads / 32;
+  constexpr int V = D / 32, N = 2, kWarps = kJoinThreads / 32, kRuns = 4;
   __shared__ int s_item[4];  // sequence (-1: none), KV head, block, part
   __shared__ Place s_place;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -343,11 +346,14 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_paged_join_many(const _
 #pragma unroll
       for (int e = 0; e < V; ++e) v[i][e] = 0.f;
     }
+    using Vec = typename std::conditional<D == 128, float4, float2>::type;  // a lane's V floats
+    auto load = [&](const float *row, float (&x)[V]) {
+      const Vec t = __ldg(reinterpret_cast<const Vec *>(row) + lane);
+      memcpy(x, &t, sizeof(t));
+    };
     if (f.seen && f.b0 == f.b1) {
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[i][e] = __ldg(p.whole + out[i] * D + lane * V + e);
+      for (int i = 0; i < N; ++i) load(p.whole + out[i] * D, v[i]);
     } else if (f.seen) {
       float M[N], L[N];
       int64_t in[N];
@@ -357,25 +363,37 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_paged_join_many(const _
         L[i] = 0.f;
         in[i] = s_item[3] * kJoinRows + min(r0 + i * kWarps, rows - 1);
       }
-#pragma unroll 2
-      for (int b = f.b0; b <= f.b1; ++b)
+#pragma unroll 1
+      for (int b = f.b0; b <= f.b1; b += kRuns) {
+        float2 a[kRuns][N];
+        float x[kRuns][N][V];
 #pragma unroll
-        for (int i = 0; i < N; ++i) M[i] = fmaxf(M[i], __ldg(&c.part_ml[f.at(c, b) + in[i]].x));
-#pragma unroll 2
-      for (int b = f.b0; b <= f.b1; ++b) {
+        for (int u = 0; u < kRuns; ++u)
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int64_t at = f.at(c, min(b + u, f.b1)) + in[i];
+            a[u][i] = __ldg(c.part_ml + at);
+            load(c.part_o + at * D, x[u][i]);
+            if (b + u > f.b1) a[u][i] = make_float2(-INFINITY, 0.f);
+          }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const int64_t at = f.at(c, b) + in[i];
-          const float2 a = __ldg(c.part_ml + at);
-          float x[V];
+          float top = M[i];
 #pragma unroll
-          for (int e = 0; e < V; ++e) x[e] = __ldg(c.part_o + at * D + lane * V + e);
-          if (a.y != 0.f) {  // the row sees some of the run's keys
-            const float g = a.x == -INFINITY ? 0.f : ex2(a.x - M[i]);
-            L[i] = fmaf(g, a.y, L[i]);
+          for (int u = 0; u < kRuns; ++u) top = fmaxf(top, a[u][i].x);
+          const float old = M[i] == -INFINITY ? 0.f : ex2(M[i] - top);
+          M[i] = top;
+          L[i] *= old;
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[i][e] = fmaf(g, x[e], v[i][e]);
-          }
+          for (int e = 0; e < V; ++e) v[i][e] *= old;
+#pragma unroll
+          for (int u = 0; u < kRuns; ++u)
+            if (a[u][i].y != 0.f) {  // the row sees some of the run's keys
+              const float g = a[u][i].x == -INFINITY ? 0.f : ex2(a[u][i].x - top);
+              L[i] = fmaf(g, a[u][i].y, L[i]);
+#pragma unroll
+              for (int e = 0; e < V; ++e) v[i][e] = fmaf(g, x[u][i][e], v[i][e]);
+            }
         }
       }
 #pragma unroll
@@ -465,8 +483,11 @@ __global__ void __launch_bounds__(128) k_attend_paged_join(const __grid_constant
 }
 
 // Sequences of more rows go to the kernel of many rows, whose blocks of 128
-// or 256 rows cost the same however few of their rows are there.
-constexpr int kFewRows = 32;
+// or 256 rows cost the same however few of their rows are there (8 sequences
+// of 8000 keys and 8 KV heads, d = 128, us by few / by many: 32 rows 74 / 135,
+// 64 rows 119 / 139, 96 rows 166 / 141; 40 sequences, 64 rows 494 / 520, 96 rows
+// 723 / 532).
+constexpr int kFewRows = 64;
 
 // Sizes of a call and where its pieces lie in the workspace
 struct Plan {
@@ -527,7 +548,7 @@ tq_status launch_paged(const PagedParams &prm, const tq_quantizer *qk, const tq_
   if (prm.many.grid > 0 || rows >= 16 * (int64_t)prm.few.grid) {
     // parts of blocks of rows: at most one that is not whole per sequence and KV head
     const int64_t per = std::min(kJoinRows, prm.few.rows);
-    const int64_t most = prm.kv_heads * (prm.total_q * prm.group / per + prm.nseq * (prm.many.grid > 0 ? 4 : 1));
+    const int64_t most = prm.kv_heads * (prm.total_q * prm.group / per + prm.nseq * (prm.many.grid > 0 ? 16 : 1));
     if (most > 0x7fffffff) return TQ_ERR_TOO_LARGE;
     k_attend_paged_join_many<D><<<(unsigned)most, kJoinThreads, 0, st>>>(prm);
   } else {

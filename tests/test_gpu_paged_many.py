@@ -1,5 +1,5 @@
 """Attention of many new tokens over a paged quantized cache (sequences of more
-than 32 query rows per KV head take a kernel of their own), against plain fp64
+than 64 query rows per KV head take a kernel of their own), against plain fp64
 with bounds from the roundings."""
 import math
 
