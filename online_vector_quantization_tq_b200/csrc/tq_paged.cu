@@ -35,6 +35,7 @@ struct StoreArray {
   uint8_t *dst;
   int row;   // bytes of a row, a multiple of 4
   int size;  // bytes of a piece: 16, 8 or 4, dividing the row and aligned at both ends
+  int all;   // pieces of a token, of all heads
 };
 struct StoreParams {
   StoreArray a[6];  // codes, signs, norms of the keys, then of the values
@@ -45,11 +46,13 @@ struct StoreParams {
 };
 
 constexpr int kStorePieces = 4;  // of a lane and token
+constexpr int kStoreTokens = 2;  // of a warp in flight
+constexpr int kStoreBlocks = 4;  // of an SM (16384 tokens, a launch among others: 17.3 us, with 8 18.4, with 16 22.5)
 
 // A warp takes a token at a time, its lanes the same pieces of every token (up
 // to 16 bytes of a row each), so that where a piece lies within a token's rows
 // is found once; blockIdx.y takes further pieces of the same tokens.  Bound by the
-// latency of slot, load and store (16384 tokens of 8 heads: 23 us, 1.6 TB/s; by
+// latency of slot, load and store (16384 tokens of 8 heads: 17 us with the launch; by
 // 4-byte words 54 us).
 __global__ void __launch_bounds__(256) k_paged_store(const __grid_constant__ StoreParams p) {
   const int lane = threadIdx.x & 31;
@@ -62,32 +65,28 @@ __global__ void __launch_bounds__(256) k_paged_store(const __grid_constant__ Sto
     size[i] = row[i] = 0;
     src[i] = nullptr;
     dst[i] = nullptr;
-#pragma unroll
-    for (int k = 0; k < 6; ++k) {
-      if (k >= p.arrays) break;
-      const int per = p.a[k].row / p.a[k].size, all = per * p.kv_heads;
-      if (n >= 0 && n < all) {
-        const int head = n / per, at = (n - head * per) * p.a[k].size;
-        size[i] = p.a[k].size;
-        row[i] = p.a[k].row;
-        src[i] = p.a[k].src + (int64_t)head * p.a[k].row + at;
-        dst[i] = p.a[k].dst + (int64_t)head * p.page_size * p.a[k].row + at;
-      }
-      n -= all;
+    int k = 0;  // the array of the piece
+    while (k < p.arrays && n >= p.a[k].all) n -= p.a[k++].all;
+    if (k < p.arrays) {
+      const StoreArray a = p.a[k];
+      const int per = a.row / a.size, head = n / per, at = (n - head * per) * a.size;
+      size[i] = a.size;
+      row[i] = a.row;
+      src[i] = a.src + (int64_t)head * a.row + at;
+      dst[i] = a.dst + (int64_t)head * p.page_size * a.row + at;
     }
   }
   const int64_t warps = (int64_t)gridDim.x * 8;
-  // two tokens in flight
-  for (int64_t token = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); token < p.tokens; token += 2 * warps) {
-    int64_t slot[2];
-    uint4 v[2][kStorePieces];
+  for (int64_t token = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); token < p.tokens; token += kStoreTokens * warps) {
+    int64_t slot[kStoreTokens];
+    uint4 v[kStoreTokens][kStorePieces];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kStoreTokens; ++u) {
       slot[u] = token + u * warps < p.tokens ? __ldg(p.slots + token + u * warps) : -1;
       if (slot[u] >= p.slots_total) slot[u] = -1;
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kStoreTokens; ++u) {
       if (slot[u] < 0) continue;
       const int64_t from = (token + u * warps) * p.kv_heads;
 #pragma unroll
@@ -102,7 +101,7 @@ __global__ void __launch_bounds__(256) k_paged_store(const __grid_constant__ Sto
       }
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kStoreTokens; ++u) {
       if (slot[u] < 0) continue;
       const int64_t page = divide(slot[u], p.page_size);
       const int64_t to = (page * p.kv_heads - page) * p.page_size + slot[u];  // page * heads * page_size + offset
@@ -574,8 +573,9 @@ tq_status paged_store_launch(const tq_quantizer *qk, const tq_quantizer *qv, con
       if (row[k] == 0) continue;
       int size = 16;  // (the cache's arrays are 16-byte aligned)
       while (row[k] % size != 0 || reinterpret_cast<uintptr_t>(src[k]) % size != 0) size /= 2;
-      p.a[p.arrays++] = {static_cast<const uint8_t *>(src[k]), static_cast<uint8_t *>(dst[k]), row[k], size};
-      p.pieces += row[k] / size * kv_heads;
+      const int all = row[k] / size * kv_heads;
+      p.a[p.arrays++] = {static_cast<const uint8_t *>(src[k]), static_cast<uint8_t *>(dst[k]), row[k], size, all};
+      p.pieces += all;
     }
   }
   p.slots = slots;
@@ -583,7 +583,7 @@ tq_status paged_store_launch(const tq_quantizer *qk, const tq_quantizer *qv, con
   p.slots_total = npages * page_size;
   p.kv_heads = kv_heads;
   p.page_size = page_size;
-  const int64_t blocks = std::min<int64_t>((tokens + 7) / 8, 8 * (int64_t)current_sms());
+  const int64_t blocks = std::min<int64_t>((tokens + 7) / 8, kStoreBlocks * (int64_t)current_sms());
   const dim3 grid((unsigned)blocks, (unsigned)((p.pieces + 32 * kStorePieces - 1) / (32 * kStorePieces)));
   if (grid.y > 65535) return TQ_ERR_TOO_LARGE;
   k_paged_store<<<grid, 256, 0, st>>>(p);
