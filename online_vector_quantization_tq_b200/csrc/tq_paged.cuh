@@ -191,18 +191,6 @@ __device__ __forceinline__ void thread_rotate(float (&v)[D], const uint32_t *dia
 #pragma unroll
   for (int i = 0; i < D; ++i) v[i] *= f;
 }
-template <int D>
-__device__ __forceinline__ void thread_rotate_back(float (&v)[D], const uint32_t *diag) {
-#pragma unroll 1
-  for (int r = 2; r >= 0; --r) {
-    thread_fwht<D>(v);
-    thread_signs<D>(v, diag + r * (D / 32));
-  }
-  const float f = 1.0f / ((float)D * sqrtf((float)D));
-#pragma unroll
-  for (int i = 0; i < D; ++i) v[i] *= f;
-}
-
 // D/32 consecutive 16-bit values of one row, written by one lane
 template <int D>
 __device__ __forceinline__ void write_row(void *out, int64_t at, const float (&v)[D / 32], int lane, int bf16) {

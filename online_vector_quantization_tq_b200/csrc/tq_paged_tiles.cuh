@@ -120,13 +120,28 @@ __device__ __forceinline__ int tiles_of(const PagedParams &p, const Cursor &cur,
   return min(max((seen + kTile - 1) / kTile - g.t0, 0), g.tiles);
 }
 
-// fp16 centroids of a 32-coordinate group as four 16-byte chunks of row r,
-// from chunk 4 g on
+// The values of a 32-coordinate group as four 16-byte chunks of row r, from
+// chunk 4 g on.  lo, hi: byte tables of the row's values (byte_tables).
+// Four-bit codebooks are symmetric, c[15 - i] = -c[i], and their tables hold the
+// upper eight values alone: a code below 8 selects by its complement and has
+// its sign set, 18 operations for eight codes against 23 with 16-entry tables.
 template <int W>
 __device__ __forceinline__ void expand_group(uint8_t *tile, int r, int g, const uint32_t *words,
                                              const uint32_t (&tlo)[4], const uint32_t (&thi)[4]) {
   uint32_t lo[8], hi[8];
-  expand_codes<W>(words, tlo, thi, lo, hi);
+  if constexpr (W == 4) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t x = words[k], n = ~x & 0x88888888u, up = n << 4;  // n: codes below 8
+      const uint32_t sel = (x ^ (n - (n >> 3))) & 0x77777777u;
+      lo[2 * k] = sm100::prmt(tlo[0], tlo[1], sel);
+      lo[2 * k + 1] = sm100::prmt(tlo[0], tlo[1], sel >> 16);
+      hi[2 * k] = sm100::prmt(thi[0], thi[1], sel) | (sm100::prmt(up, n, 0x5140u) & 0x80808080u);
+      hi[2 * k + 1] = sm100::prmt(thi[0], thi[1], sel >> 16) | (sm100::prmt(up, n, 0x7362u) & 0x80808080u);
+    }
+  } else {
+    expand_codes<W>(words, tlo, thi, lo, hi);
+  }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int chunk = 4 * g + k;
@@ -156,16 +171,19 @@ __device__ __forceinline__ void load_words(uint32_t *w, const uint8_t *from) {
   }
 }
 
-// Byte tables of a row's values: centroids times f, rounded to fp16
+// Byte tables of a row's values: centroids times f, rounded to fp16 (of four-bit
+// codes: the upper eight)
 template <int W>
 __device__ __forceinline__ void byte_tables(const float *c, float f, uint32_t (&lo)[4], uint32_t (&hi)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     lo[i] = hi[i] = 0u;
-    if (4 * i < (1 << W)) {
+    if (4 * i < (W == 4 ? 8 : 1 << W)) {
+      constexpr int kFirst = W == 4 ? 8 : 0;
       const float2 ff = make_float2(f, f);
-      const uint32_t a = flash::pack16<false>(flash::mul2(make_float2(c[4 * i], c[4 * i + 1]), ff));
-      const uint32_t b = flash::pack16<false>(flash::mul2(make_float2(c[4 * i + 2], c[4 * i + 3]), ff));
+      const uint32_t a = flash::pack16<false>(flash::mul2(make_float2(c[kFirst + 4 * i], c[kFirst + 4 * i + 1]), ff));
+      const uint32_t b =
+          flash::pack16<false>(flash::mul2(make_float2(c[kFirst + 4 * i + 2], c[kFirst + 4 * i + 3]), ff));
       lo[i] = sm100::prmt(a, b, 0x6420u);
       hi[i] = sm100::prmt(a, b, 0x7531u);
     }
@@ -526,10 +544,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
         const float m = fminf(fmaxf(mult * s_key[nr], 1.17549435e-38f), 3.402823466e38f), scale = s_value[nr];
         const int end = (g.t0 + j + 1) * kTile;
         if (end > lim_first || (s_gap[nr][0] | s_gap[nr][1] | s_gap[nr][2] | s_gap[nr][3]))
-          flash::softmax_tile_twice<D, true, 2>(S, O, n == 0, m, lim - (end - kTile), st, none, scale, &p_half[i],
+          flash::softmax_tile_twice<D, true, 0>(S, O, n == 0, m, lim - (end - kTile), st, none, scale, &p_half[i],
                                                 &p_full[i]);
         else
-          flash::softmax_tile_twice<D, false, 2>(S, O, n == 0, m, 0, st, none, scale, &p_half[i], &p_full[i]);
+          flash::softmax_tile_twice<D, false, 0>(S, O, n == 0, m, 0, st, none, scale, &p_half[i], &p_full[i]);
       }
       if (ok && cnt) ok = sm100::mbar_poll_abort(&s_full[i], (uint32_t)(ns++ & 1), &s_abort, p.err, 126);
       if (!ok) break;
