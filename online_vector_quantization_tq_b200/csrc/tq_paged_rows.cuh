@@ -230,9 +230,11 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
   if (!s_some) return;
   const uint32_t lane4 = lane * 4 | 1u << 8;
   // fp16 results are precise enough to show the rounding of the rotated
-  // queries to fp16: their low terms are multiplied too, from shared memory.
-  // (Not by the variant of 8 rows at d = 128, which the code alone made 5 %
-  // slower: fp16 queries take the one of 16 rows there.)
+  // queries and of the weights to fp16: their low terms are multiplied too, the
+  // queries' from shared memory.  (Not by the variant of 8 rows at d = 128,
+  // which the code alone made 5 % slower: fp16 queries take the one of 16 rows
+  // there.)
+  constexpr bool kLow = D == 64 || NQ > 1;
   const bool low = !p.bf16;
   Cursor cur = start_run(p, p.few, s_run);
 
@@ -504,7 +506,7 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
             }
           }
         }
-        if (D == 128 && NQ > 1 && low) {  // (with lookups of its own, which cost the others less)
+        if (D == 128 && kLow && low) {  // (with lookups of its own, which cost the others less)
 #pragma unroll
           for (int w = 0; w < NW; ++w) {
             const uint32_t a[4] = {lookup_again<0>(word[0][w], lane4), lookup_again<0>(word[1][w], lane4),
@@ -613,7 +615,7 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
             }
           }
       }
-      uint32_t wb[NQ][2];
+      uint32_t wb[NQ][2], wl[NQ][2];  // weights, and for fp16 results their low terms
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
         float w[2][2];
@@ -628,6 +630,11 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
           const float f = vn[i] * vinv;
           const __half2 h = __floats2half2_rn(w[i][0] * f, w[i][1] * f);
           wb[q][i] = transpose8(*reinterpret_cast<const uint32_t *>(&h));
+          if (kLow && low) {
+            const float2 g = __half22float2(h);
+            const __half2 l = __floats2half2_rn(w[i][0] * f - g.x, w[i][1] * f - g.y);
+            wl[q][i] = transpose8(*reinterpret_cast<const uint32_t *>(&l));
+          }
         }
       }
       // values: lane (r, c) has coordinates of r for keys of c; the nibbles of
@@ -658,7 +665,10 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
 #pragma unroll
         for (int b = 0; b < 4; ++b)
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) mma16816(o[q][4 * w + b], a[b], wb[q][0], wb[q][1]);
+          for (int q = 0; q < NQ; ++q) {
+            mma16816(o[q][4 * w + b], a[b], wb[q][0], wb[q][1]);
+            if (kLow && low) mma16816(o[q][4 * w + b], a[b], wl[q][0], wl[q][1]);
+          }
       }
       __syncwarp();  // the stage is read before the next copy into it is issued
     }
