@@ -545,9 +545,13 @@ tq_status launch_paged(const PagedParams &prm, const tq_quantizer *qk, const tq_
   rc = qk->m ? paged_rows_launch<D, true>(prm, qk->w, qv->w, st) : paged_rows_launch<D, false>(prm, qk->w, qv->w, st);
   if (rc != TQ_OK) return rc;
   if (prm.many.grid > 0 || rows >= 16 * (int64_t)prm.few.grid) {
-    // parts of blocks of rows: at most one that is not whole per sequence and KV head
-    const int64_t per = std::min(kJoinRows, prm.few.rows);
-    const int64_t most = prm.kv_heads * (prm.total_q * prm.group / per + prm.nseq * (prm.many.grid > 0 ? 16 : 1));
+    // parts of blocks of rows: as many as the rows fill, and of one block more per sequence and KV head
+    int64_t most = 0;
+    for (const PagedCut *c : {&prm.few, &prm.many}) {
+      if (c->grid == 0) continue;
+      const int64_t parts = (c->rows + kJoinRows - 1) / kJoinRows;
+      most = std::max(most, prm.kv_heads * (prm.total_q * prm.group * parts / c->rows + prm.nseq * parts));
+    }
     if (most > 0x7fffffff) return TQ_ERR_TOO_LARGE;
     k_attend_paged_join_many<D><<<(unsigned)most, kJoinThreads, 0, st>>>(prm);
   } else {

@@ -414,3 +414,11 @@ def test_arrays_of_the_wrong_shape_are_refused(tq):
             tq.tq_paged_store(qk, qv, bad, ve, slots, kc, vc)
     with pytest.raises(ValueError):
         tq.tq_paged_store(qk, qv, ke, ve, slots.cpu(), kc, vc)
+
+
+@pytest.mark.parametrize("d,group,most", [(64, 4, 5), (64, 8, 2), (128, 4, 4), (64, 4, 2), (128, 16, 4)])
+def test_large_batches_of_unequal_sequences(tq, d, group, most):
+    """Enough rows for the join by blocks of rows, where many sequences have
+    fewer rows than a block has."""
+    seqs = [(most if i % 5 == 0 else i % 2, 20 + 7 * (i % 9)) for i in range(230)]
+    run_case(tq, d, 4, False, 4, 4, group, 16, seqs, "bf16", seed=d + group + most)
