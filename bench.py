@@ -57,9 +57,9 @@ CSRC = os.path.join(ROOT, "online_vector_quantization_tq_b200", "csrc")
 # those sources are unchanged; otherwise the roofline's traffic is null.
 TRAFFIC = {
     # kernel@workload: (source file, digest, bytes per launch, the capture)
-    "k_encode_tc2@kv": ("tq_encode_tc.cu", "9831e14a2c4ee1a7", 326491392, "kv workload, launch 4, ncu --set full"),
-    "k_score_tc@kv": ("tq_score_tc.cu", "29c8a83c49dff57f", 79304448, "kv workload, launch 4, ncu --set full"),
-    "k_attend_split@decode_attend": ("tq_attend.cu", "8a7739e9493e3030", 616206848, "decode_attend workload, launch 3, ncu --set full"),
+    "k_encode_tc2@kv": ("tq_encode_tc.cu", "eb5da97e2a3fa181", 325326080, "kv workload, launch 4, ncu DRAM byte counters"),
+    "k_score_tc@kv": ("tq_score_tc.cu", "7438b71ea7d476b3", 75929344, "kv workload, launch 4, ncu DRAM byte counters"),
+    "k_attend_split@decode_attend": ("tq_attend.cu", "65d9e1af78ce527e", 614371840, "decode_attend workload, launch 3, ncu DRAM byte counters"),
 }
 
 
