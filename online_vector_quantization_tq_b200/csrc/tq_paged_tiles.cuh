@@ -27,6 +27,14 @@
 //   warps 12-15      expand values, one row a thread
 //   warp 16          tcgen05
 //
+// Between the issuing thread and a softmax warpgroup the barriers alternate: a
+// segment's queries (q_full), then per tile its logits (s_full) and its weights
+// (p_half, p_full), at last its output (o_full).  Neither side completes a
+// barrier's next phase before the other has seen the last one: a warpgroup
+// without a tile in a segment neither arrives on q_full nor is waited for, and
+// the output has a barrier of its own, since the next segment's logits may
+// complete s_full before the warpgroup has come to look at the output.
+//
 // Keys and values share one ring of slots (a tile of 16-bit rows, 128-byte
 // swizzle), in the order in which the products first need them.
 #pragma once
@@ -200,7 +208,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((0u - sm100::smem_u32(smem_raw)) & 1023u);
   float *s_none = reinterpret_cast<float *>(smem + SM::kNone);
-  __shared__ uint64_t full[SM::kSlots], empty[SM::kSlots], q_full[2], s_full[2], p_half[2], p_full[2], merge, merged;
+  __shared__ uint64_t full[SM::kSlots], empty[SM::kSlots], q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], merge, merged;
   __shared__ uint32_t s_tmem;
   __shared__ int64_t s_run[5];
   __shared__ int s_some, s_gap[kNorms][4];
@@ -224,6 +232,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
       sm100::mbar_init(&s_full[i], 1);
       sm100::mbar_init(&p_half[i], kTile);
       sm100::mbar_init(&p_full[i], kTile);
+      sm100::mbar_init(&o_full[i], 1);
     }
     sm100::mbar_init(&merge, kTile);
     sm100::mbar_init(&merged, kTile);
@@ -425,7 +434,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
       };
       do {
         const Segment g = segment_of<D, IP>(p, cur);
-      enter(g);
+        enter(g);
         const int cnt[2] = {tiles_of(p, cur, g, 0), tiles_of(p, cur, g, 1)};
         auto logits = [&](int i, int j) {  // S_i = Q K_j^T
           // (a step along the operand advances the descriptor's address field, in units of 16 bytes)
@@ -467,7 +476,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
         };
         auto free_value = [&](int j) { sm100::mma_commit(&empty[(ring.value(j)) % SM::kSlots]); };
         for (int i = 0; i < (g.turns ? 1 : 2) && ok; ++i)
-          ok = sm100::mbar_poll_abort(&q_full[i], (uint32_t)(nq[i]++ & 1), &s_abort, p.err, 124);
+          if (cnt[i]) ok = sm100::mbar_poll_abort(&q_full[i], (uint32_t)(nq[i]++ & 1), &s_abort, p.err, 124);
         sm100::tc_fence_after();
         if (g.turns) {
           for (int j = 0; j < 2 && j < g.tiles && ok; ++j) {
@@ -481,7 +490,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
               logits(j & 1, j + 2);
               if (ok) free_keys(j + 2);
             } else if (ok) {
-              sm100::mma_commit(&s_full[j & 1]);  // the warpgroup's output is complete
+              sm100::mma_commit(&o_full[j & 1]);  // the warpgroup's output is complete
             }
           }
         } else {
@@ -495,7 +504,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
               if (ok && j + 1 < cnt[i])
                 logits(i, j + 1);
               else if (ok)
-                sm100::mma_commit(&s_full[i]);
+                sm100::mma_commit(&o_full[i]);
             }
             if (ok) free_value(j);
             if (ok && j + 1 < g.tiles) free_keys(j + 1);
@@ -510,7 +519,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t S = tmem + kTile * i + lanes, O = tmem + 2 * kTile + kTile * i + lanes;
     const float unit = fabsf(p.scale) * 1.4426950408889634f;
-    int ns = 0, nm = 0;  // uses of s_full, of merge
+    int ns = 0, no = 0, nm = 0;  // uses of s_full, of o_full, of merge
     bool ok = true;
     do {
       const Segment g = segment_of<D, IP>(p, cur);
@@ -521,7 +530,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
       const int64_t at = (int64_t)(cur.s.start + (mine ? row / p.group : 0)) * p.heads + cur.head * p.group +
                          (mine ? row % p.group : 0);
       const float mult = (mine ? __ldg(p.qscale + at) : 1.f) * unit;
-      if (i == 0 || !g.turns) {
+      if (cnt && (i == 0 || !g.turns)) {
         uint8_t *q = smem + SM::kQ + i * SM::kQTile;
         const uint4 *from = reinterpret_cast<const uint4 *>(p.qprep + at * DQ);
 #pragma unroll 8
@@ -549,7 +558,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
         else
           flash::softmax_tile_twice<D, false, 0>(S, O, n == 0, m, 0, st, none, scale, &p_half[i], &p_full[i]);
       }
-      if (ok && cnt) ok = sm100::mbar_poll_abort(&s_full[i], (uint32_t)(ns++ & 1), &s_abort, p.err, 126);
+      if (ok && cnt) ok = sm100::mbar_poll_abort(&o_full[i], (uint32_t)(no++ & 1), &s_abort, p.err, 126);
       if (!ok) break;
       sm100::tc_fence_after();
       float M = st.sum != 0.f ? st.ref : -INFINITY, L = st.sum, f0 = 0.f, f1 = 0.f;
