@@ -28,6 +28,9 @@
 //                   TMEM and V (keys x D) as an MN-major operand
 //   warps 10-11     look at value tiles before they are used: see guard_values
 //
+// A tile's output has a barrier of its own (o_full): the next item's logits may
+// complete s_full before the softmax has come to look at the output.
+//
 // Bound by the tensor cores and, equally, the exponentials.
 #include <algorithm>
 #include <cfloat>
@@ -201,7 +204,7 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((0u - sm100::smem_u32(smem_raw)) & 1023u);
   __shared__ uint64_t q_full[2], q_empty[2], k_full[kStages], k_empty[kStages], v_full[kStages], v_ok[kStages],
-      v_empty[kStages], s_full[2], p_half[2], p_full[2], item_full[2], item_empty[2];
+      v_empty[kStages], s_full[2], p_half[2], p_full[2], o_full[2], item_full[2], item_empty[2];
   __shared__ uint32_t s_tmem;
   __shared__ int4 s_item[2];  // x < 0: no more
   // whether an item's values had to be cleared; the guard is at most two items ahead of the softmax
@@ -216,6 +219,7 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       sm100::mbar_init(&s_full[i], 1);
       sm100::mbar_init(&p_half[i], kTile);
       sm100::mbar_init(&p_full[i], kTile);
+      sm100::mbar_init(&o_full[i], 1);
       sm100::mbar_init(&item_full[i], 1);
       sm100::mbar_init(&item_empty[i], 2 * kTile + 64 + 1);
     }
@@ -370,7 +374,7 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
                 have_k = true;
                 if (ok) logits(i, pos + 1, j + 2 == w.cnt[i]);
               } else {
-                sm100::mma_commit(&s_full[i]);  // the tile's output is complete
+                sm100::mma_commit(&o_full[i]);  // the tile's output is complete
               }
             }
             if (!ok) break;
@@ -400,7 +404,7 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
     const int i = warp >> 2, r = tid & (kTile - 1);
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s = tmem + kTile * i + lanes, o = tmem + 2 * kTile + kTile * i + lanes;
-    int ns = 0;  // uses of s_full
+    int ns = 0, no = 0;  // uses of s_full, of o_full
     int4 item;
     bool ok = true;
     for (int k = 0; ok && take(k, item); ++k) {
@@ -419,7 +423,7 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
         else
           flash::softmax_tile<D, BF16, false, 2>(s, o, j == 0, p.mult, 0, row, &p_half[i], &p_full[i]);
       }
-      if (ok) ok = sm100::mbar_poll_abort(&s_full[i], (uint32_t)(ns++ & 1), &s_abort, p.err, 111);
+      if (ok) ok = sm100::mbar_poll_abort(&o_full[i], (uint32_t)(no++ & 1), &s_abort, p.err, 111);
       if (!ok) break;
       sm100::tc_fence_after();
       const float inv = 1.0f / row.sum;
