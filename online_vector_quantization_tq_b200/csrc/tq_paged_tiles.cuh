@@ -267,8 +267,11 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
              sm100::mbar_wait_abort(&empty[at % SM::kSlots], (uint32_t)((at / SM::kSlots - 1) & 1), &s_abort, p.err, 121);
     };
     // Largest of a norm over the warpgroup's threads, put down before `agree`
-    // and read behind it, alternately in two places.  agree: whether any of the
-    // threads gave up (they have to leave together).
+    // and read behind it, alternately in two places (a turn is the tile's number
+    // in the run: were it counted anew in each segment, the last tile of one and
+    // the first of the next could share a place, with no barrier between the
+    // read and the write).  agree: whether any of the threads gave up (they have
+    // to leave together).
     auto put_top = [&](int what, int turn, float v) {
       v = finite_or_0(v);  // not below 0: ordered as an integer
       const int top = __reduce_max_sync(0xffffffffu, __float_as_int(v));
@@ -335,12 +338,12 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
           const int at = ring.key(j), nr = (ring.before + j) % kNorms;
           const bool gap = __any_sync(0xffffffffu, n.x < 0.f);
           const float none = n.x < 0.f ? -1.f : 0.f;
-          put_top(0, j, fmaxf(n.x, 0.f));
-          put_top(1, j, v);
+          put_top(0, ring.before + j, fmaxf(n.x, 0.f));
+          put_top(1, ring.before + j, v);
           ok = agree(wait_slot(at));
           if (!ok) break;
-          const float e = flash::exponent_above(top_of(0, j));
-          exponent = fmaxf(exponent, flash::exponent_above(top_of(1, j)));
+          const float e = flash::exponent_above(top_of(0, ring.before + j));
+          exponent = fmaxf(exponent, flash::exponent_above(top_of(1, ring.before + j)));
           // a value that is not finite makes a NaN of every row that sees its key, and of no other
           const float f = fabsf(v) < INFINITY ? fmaxf(n.x, 0.f) * flash::ex2(-e) + 0.f * n.x : NAN;
           byte_tables<WK>(p.ckf, f, tlo, thi);
@@ -402,10 +405,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
           const int64_t row = pg >= 0 ? row_of(j + 1, pg) : 0;
           page = page_of(j + 2);
           const int at = ring.value(j);
-          put_top(2, j, v);
+          put_top(2, ring.before + j, v);
           ok = agree(wait_slot(at));
           if (!ok) break;
-          exponent = fmaxf(exponent, flash::exponent_above(top_of(2, j)));  // (as the keys' threads find it)
+          exponent = fmaxf(exponent, flash::exponent_above(top_of(2, ring.before + j)));  // (as the keys' threads find it)
           byte_tables<WV>(p.cvf, finite_or_0(v) * flash::ex2(-exponent), tlo, thi);
           uint8_t *slot = smem + SM::kRing + (at % SM::kSlots) * SM::kSlot;
 #pragma unroll
