@@ -260,8 +260,9 @@ tq_status tq_paged_store(const tq_quantizer *qk, const tq_quantizer *qv, const t
  *       are left out), any of them possibly none.  Tokens of no sequence, and
  *       those at or behind total_q, are left as they were in out.
  *   kv_len: device int32 [nseq]; the sequence's keys, its new tokens (already
- *       stored) the last of them: new token j of n sees the first
- *       kv_len - n + j + 1 keys.  A token that sees none gets zeros.
+ *       stored) the last of them: new token j of n = q_start[i+1] - q_start[i]
+ *       sees the first kv_len - n + j + 1 keys (n counts the tokens that
+ *       max_new or total_q leaves out too).  A token that sees none gets zeros.
  *   page_table: device int32, sequence i's pages in order at
  *       page_table + i*ldt, max_pages entries (keys that lie beyond are not
  *       attended).  Only the entries that kv_len needs are read; an entry

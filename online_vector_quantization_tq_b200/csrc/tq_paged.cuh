@@ -205,17 +205,20 @@ __device__ __forceinline__ void write_row(void *out, int64_t at, const float (&v
 }
 
 struct Seq {
-  int start, n, len;  // first query token, new tokens, keys that can be read
-  int kv;             // keys by kv_len (the causal limit counts from it)
+  int start, n, len;  // first query token, new tokens (at most max_new), keys that can be read
+  // keys that the first new token sees, by kv_len and all new tokens of the
+  // sequence, those that max_new or total_q leaves out among them; may be below 1
+  int first;
 };
 __device__ __forceinline__ Seq seq_of(const PagedParams &p, int i) {
   Seq s;
   const int64_t a = min(max((int64_t)__ldg(p.q_start + i), (int64_t)0), p.total_q);
-  const int64_t b = min(max((int64_t)__ldg(p.q_start + i + 1), a), p.total_q);
+  const int64_t end = __ldg(p.q_start + i + 1), b = min(max(end, a), p.total_q);
   s.start = (int)a;
   s.n = (int)min(b - a, (int64_t)p.max_new);
-  s.kv = max(__ldg(p.kv_len + i), 0);
-  s.len = (int)min((int64_t)s.kv, (int64_t)p.max_pages * p.page_size);
+  const int kv = max(__ldg(p.kv_len + i), 0);
+  s.first = (int)(kv - (end - a) + 1);
+  s.len = (int)min((int64_t)kv, (int64_t)p.max_pages * p.page_size);
   return s;
 }
 
@@ -226,7 +229,7 @@ __device__ __forceinline__ int blocks_of(const PagedParams &p, const PagedCut &c
 // Keys that the last row of block k sees (the first of its rows may see fewer)
 __device__ __forceinline__ int seen_by(const PagedParams &p, const PagedCut &c, const Seq &s, int k) {
   const int last = min((k + 1) * c.rows, s.n * p.group) - 1;
-  return max(0, min(s.len, s.kv - s.n + 1 + last / p.group));
+  return max(0, min(s.len, s.first + last / p.group));
 }
 __device__ __forceinline__ int units_of(const PagedParams &p, const PagedCut &c, const Seq &s, int k) {
   return (seen_by(p, c, s, k) + (1 << c.unit) - 1) >> c.unit;

@@ -241,7 +241,7 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
   for (;;) {
     const Seq s = cur.s;
     const int head = cur.head, rows = s.n * p.group, row0 = cur.block * kRows;
-    const int hidden = s.kv - s.n + 1;  // a row of new token t sees the keys below hidden + t
+    const int hidden = s.first;  // a row of new token t sees the keys below hidden + t
     const int seen = seen_by(p, p.few, s, cur.block);
     const int k0 = cur.unit << p.few.unit, k1 = min(k0 + (cur.take << p.few.unit), seen);
 

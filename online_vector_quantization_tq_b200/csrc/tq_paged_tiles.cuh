@@ -114,7 +114,7 @@ __device__ __forceinline__ Segment segment_of(const PagedParams &p, const Cursor
   g.rows = cur.s.n * p.group;
   g.row0 = cur.block * SM::kRows;
   g.turns = SM::kQTiles == 1 || g.rows - g.row0 <= kTile;
-  g.hidden = cur.s.kv - cur.s.n + 1;
+  g.hidden = cur.s.first;
   g.seen = seen_by(p, p.many, cur.s, cur.block);
   g.t0 = cur.unit;
   g.tiles = cur.take;

@@ -23,3 +23,54 @@ def test_fewer_keys_than_new_tokens(tq, d, ip):  # noqa: F811
     run_case(tq, d, 4, ip, 3, 2, 1, 16, seqs, "bf16", seed=d + 1, many=True)
     run_case(tq, d, 3, ip, 4, 1, 4, 48, [(129, 20), (96, 96), (70, 64), (1, 5)], "f16", seed=d + 2, many=True)
     tq.tq_sync_check(quantizer(tq, d, 4, ip)[0])
+
+
+@pytest.mark.parametrize("d,ip,dtype", [(64, True, "f16"), (128, False, "bf16")])
+@pytest.mark.parametrize("max_new,group", [(1, 4), (5, 4), (40, 4), (150, 2)])
+def test_more_new_tokens_than_max_new(tq, d, ip, dtype, max_new, group):  # noqa: F811
+    """Of a sequence with more than max_new new tokens the first max_new are
+    attended, each with the keys that it sees among all of them; the others'
+    rows are left as they were."""
+    rng = np.random.default_rng(max_new)
+    (qk, tk), (qv, tv) = quantizer(tq, d, 4, ip), quantizer(tq, d, 4, False, seed=1)
+    seqs = [(max_new + 9, 300), (2 * max_new + 300, 2 * max_new + 310), (max_new, 77), (max_new + 1, max_new), (0, 9)]
+    news, kv_lens = [s[0] for s in seqs], [s[1] for s in seqs]
+    batch = Batch(tq, qk, qv, 2, 16, kv_lens, rng)
+    heads, total = 2 * group, sum(news)
+    starts = [sum(news[:i]) for i in range(len(news) + 1)]
+    y = torch.from_numpy(rng.standard_normal((total, heads * d)).astype(np.float32)).to(DT[dtype]).cuda()
+    out = torch.full_like(y, -7.0)
+    tq.tq_attend_paged(qk, qv, y, torch.tensor(starts, dtype=torch.int32, device="cuda"), *batch.caches, batch.table_dev,
+                       torch.tensor(kv_lens, dtype=torch.int32, device="cuda"), max_new, 1 / math.sqrt(d), out=out)
+    tq.tq_sync_check(qk)
+    res, yy = out.double().cpu().numpy(), y.double().cpu().numpy()
+    for i, (n, kv) in enumerate(seqs):
+        m = min(n, max_new)
+        rows = slice(starts[i], starts[i] + m)
+        assert np.all(res[starts[i] + m: starts[i + 1]] == -7.0)
+        for h in range(2):
+            cols = slice(h * group * d, (h + 1) * group * d)
+            limits = np.repeat(np.clip(kv - n + 1 + np.arange(m), 0, kv), group)
+            ref, bound = attend(yy[rows, cols].reshape(m * group, d), limits, 1 / math.sqrt(d),
+                                unpack(batch.rows[0][i][h], tk), tk, unpack(batch.rows[1][i][h], tv), tv, dtype,
+                                m * group > 64)
+            got = res[rows, cols].reshape(m * group, d)
+            assert np.all(np.abs(got - ref) <= bound), f"sequence {i}, head {h}"
+            assert np.all(got[limits <= 0] == 0.0)
+
+
+@pytest.mark.parametrize("n,there,group,kv", [(7, 5, 4, 50), (170, 150, 1, 200)])
+def test_sequences_that_end_behind_the_queries(tq, n, there, group, kv):  # noqa: F811
+    """Fewer rows of queries than q_start counts: those that are there see what
+    they would see beside the others."""
+    d = 128
+    rng = np.random.default_rng(n)
+    (qk, tk), (qv, tv) = quantizer(tq, d, 4, False), quantizer(tq, d, 4, False, seed=1)
+    batch = Batch(tq, qk, qv, 1, 16, [kv], rng)
+    y = torch.from_numpy(rng.standard_normal((there, group * d)).astype(np.float32)).bfloat16().cuda()
+    out = tq.tq_attend_paged(qk, qv, y, torch.tensor([0, n], dtype=torch.int32, device="cuda"), *batch.caches,
+                             batch.table_dev, torch.tensor([kv], dtype=torch.int32, device="cuda"), n, 0.1)
+    limits = np.repeat(kv - n + 1 + np.arange(there), group)
+    ref, bound = attend(y.double().cpu().numpy().reshape(there * group, d), limits, 0.1, unpack(batch.rows[0][0][0], tk),
+                        tk, unpack(batch.rows[1][0][0], tv), tv, "bf16", there * group > 64)
+    assert np.all(np.abs(out.double().cpu().numpy().reshape(there * group, d) - ref) <= bound)
