@@ -130,8 +130,27 @@ def _ld(x: torch.Tensor) -> int:
     return x.stride(0)
 
 
-def _workspace(nbytes: int, device) -> torch.Tensor:
-    return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A result that a call on `stream` writes.  torch hands memory out, and
+    takes it back, in the order of one stream: what another than the current
+    one writes has to come from its own memory, and the current one, whose
+    tensor it looks like to the caller, has to be done with it before it is
+    reused."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _workspace(nbytes: int, device, stream=None) -> torch.Tensor:
+    """Scratch of a call on `stream`, from that stream's memory (see _empty)."""
+    n = max(int(nbytes), 16)
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 @dataclass
@@ -229,10 +248,10 @@ class Quantizer:
             s.ctypes.data_as(ctypes.c_void_p)))
         return r, (diag if self.rotation == "hadamard" else None), s
 
-    def empty_encoded(self, n: int, device="cuda") -> Encoded:
-        return Encoded(torch.empty((n, self.code_bytes), dtype=torch.uint8, device=device),
-                       torch.empty((n, self.sign_bytes), dtype=torch.uint8, device=device),
-                       torch.empty((n, 2), dtype=torch.float32, device=device))
+    def empty_encoded(self, n: int, device="cuda", stream=None) -> Encoded:
+        return Encoded(_empty((n, self.code_bytes), torch.uint8, device, stream),
+                       _empty((n, self.sign_bytes), torch.uint8, device, stream),
+                       _empty((n, 2), torch.float32, device, stream))
 
     def empty_paged(self, npages: int, kv_heads: int, page_size: int, device="cuda") -> PagedCache:
         lead = (npages, kv_heads, page_size)
@@ -271,7 +290,7 @@ def tq_encode(q: Quantizer, x: torch.Tensor, out: Encoded | None = None, chan: t
               stream=None) -> Encoded:
     n = x.shape[0]
     if out is None:
-        out = q.empty_encoded(n, x.device)
+        out = q.empty_encoded(n, x.device, stream)
     out.check()
     if chan is not None and chan.dtype != torch.int32:
         raise TypeError("chan must be int32")
@@ -281,7 +300,7 @@ def tq_encode(q: Quantizer, x: torch.Tensor, out: Encoded | None = None, chan: t
     if workspace is None:
         ws = L.tq_encode_workspace_bytes(q.handle, n)
         if ws:
-            workspace = _workspace(ws, x.device)
+            workspace = _workspace(ws, x.device, stream)
     if workspace is None:
         _check("tq_encode", L.tq_encode(*args, _stream(stream)))
     else:
@@ -292,8 +311,8 @@ def tq_encode(q: Quantizer, x: torch.Tensor, out: Encoded | None = None, chan: t
 def tq_prepare_queries(q: Quantizer, y: torch.Tensor, ychan: torch.Tensor | None = None, ychan_rows: int = 0,
                        stream=None):
     nq = y.shape[0]
-    ytil = torch.empty((nq, q.d), dtype=torch.float32, device=y.device)
-    p = torch.empty((nq, q.m), dtype=torch.float32, device=y.device)
+    ytil = _empty((nq, q.d), torch.float32, y.device, stream)
+    p = _empty((nq, q.m), torch.float32, y.device, stream)
     _check("tq_prepare_queries", lib().tq_prepare_queries(
         q.handle, _ptr(y), nq, _ld(y), _ptr(ychan), ychan_rows, _ptr(ytil), _ptr(p), _stream(stream)))
     return ytil, p
@@ -308,9 +327,9 @@ def tq_score(q: Quantizer, y: torch.Tensor, groups: int, G: int, enc: Encoded, k
              workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     enc.check()
     if out is None:
-        out = torch.empty((groups * G, keys_per_group), dtype=torch.float32, device=y.device)
+        out = _empty((groups * G, keys_per_group), torch.float32, y.device, stream)
     if workspace is None:
-        workspace = score_workspace(q, groups * G, y.device)
+        workspace = _workspace(lib().tq_score_workspace_bytes(q.handle, groups * G), y.device, stream)
     _check("tq_score", lib().tq_score(
         q.handle, _ptr(y), groups, G, _ld(y), _ptr(ychan), _ptr(enc.codes), _ptr(enc.signs), _ptr(enc.norms),
         keys_per_group, _ptr(out), int(bool(accumulate)), _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -322,7 +341,8 @@ def tq_score_prepare(q: Quantizer, y: torch.Tensor, groups: int, G: int, workspa
     """Query half of tq_score: writes the prepared queries into `workspace`
     (allocated when None) and returns it, for tq_score_prepared."""
     if workspace is None:
-        workspace = score_workspace(q, groups * G, y.device)
+        nbytes = max(lib().tq_score_workspace_bytes(q.handle, groups * G), 16)
+        workspace = _empty(nbytes, torch.uint8, y.device, stream)
     _check("tq_score_prepare", lib().tq_score_prepare(
         q.handle, _ptr(y), groups, G, _ld(y), _ptr(ychan), _ptr(workspace), workspace.numel(), _stream(stream)))
     return workspace
@@ -335,7 +355,7 @@ def tq_score_prepared(q: Quantizer, groups: int, G: int, enc: Encoded, keys_per_
     `workspace`."""
     enc.check()
     if out is None:
-        out = torch.empty((groups * G, keys_per_group), dtype=torch.float32, device=enc.codes.device)
+        out = _empty((groups * G, keys_per_group), torch.float32, enc.codes.device, stream)
     _check("tq_score_prepared", lib().tq_score_prepared(
         q.handle, groups, G, _ptr(enc.codes), _ptr(enc.signs), _ptr(enc.norms), keys_per_group, _ptr(out),
         int(bool(accumulate)), _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -353,12 +373,12 @@ def tq_topk(q: Quantizer, y: torch.Tensor, enc: Encoded, k: int, n: int | None =
     enc.check()
     n = enc.codes.shape[0] if n is None else n
     if out is None:
-        vals = torch.empty((nq, k), dtype=torch.float32, device=y.device)
-        idx = torch.empty((nq, k), dtype=torch.int64, device=y.device)
+        vals = _empty((nq, k), torch.float32, y.device, stream)
+        idx = _empty((nq, k), torch.int64, y.device, stream)
     else:
         vals, idx = out
     if workspace is None:
-        workspace = topk_workspace(q, nq, n, k, y.device)
+        workspace = _workspace(lib().tq_topk_workspace_bytes(q.handle, nq, n, k), y.device, stream)
     _check("tq_topk", lib().tq_topk(
         q.handle, _ptr(y), nq, _ld(y), _ptr(enc.codes), _ptr(enc.signs), _ptr(enc.norms), n, k,
         _ptr(vals), _ptr(idx), _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -374,9 +394,9 @@ def tq_attend(qv: Quantizer, logits: torch.Tensor, groups: int, G: int, venc: En
     venc.check()
     n = keys_per_group - key_base if nkeys is None else nkeys
     if out is None:
-        out = torch.empty((groups * G, qv.d), dtype=torch.float32, device=logits.device)
+        out = _empty((groups * G, qv.d), torch.float32, logits.device, stream)
     if workspace is None:
-        workspace = _workspace(lib().tq_attend_workspace_bytes(qv.handle, groups, G, n), logits.device)
+        workspace = _workspace(lib().tq_attend_workspace_bytes(qv.handle, groups, G, n), logits.device, stream)
     _check("tq_attend", lib().tq_attend(
         qv.handle, _ptr(logits), _ld(logits), groups, G, float(scale), _ptr(venc.codes),
         _ptr(venc.norms), keys_per_group, key_base, n, _ptr(out), _ld(out), _ptr(workspace), workspace.numel(),
@@ -468,7 +488,7 @@ def tq_attend_prompt(q: Quantizer, y: torch.Tensor, k: torch.Tensor, v: torch.Te
     if nseq < 0:
         raise ValueError("cu_seqlens must have one entry more than there are sequences")
     if out is None:
-        out = torch.empty_like(y, memory_format=torch.contiguous_format)
+        out = _empty(y.shape, y.dtype, y.device, stream)
     elif out.dtype != dtype or out.shape != y.shape:
         raise ValueError("out must have y's shape and type")
     device = _one_device(q, "y k v cu_seqlens out", y, k, v, cu_seqlens, out)
@@ -528,13 +548,13 @@ def tq_attend_paged(qk: Quantizer, qv: Quantizer, y: torch.Tensor, q_start: torc
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != nseq:
         raise TypeError(f"page_table must be an int32 tensor of {nseq} rows")
     if out is None:
-        out = torch.empty_like(y, memory_format=torch.contiguous_format)
+        out = _empty(y.shape, y.dtype, y.device, stream)
     elif out.dtype != y.dtype or out.shape != y.shape:
         raise ValueError("out must have y's shape and type")
     max_pages = page_table.shape[1]
     if workspace is None:
-        workspace = attend_paged_workspace(qk, qv, total_q, nseq, heads, kv_heads, max_new, max_pages, page_size,
-                                           y.device)
+        workspace = _workspace(lib().tq_attend_paged_workspace_bytes(
+            qk.handle, qv.handle, total_q, nseq, heads, kv_heads, max_new, max_pages, page_size), y.device, stream)
     device = _one_device(qk, "y q_start kv_len page_table out workspace kcache.codes kcache.norms vcache.codes "
                              "vcache.norms kcache.signs", y, q_start, kv_len, page_table, out, workspace, kcache.codes,
                          kcache.norms, vcache.codes, vcache.norms, kcache.signs)
@@ -555,7 +575,7 @@ def tq_set_qjl_onthefly(q: Quantizer, enable: bool = True) -> None:
 def tq_qjl_matrix(q: Quantizer, device="cuda", stream=None) -> torch.Tensor:
     """S (m x d fp16 bit patterns as int16, row-major) generated on the
     device from the quantizer seed."""
-    out = torch.empty((q.m, q.d), dtype=torch.int16, device=device)
+    out = _empty((q.m, q.d), torch.int16, device, stream)
     _check("tq_qjl_matrix", lib().tq_qjl_matrix(q.handle, _ptr(out), _stream(stream)))
     return out
 
@@ -566,8 +586,8 @@ def tq_rerank(y: torch.Tensor, x: torch.Tensor, cand: torch.Tensor, k: int, out=
     x, and the k best per query: (scores fp32 [nq, k], keys int64 [nq, k])."""
     nq, kc = cand.shape
     if out is None:
-        vals = torch.empty((nq, k), dtype=torch.float32, device=y.device)
-        idx = torch.empty((nq, k), dtype=torch.int64, device=y.device)
+        vals = _empty((nq, k), torch.float32, y.device, stream)
+        idx = _empty((nq, k), torch.int64, y.device, stream)
     else:
         vals, idx = out
     if cand.dtype != torch.int64 or not cand.is_contiguous():
@@ -582,9 +602,9 @@ def tq_outlier_channels(x: torch.Tensor, groups: int, rows_per_group: int, count
     """Per group, the `count` highest-mean-square channels and the rest (both
     ascending int32 tensors on x's device)."""
     dim = x.shape[1]
-    sel = torch.empty((groups, count), dtype=torch.int32, device=x.device)
-    rest = torch.empty((groups, dim - count), dtype=torch.int32, device=x.device)
-    ws = _workspace(lib().tq_outlier_workspace_bytes(groups, dim), x.device)
+    sel = _empty((groups, count), torch.int32, x.device, stream)
+    rest = _empty((groups, dim - count), torch.int32, x.device, stream)
+    ws = _workspace(lib().tq_outlier_workspace_bytes(groups, dim), x.device, stream)
     _check("tq_outlier_channels", lib().tq_outlier_channels(
         _ptr(x), _dtype(x), groups, rows_per_group, dim, _ld(x), count, _ptr(sel), _ptr(rest),
         _ptr(ws), ws.numel(), _stream(stream)))
