@@ -548,9 +548,11 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float2 kn = *reinterpret_cast<const float2 *>(st + ST::kNormK + (8 * i + kpos) * 8);
-          vn[i] = *reinterpret_cast<const float *>(st + ST::kNormV + (8 * i + kpos) * 8);
-          // a value that is not finite makes a NaN of every row that sees its key, and of no other
-          if (!(vn[i] < INFINITY)) {
+          vn[i] = fabsf(*reinterpret_cast<const float *>(st + ST::kNormV + (8 * i + kpos) * 8));
+          kn.x = fabsf(kn.x);
+          // a norm that is not finite makes a NaN of every row that sees its key, and of no other (an infinite one
+          // could make a logit of -inf, and its key would drop out)
+          if (!(vn[i] + kn.x + (IP ? fabsf(kn.y) : 0.f) < INFINITY)) {
             kn.x = NAN;
             vn[i] = 0.f;
           }

@@ -325,7 +325,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
           }
           if (pg >= 0) {
             n = __ldg(p.knorms + row);
-            v = __ldg(&p.vnorms[row].x);
+            n.x = fabsf(n.x);  // (below 0 is for what has no page)
+            v = fabsf(__ldg(&p.vnorms[row].x));
           } else if (pg == -1) {
             n.x = -1.f;
           }
@@ -344,8 +345,9 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
           if (!ok) break;
           const float e = flash::exponent_above(top_of(0, ring.before + j));
           exponent = fmaxf(exponent, flash::exponent_above(top_of(1, ring.before + j)));
-          // a value that is not finite makes a NaN of every row that sees its key, and of no other
-          const float f = fabsf(v) < INFINITY ? fmaxf(n.x, 0.f) * flash::ex2(-e) + 0.f * n.x : NAN;
+          // a norm that is not finite makes a NaN of every row that sees its key, and of no other
+          const float f =
+              v + n.x + (IP ? fabsf(n.y) : 0.f) < INFINITY ? fmaxf(n.x, 0.f) * flash::ex2(-e) : NAN;
           byte_tables<WK>(p.ckf, f, tlo, thi);
           uint8_t *slot = smem + SM::kRing + (at % SM::kSlots) * SM::kSlot;
 #pragma unroll
@@ -383,7 +385,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
           v = 0.f;
           if (pg >= 0) {
             n = __ldg(p.knorms + row);
-            v = __ldg(&p.vnorms[row].x);
+            n.x = fabsf(n.x);
+            v = fabsf(__ldg(&p.vnorms[row].x));
           }
         }
       } else {
@@ -398,7 +401,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
             for (int i = 0; i < WV; ++i) w[q][i] = 0u;
             if (pg >= 0) load_words<WV>(w[q], p.vcodes + row * (WV * D / 8) + q * (4 * WV));
           }
-          if (pg >= 0) v = __ldg(&p.vnorms[row].x);
+          if (pg >= 0) v = fabsf(__ldg(&p.vnorms[row].x));
         }
         for (int j = 0; j < g.tiles; ++j) {
           const int pg = page;
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
             if (pg >= 0) load_words<WV>(w[q], p.vcodes + row * (WV * D / 8) + q * (4 * WV));
           }
           v = 0.f;
-          if (pg >= 0) v = __ldg(&p.vnorms[row].x);
+          if (pg >= 0) v = fabsf(__ldg(&p.vnorms[row].x));
           sm100::fence_proxy_async();
           sm100::mbar_arrive(&full[at % SM::kSlots]);
         }

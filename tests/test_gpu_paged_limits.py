@@ -74,3 +74,38 @@ def test_sequences_that_end_behind_the_queries(tq, n, there, group, kv):  # noqa
     ref, bound = attend(y.double().cpu().numpy().reshape(there * group, d), limits, 0.1, unpack(batch.rows[0][0][0], tk),
                         tk, unpack(batch.rows[1][0][0], tv), tv, "bf16", there * group > 64)
     assert np.all(np.abs(out.double().cpu().numpy().reshape(there * group, d) - ref) <= bound)
+
+
+@pytest.mark.parametrize("n,group", [(3, 4), (3, 5), (40, 4), (200, 2)])  # few rows twice, many rows twice
+@pytest.mark.parametrize("d,ip", [(128, True), (128, False), (64, True), (64, False)])
+@pytest.mark.parametrize("what", [math.inf, -math.inf])
+def test_infinite_norms(tq, d, ip, n, group, what):  # noqa: F811
+    """An infinite norm of a key, of its residual or of a value makes NaN of the
+    tokens that see it, whatever the signs of their products; the tokens before
+    it, and the other sequence, keep their results, bit for bit."""
+    rng = np.random.default_rng(n + d)
+    (qk, _), (qv, _) = quantizer(tq, d, 4, ip), quantizer(tq, d, 4, False, seed=1)
+    kv = n + 150
+    batch = Batch(tq, qk, qv, 1, 16, [kv, 60], rng)
+    y = torch.randn(n + 1, group * d, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    start = torch.tensor([0, n, n + 1], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([kv, 60], dtype=torch.int32, device="cuda")
+
+    def call():
+        return tq.tq_attend_paged(qk, qv, y, start, *batch.caches, batch.table_dev, lens, n, 0.1)
+    clean = call()
+    assert bool(torch.isfinite(clean).all())
+    for side, which in ((0, 0), (1, 0)) + (((0, 1),) if ip else ()):
+        for t in (0, 1, n - 1):
+            at = kv - n + t
+            norms = batch.caches[side].norms[batch.table[0, at // 16], 0, at % 16]
+            keep = norms.clone()
+            norms[which] = what
+            out = call()
+            norms.copy_(keep)
+            assert torch.equal(out[:t], clean[:t]) and torch.equal(out[n:], clean[n:])
+            assert bool(torch.isnan(out[t:n]).all())
+    # residual norms of keys without sign bits, and second entries of values, are not looked at
+    for cache in batch.caches[1:] if ip else batch.caches:
+        cache.norms[..., 1] = what
+    assert torch.equal(call(), clean)
