@@ -380,18 +380,18 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_paged_join_many(const _
           float top = M[i];
 #pragma unroll
           for (int u = 0; u < kRuns; ++u) top = fmaxf(top, a[u][i].x);
-          const float old = M[i] == -INFINITY ? 0.f : ex2(M[i] - top);
+          const float old = M[i] == -INFINITY ? 0.f : ex2_half(M[i] - top);
           M[i] = top;
-          L[i] *= old;
+          L[i] = old * L[i] * old;
 #pragma unroll
-          for (int e = 0; e < V; ++e) v[i][e] *= old;
+          for (int e = 0; e < V; ++e) v[i][e] *= old * old;
 #pragma unroll
           for (int u = 0; u < kRuns; ++u)
             if (a[u][i].y != 0.f) {  // the row sees some of the run's keys
-              const float g = a[u][i].x == -INFINITY ? 0.f : ex2(a[u][i].x - top);
-              L[i] = fmaf(g, a[u][i].y, L[i]);
+              const float g = a[u][i].x == -INFINITY ? 0.f : ex2_half(a[u][i].x - top);
+              L[i] = fmaf(g * a[u][i].y, g, L[i]);
 #pragma unroll
-              for (int e = 0; e < V; ++e) v[i][e] = fmaf(g, x[u][i][e], v[i][e]);
+              for (int e = 0; e < V; ++e) v[i][e] = fmaf(g * g, x[u][i][e], v[i][e]);
             }
         }
       }
@@ -458,10 +458,10 @@ __global__ void __launch_bounds__(128) k_attend_paged_join(const __grid_constant
 #pragma unroll
       for (int e = 0; e < V; ++e) x[e] = po[e];
       if (a.y != 0.f) {  // the row sees some of the run's keys
-        const float g = a.x == -INFINITY ? 0.f : ex2(a.x - M);
-        L = fmaf(g, a.y, L);
+        const float g = a.x == -INFINITY ? 0.f : ex2_half(a.x - M);
+        L = fmaf(g * a.y, g, L);
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = fmaf(g, x[e], v[e]);
+        for (int e = 0; e < V; ++e) v[e] = fmaf(g * g, x[e], v[e]);
       }
     }
   }

@@ -181,7 +181,7 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
   __shared__ int s_pmax[ST::kQueryRows];
   __shared__ float s_psum[ST::kQueryRows];
   __shared__ uint16_t s_c[32];
-  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_v[kWarps];
+  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
   {
@@ -463,7 +463,6 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
         m[q][e] = limit[q][e] = -INFINITY;
         l[q][e] = base[q][e] = 0.f;
       }
-    float vtop = pow2_above(0.f), vinv = 1.0f / vtop;  // power of two above the value norms seen; weights carry 1 / it
     for (int key0 = k0 + warp * kBlock; key0 < k1; key0 += kStep) {
       cp_async_wait<kStages - 2>();
       __syncwarp();
@@ -577,43 +576,35 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
           if (kk >= seen) vn[i] = 0.f;  // what lies behind the last key may be anything
         }
       }
-      // The exponents' references: O and l are rescaled only when a maximum has
-      // grown by more than 8 (weights stay below 2^8), or a value norm above
-      // its power of two.
-      bool grow = fmaxf(vn[0], vn[1]) > vtop;
+      // The exponents' references: the largest logit plus its value norm's
+      // exponent, of the keys that the row sees, so that what the values are
+      // multiplied by, weight times norm, stays below 2^8 and no norm of a key
+      // that is hidden or of little weight takes bits from the others'.  O and l
+      // are rescaled only when a reference has grown by more than 8.
+      const float ve[2] = {norm_exponent(vn[0]), norm_exponent(vn[1])};
+      bool grow = false;
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float t = fmaxf(x[q][0][e], x[q][1][e]);
-          grow |= t > limit[q][e];
-        }
+        for (int e = 0; e < 2; ++e) grow |= fmaxf(x[q][0][e] + ve[0], x[q][1][e] + ve[1]) > limit[q][e];
       if (__any_sync(0xffffffffu, grow)) {
-        float vt = fmaxf(vn[0], vn[1]);
-#pragma unroll
-        for (int b = 4; b < 32; b <<= 1) vt = fmaxf(vt, __shfl_xor_sync(0xffffffffu, vt, b));
-        const float vnew = vt > vtop ? pow2_above(vt) : vtop;
-        const float vf = vtop / vnew;
-        vtop = vnew;
-        vinv = 1.0f / vtop;
 #pragma unroll
         for (int q = 0; q < NQ; ++q)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float t = fmaxf(x[q][0][e], x[q][1][e]);
+            float t = fmaxf(x[q][0][e] + ve[0], x[q][1][e] + ve[1]);
 #pragma unroll
             for (int b = 4; b < 32; b <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, b));
-            float f = 1.f;
             if (t > m[q][e]) {
-              f = ex2(m[q][e] - t);
+              const float f = ex2_half(m[q][e] - t);
               m[q][e] = base[q][e] = t;
               limit[q][e] = t + 8.f;
-            }
-            l[q][e] *= f;
+              l[q][e] = f * l[q][e] * f;
 #pragma unroll
-            for (int k = 0; k < MT; ++k) {
-              o[q][k][e] *= f * vf;
-              o[q][k][2 + e] *= f * vf;
+              for (int k = 0; k < MT; ++k) {
+                o[q][k][e] *= f * f;
+                o[q][k][2 + e] *= f * f;
+              }
             }
           }
       }
@@ -629,12 +620,11 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float f = vn[i] * vinv;
-          const __half2 h = __floats2half2_rn(w[i][0] * f, w[i][1] * f);
+          const __half2 h = __floats2half2_rn(w[i][0] * vn[i], w[i][1] * vn[i]);
           wb[q][i] = transpose8(*reinterpret_cast<const uint32_t *>(&h));
           if (kLow && low) {
             const float2 g = __half22float2(h);
-            const __half2 l = __floats2half2_rn(w[i][0] * f - g.x, w[i][1] * f - g.y);
+            const __half2 l = __floats2half2_rn(w[i][0] * vn[i] - g.x, w[i][1] * vn[i] - g.y);
             wl[q][i] = transpose8(*reinterpret_cast<const uint32_t *>(&l));
           }
         }
@@ -688,7 +678,6 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
           s_l[warp][8 * q + 2 * c + e] = l[q][e];
         }
       }
-    if (lane == 0) s_v[warp] = vtop;
     __syncthreads();  // every warp is done with the ring
     load_projection();  // (for the next block of rows)
     // coordinate (D / 8) r + i of a row, i = 2 t + (e >> 1), stands at 8 i + r
@@ -711,11 +700,11 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
       for (int e = 0; e < D / 32; ++e) v[e] = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = s_m[w][i] == -INFINITY ? 0.f : ex2(s_m[w][i] - M);
+        const float f = s_m[w][i] == -INFINITY ? 0.f : ex2_half(s_m[w][i] - M);
         if (s_l[w][i] != 0.f) {  // the row sees some of the warp's keys
-          L += f * s_l[w][i];
+          L += f * s_l[w][i] * f;
 #pragma unroll
-          for (int e = 0; e < D / 32; ++e) v[e] += f * (s_v[w] * p.vunit) * so[(w * kRows + i) * LDO + lane * (D / 32) + e];
+          for (int e = 0; e < D / 32; ++e) v[e] += f * f * p.vunit * so[(w * kRows + i) * LDO + lane * (D / 32) + e];
         }
       }
       float *to;

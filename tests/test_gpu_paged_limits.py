@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import tq_oracle as o
 from tests.paged_reference import attend, unpack
 from tests.test_gpu_paged import DT, Batch, check, quantizer, run_case, tq  # noqa: F401
 
@@ -109,3 +110,96 @@ def test_infinite_norms(tq, d, ip, n, group, what):  # noqa: F811
     for cache in batch.caches[1:] if ip else batch.caches:
         cache.norms[..., 1] = what
     assert torch.equal(call(), clean)
+
+
+def set_norms(batch, side, norms):
+    """Norms of the first sequence's keys (side 0) or values (side 1), for every KV head."""
+    cache, n = batch.caches[side], len(norms)
+    for h in range(batch.kv_heads):
+        batch.rows[side][0][h][2][:, 0] = norms
+        for j in range(n):
+            cache.norms[batch.table[0, j // batch.page], h, j % batch.page, 0] = float(norms[j])
+
+
+def documented(got, y, limits, scale, ke, tk, ve, tv):
+    """Worst share of the precision that include/tq.h states, 2^-9 sum_k softmax_k
+    ||v_k|| / sqrt(d) per coordinate beside the output's own rounding, as rows'
+    2-norms: 2^-9 sum_k softmax_k ||v_k|| + 2^-8 ||out||.  (Codes drawn at random
+    have ||c|| of about 1.5.  One key with all the weight: its rounding is at most
+    2^-11 of 1.5 ||v||.  Two with half each: a logit's error, of 2^-11 0.41 a factor
+    and coordinate, has an rms of 1.2e-3 at scale ||k|| = 2, which moves the output
+    by a quarter of that times 2.1 ||v||, 2^-10.6 ||v||; more keys, less.)"""
+    ref, _ = attend(y, limits, scale, ke, tk, ve, tv, "bf16")
+    yt, p = o.prepare_query(y, tk)
+    see = np.arange(len(ke["norm"]))[None] < np.asarray(limits)[:, None]
+    x = np.where(see, scale * o.score(yt, p, ke, tk), -np.inf)
+    assert np.abs(np.where(see, x, 0.0)).max() < 30
+    w = np.exp(x - x.max(1, keepdims=True))
+    w /= w.sum(1, keepdims=True)
+    bound = 2.0 ** -9 * (w @ ve["norm"])
+    size = np.linalg.norm(ref, axis=1)
+    return float((np.linalg.norm(got - ref, axis=1) / (bound + 2.0 ** -8 * (size + bound))).max())
+
+
+# (new tokens, query heads of a KV head): few rows, of each block height, and many
+ROWS = [(4, 2), (4, 4), (5, 4), (16, 4)]
+
+
+@pytest.mark.parametrize("n,group", ROWS)
+@pytest.mark.parametrize("d,ip", [(128, False), (128, True), (64, False), (64, True)])
+def test_norms_that_a_token_does_not_see(tq, d, ip, n, group):  # noqa: F811
+    """The last new token's key or value has a norm 2^16 to 2^60 times the others'
+    (of 2.6 decades): the tokens before it keep the documented precision."""
+    rng = np.random.default_rng(n)
+    (qk, tk), (qv, tv) = quantizer(tq, d, 4, ip), quantizer(tq, d, 4, False, seed=1)
+    kv = n + 150
+    batch = Batch(tq, qk, qv, 1, 16, [kv], rng)
+    rows = n * group
+    y = torch.from_numpy(rng.standard_normal((n, group * d)).astype(np.float32)).bfloat16().cuda()
+    yy = y.double().cpu().numpy().reshape(rows, d)
+    limits = np.repeat(kv - n + 1 + np.arange(n), group)
+    before = [batch.rows[s][0][0][2][:, 0].copy() for s in (0, 1)]
+    seen = slice(0, rows - group)
+    scale = 0.2 / math.sqrt(d)
+    for side, up in ((1, 16), (1, 30), (1, 60), (0, 16), (0, 40)):
+        for s in (0, 1):
+            norms = before[s].copy()
+            if s == side:
+                norms[-1] = np.float32(10.0 * 2.0 ** up)
+            set_norms(batch, s, norms)
+        out = tq.tq_attend_paged(qk, qv, y, torch.tensor([0, n], dtype=torch.int32, device="cuda"), *batch.caches,
+                                 batch.table_dev, torch.tensor([kv], dtype=torch.int32, device="cuda"), n, scale)
+        got = out.double().cpu().numpy().reshape(rows, d)
+        assert np.all(np.isfinite(got))
+        ke, ve = unpack(batch.rows[0][0][0], tk), unpack(batch.rows[1][0][0], tv)
+        some = {k: v[:-1] for k, v in ke.items()}, {k: v[:-1] for k, v in ve.items()}
+        worst = documented(got[seen], yy[seen], limits[seen], scale, some[0], tk, some[1], tv)
+        assert worst <= 1.0, (side, up, worst)
+
+
+@pytest.mark.parametrize("n,group", ROWS)
+@pytest.mark.parametrize("d,ip", [(128, False), (64, True)])
+def test_norms_of_very_different_sizes(tq, d, ip, n, group):  # noqa: F811
+    """Value norms over 2^-60 to 2^60 and key norms over 2^-20 to 2^4, key by key,
+    or a few large ones on keys of little weight: the documented precision."""
+    rng = np.random.default_rng(n + 1)
+    (qk, tk), (qv, tv) = quantizer(tq, d, 4, ip), quantizer(tq, d, 4, False, seed=1)
+    kv, rows = n + 400, n * group
+    batch = Batch(tq, qk, qv, 1, 16, [kv], rng)
+    y = torch.from_numpy(rng.standard_normal((n, group * d)).astype(np.float32)).bfloat16().cuda()
+    yy = y.double().cpu().numpy().reshape(rows, d)
+    limits = np.repeat(kv - n + 1 + np.arange(n), group)
+    scale = 1.0 / math.sqrt(d)
+    one = rng.uniform(4.0, 16.0, kv)
+    few = np.where(rng.random(kv) < 0.02, 2.0 ** 20, 1.0)  # where the logits turn out low, these weigh little
+    for knorm, vnorm in ((one, 2.0 ** rng.uniform(-60, 60, kv)), (2.0 ** rng.uniform(-20, 4, kv), one),
+                         (one * np.minimum(few, 2.0) ** 0.5, few), (one, np.where(np.arange(kv) < 200, 2.0 ** -50, 1.0)),
+                         (one, np.where(np.arange(kv) < 200, 1.0, 2.0 ** -50)), (one, np.full(kv, 2.0 ** -90)),
+                         (one, np.full(kv, 2.0 ** 90))):
+        set_norms(batch, 0, knorm.astype(np.float32))
+        set_norms(batch, 1, vnorm.astype(np.float32))
+        out = tq.tq_attend_paged(qk, qv, y, torch.tensor([0, n], dtype=torch.int32, device="cuda"), *batch.caches,
+                                 batch.table_dev, torch.tensor([kv], dtype=torch.int32, device="cuda"), n, scale)
+        worst = documented(out.double().cpu().numpy().reshape(rows, d), yy, limits, scale,
+                           unpack(batch.rows[0][0][0], tk), tk, unpack(batch.rows[1][0][0], tv), tv)
+        assert worst <= 1.0, worst
