@@ -18,8 +18,8 @@
 // product starts on the first 64 keys while the others' weights are computed.
 //
 // 128 x 128 exponentials cost the special-function units as many cycles as
-// the tile's two products cost the tensor cores, so some of them run on the
-// FMA pipe instead (ex2_poly2).
+// the tile's two products cost the tensor cores, so in the prompt kernel some of
+// them run on the FMA pipe instead (ex2_poly2).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -220,7 +220,7 @@ __device__ __forceinline__ void hide(float (&x)[32], int col, int see, const flo
     }
   }
 }
-template <int D, bool MASK, int PAIRS>
+template <int D, bool MASK>
 __device__ __forceinline__ void softmax_tile_twice(uint32_t s, uint32_t o, bool first, float mult, int see, Row &row,
                                                    const float *none, float scale, uint64_t *half, uint64_t *full) {
   uint32_t buf[2][32];
@@ -253,10 +253,7 @@ __device__ __forceinline__ void softmax_tile_twice(uint32_t s, uint32_t o, bool 
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float2 e = fma2(make_float2(x[2 * i], x[2 * i + 1]), m2, b2);
-      if (i % 8 >= 8 - PAIRS)
-        e = ex2_poly2<false>(e);
-      else
-        e = make_float2(ex2(e.x), ex2(e.y));
+      e = make_float2(ex2(e.x), ex2(e.y));
       sum[i & 1] = add2(sum[i & 1], e);
       w[i] = pack16<false>(e);
     }

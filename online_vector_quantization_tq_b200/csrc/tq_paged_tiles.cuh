@@ -559,10 +559,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
         const float m = fminf(fmaxf(mult * s_key[nr], 1.17549435e-38f), 3.402823466e38f), scale = s_value[nr];
         const int end = (g.t0 + j + 1) * kTile;
         if (end > lim_first || (s_gap[nr][0] | s_gap[nr][1] | s_gap[nr][2] | s_gap[nr][3]))
-          flash::softmax_tile_twice<D, true, 0>(S, O, n == 0, m, lim - (end - kTile), st, none, scale, &p_half[i],
+          flash::softmax_tile_twice<D, true>(S, O, n == 0, m, lim - (end - kTile), st, none, scale, &p_half[i],
                                                 &p_full[i]);
         else
-          flash::softmax_tile_twice<D, false, 0>(S, O, n == 0, m, 0, st, none, scale, &p_half[i], &p_full[i]);
+          flash::softmax_tile_twice<D, false>(S, O, n == 0, m, 0, st, none, scale, &p_half[i], &p_full[i]);
       }
       if (ok && cnt) ok = sm100::mbar_poll_abort(&o_full[i], (uint32_t)(no++ & 1), &s_abort, p.err, 126);
       if (!ok) break;
