@@ -280,7 +280,9 @@ tq_status tq_paged_store(const tq_quantizer *qk, const tq_quantizer *qv, const t
  * 2^-9 sum_k softmax_k ||v_k|| / sqrt(d) of the exact value per coordinate
  * beside its own rounding, for scaled logits up to about 30.  With up to 64
  * rows the centroids' common factor leaves them within 2^-13 and fp16 queries
- * keep 22 bits.  Value norms up to 2^100.  A key, residual or value norm that
+ * keep 22 bits.  Norms up to 2^100, of any sizes side by side: neither a norm
+ * that a token does not see nor one of little weight takes precision from the
+ * others'.  A key, residual or value norm that
  * is not finite makes NaN of the tokens that see it, and of no other; the sign
  * of a norm does not count.
  * Lengths and tables are read on the device: the call can be captured in a

@@ -97,16 +97,27 @@ __device__ __forceinline__ uint32_t pack16(float2 v) {
   return r;
 }
 
-// One row's running softmax state, in base 2: the exponent's reference, the
-// sum of the weights, and the exponent by which the values of O are scaled down
-// (the paged cache's, whose norms may be of any size).
+// One row's running softmax state, in base 2: the exponent's reference and the
+// sum of the weights.  The reference has two parts, a logit and (of the paged
+// cache, 0 otherwise) the exponent of a value norm: what a value is multiplied by,
+// weight times norm, is what stays below 2^kSlack.  They are kept apart because
+// beside a large logit the exponent would be lost in a sum, from the weights but
+// not from the values.  The sum, relative to both, may be as large as 2^80 a key
+// and as small as 2^-100: see move_reference.
 struct Row {
-  float ref = -INFINITY, sum = 0.f, scale = -100.f;
+  float ref = -INFINITY, norm = 0.f, sum = 0.f;
+  __device__ float exponent() const { return ref + norm; }  // of sum and O
 };
 
 // Exponent of the power of two above v (v >= 0), within what fp32 factors hold
 __device__ __forceinline__ float exponent_above(float v) {
   return fminf(fmaxf((float)((int)(__float_as_uint(v) >> 23) - 126), -100.f), 100.f);
+}
+
+// The same of a value norm, no less than -80 (a weight is at most 2^8 over its
+// key's norm, and the sum of 2^29 of them has to fit fp32)
+__device__ __forceinline__ float norm_exponent(float v) {
+  return fmaxf(__uint_as_float((__float_as_uint(v) >> 23) + 0x4B000000u) - (8388608.f + 126.f), -80.f);
 }
 
 // O *= f, one row per thread (whole warps)
@@ -124,21 +135,34 @@ __device__ __forceinline__ void scale_rows(uint32_t o, float f) {
   sm100::tmem_wait_st();
 }
 
-// Moves a row's reference up to `most` (base 2, of this tile) where it has
-// grown by more than the slack, by whole warps; sum and O follow.  first: O is
-// not there yet.  `scale` is what row.scale becomes (no less than it was).
-template <int D>
-__device__ __forceinline__ void move_reference(uint32_t o, bool first, float most, float scale, Row &row) {
-  const bool grow = most > row.ref + kSlack || (row.ref == -INFINITY && most > -INFINITY) || scale > row.scale;
-  if (!__any_sync(0xffffffffu, grow)) return;
-  float up = 0.f;
-  if (most > row.ref) {
-    up = most - row.ref;  // infinite for the first visible keys
+// A logit this large (base 2) makes the fused a * mult - reference differ from
+// the rounded product that the reference is by more than a weight's rounding;
+// from 2^28 on the weights would leave fp32.  Then the product is rounded first.
+constexpr float kLargeLogit = 65536.f;
+
+// Moves a row's reference up to a tile's highest logit (base 2) and the exponent
+// of the values there, where the two together have grown by more than the slack,
+// by whole warps; sum and O follow (the sum by a root of the factor twice: a
+// factor of 2^-126 or less is 0, and the sum may be 2^180 above what it is then
+// added to).  first: O is not there yet.  Returns whether the warp has large
+// logits; SMALL: if so, nothing is moved.
+template <int D, bool SMALL>
+__device__ __forceinline__ bool move_reference(uint32_t o, bool first, float most, float norm, Row &row) {
+  const float up = (most - row.ref) + (norm - row.norm);  // infinite for the first visible keys, a NaN for none so far
+  const float top = fmaxf(most, row.ref);
+  const bool large = fabsf(top) > kLargeLogit && top > -INFINITY;
+  if (!__any_sync(0xffffffffu, up > kSlack || large)) return false;
+  const bool some = __any_sync(0xffffffffu, large);
+  if (some && SMALL) return true;
+  float f = 1.f;
+  if (up > 0.f) {
+    f = ex2(-0.5f * up);
     row.ref = most;
+    row.norm = norm;
   }
-  row.sum *= ex2(-up);
-  if (!first) scale_rows<D>(o, ex2(row.scale - scale - up));
-  row.scale = scale;
+  row.sum = f * row.sum * f;
+  if (!first && __any_sync(0xffffffffu, f != 1.f)) scale_rows<D>(o, f * f);
+  return some;
 }
 
 // Weights are in TMEM: the product that reads them may start
@@ -174,7 +198,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t s, uint32_t o, bool first,
 #pragma unroll
   for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], x[124 + k]);
   const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mult;
-  move_reference<D>(o, first, most, row.scale, row);
+  move_reference<D, false>(o, first, most, 0.f, row);
   const float base = row.ref == -INFINITY ? 0.f : -row.ref;
   const float2 m2 = make_float2(mult, mult), b2 = make_float2(base, base);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -198,21 +222,26 @@ __device__ __forceinline__ void softmax_tile(uint32_t s, uint32_t o, bool first,
   row.sum += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
-// The same with fp16 weights for the paged cache, whose values come scaled down
-// by 2^scale.  S is read twice, for the maximum and for the weights, 32 columns
-// at a time, each read issued before the columns in hand are worked on: the
-// warps that expand operands leave no registers for a row of 128 logits.  (P's
-// columns reach no further than S's that are read already.)  none: one value a
-// key in shared memory, below 0 where there is no such key; looked at under
-// MASK.  (All exponentials on the special-function unit: the expansion leaves
-// no issue slots to spare; 512 new tokens on 16384 keys, us, with 0 of eight
-// pairs on the FMA pipe 271, with 1 275, 2 281, 3 284.)
+// The same with fp16 weights for the paged cache.  S is read twice, for the
+// maximum and for the weights, 32 columns at a time, each read issued before the
+// columns in hand are worked on: the warps that expand operands leave no
+// registers for a row of 128 logits.  (P's columns reach no further than S's
+// that are read already.)  The tile's values come scaled down by 2^scale, which
+// the weights take back: the reference is of weight times 2^scale, so that P
+// times the operand, in units of the reference, is what O adds up, whatever the
+// other tiles' scales.  (All exponentials on the special-function unit: the
+// expansion leaves no issue slots to spare; 512 new tokens on 16384 keys, us,
+// with 0 of eight pairs on the FMA pipe 271, with 1 275, 2 281, 3 284.)
+//
+// keys: a factor of each key's logit in shared memory, below 0 where there is no
+// such key; under MASK these are left out.  A warp with large logits does nothing
+// and returns false: softmax_tile_own then takes the tile.
 template <bool MASK>
-__device__ __forceinline__ void hide(float (&x)[32], int col, int see, const float *none) {
+__device__ __forceinline__ void hide(float (&x)[32], int col, int see, const float *keys) {
   if constexpr (MASK) {
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
-      const float4 k = *reinterpret_cast<const float4 *>(none + col + i);
+      const float4 k = *reinterpret_cast<const float4 *>(keys + col + i);
       x[i] = k.x < 0.f || col + i >= see ? -INFINITY : x[i];
       x[i + 1] = k.y < 0.f || col + i + 1 >= see ? -INFINITY : x[i + 1];
       x[i + 2] = k.z < 0.f || col + i + 2 >= see ? -INFINITY : x[i + 2];
@@ -221,8 +250,8 @@ __device__ __forceinline__ void hide(float (&x)[32], int col, int see, const flo
   }
 }
 template <int D, bool MASK>
-__device__ __forceinline__ void softmax_tile_twice(uint32_t s, uint32_t o, bool first, float mult, int see, Row &row,
-                                                   const float *none, float scale, uint64_t *half, uint64_t *full) {
+__device__ __forceinline__ bool softmax_tile_twice(uint32_t s, uint32_t o, bool first, float mult, int see, Row &row,
+                                                   const float *keys, float scale, uint64_t *half, uint64_t *full) {
   uint32_t buf[2][32];
   float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
   sm100::tmem_ld32(s, buf[0]);
@@ -231,16 +260,16 @@ __device__ __forceinline__ void softmax_tile_twice(uint32_t s, uint32_t o, bool 
     sm100::tmem_wait_ld();
     sm100::tmem_ld32(s + 32 * ((c + 1) & 3), buf[(c + 1) & 1]);
     float(&x)[32] = reinterpret_cast<float(&)[32]>(buf[c & 1]);
-    hide<MASK>(x, 32 * c, see, none);
+    hide<MASK>(x, 32 * c, see, keys);
 #pragma unroll
     for (int i = 0; i < 32; i += 8)
 #pragma unroll
       for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], fmaxf(x[i + k], x[i + 4 + k]));
   }
-  const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mult;
+  const float highest = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mult;
   sm100::tmem_wait_ld();
-  move_reference<D>(o, first, most, fmaxf(row.scale, scale), row);
-  const float base = row.ref == -INFINITY ? 0.f : -row.ref;
+  if (move_reference<D, true>(o, first, highest, scale, row)) return false;
+  const float base = scale - row.norm - (row.ref == -INFINITY ? 0.f : row.ref);
   const float2 m2 = make_float2(mult, mult), b2 = make_float2(base, base);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 2
@@ -248,7 +277,7 @@ __device__ __forceinline__ void softmax_tile_twice(uint32_t s, uint32_t o, bool 
     sm100::tmem_wait_ld();
     if (c < 3) sm100::tmem_ld32(s + 32 * (c + 1), buf[(c + 1) & 1]);
     float(&x)[32] = reinterpret_cast<float(&)[32]>(buf[c & 1]);
-    hide<MASK>(x, 32 * c, see, none);
+    hide<MASK>(x, 32 * c, see, keys);
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -260,7 +289,59 @@ __device__ __forceinline__ void softmax_tile_twice(uint32_t s, uint32_t o, bool 
     sm100::tmem_st16(s + 16 * c, w);
     if (c & 1) hand_over(c == 1 ? half : full);
   }
-  row.sum += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+  row.sum += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) * ex2(-scale);
+  return true;
+}
+
+// The same tile with a factor of each key's logit, `keys`, and with values scaled
+// down by a factor of each key's own, kFactors behind it.  Products are rounded
+// before the reference is subtracted.  Three passes over S: the highest logit,
+// the largest weight times norm relative to it, the weights.
+constexpr int kFactors = 8 * 128;
+__device__ __forceinline__ void own_logits(uint32_t s, int c, float mult, int see, const float *keys, float (&x)[32]) {
+  sm100::tmem_ld32(s + 32 * c, reinterpret_cast<uint32_t(&)[32]>(x));
+  sm100::tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float k = keys[32 * c + i];
+    x[i] = k < 0.f || 32 * c + i >= see ? -INFINITY : __fmul_rn(x[i] * k, mult);
+  }
+}
+template <int D>
+__device__ __noinline__ Row softmax_tile_own(uint32_t s, uint32_t o, bool first, float mult, int see, Row row,
+                                             const float *keys, uint64_t *half, uint64_t *full) {
+  const float *values = keys + kFactors;
+  float x[32], highest = -INFINITY, norm = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    own_logits(s, c, mult, see, keys, x);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) highest = fmaxf(highest, x[i]);
+  }
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    own_logits(s, c, mult, see, keys, x);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) norm = fmaxf(norm, x[i] - highest + norm_exponent(values[32 * c + i]));
+  }
+  move_reference<D, false>(o, first, highest, norm, row);
+  const float ref = row.ref == -INFINITY ? 0.f : row.ref;
+  float sum = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    own_logits(s, c, mult, see, keys, x);
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 e = make_float2(ex2(x[2 * i] - ref - row.norm), ex2(x[2 * i + 1] - ref - row.norm));
+      sum += e.x + e.y;
+      w[i] = pack16<false>(mul2(e, *reinterpret_cast<const float2 *>(values + 32 * c + 2 * i)));
+    }
+    sm100::tmem_st16(s + 16 * c, w);
+    if (c & 1) hand_over(c == 1 ? half : full);
+  }
+  row.sum += sum;
+  return row;
 }
 
 }  // namespace flash

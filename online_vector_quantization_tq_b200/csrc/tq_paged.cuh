@@ -5,6 +5,7 @@
 
 #include <cuda_fp16.h>
 
+#include "tq_flash.cuh"
 #include "tq_kernels.h"
 #include "tq_sm100.cuh"
 
@@ -96,16 +97,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Rows' references are exponents of weight times value norm (a logit in base 2
-// plus norm_exponent), so the sum of the weights alone, relative to them, may be
-// as large as 2^80 a key and as small as 2^-128: where a reference moves, the
-// sum is multiplied by a root of the factor twice, which loses nothing that
-// matters beside it (a factor of 2^-126 or less is 0, and 80 + 128 < 2 * 126).
+// Parts of a row are added up relative to the largest exponent of weight times
+// value norm (flash::Row), where the sum of the weights alone may be as large as
+// 2^80 a key and as small as 2^-100.  So a part's sum is multiplied by a root of
+// its factor twice, which loses nothing that matters beside the others (a factor
+// of 2^-126 or less is 0, and 80 + 100 < 2 * 126).
 __device__ __forceinline__ float ex2_half(float x) { return ex2(0.5f * x); }
-// Exponent e of a value norm v below 2^e (v >= 0), no less than -80
-__device__ __forceinline__ float norm_exponent(float v) {
-  return fmaxf(__uint_as_float((__float_as_uint(v) >> 23) + 0x4B000000u) - (8388608.f + 126.f), -80.f);
-}
 // Power of two above v (v >= 0), kept where its reciprocal is normal too
 __device__ __forceinline__ float pow2_above(float v) {
   const uint32_t e = (__float_as_uint(v) >> 23) + 1u;  // biased exponent, one up

@@ -454,14 +454,21 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
       for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[q][t][e] = 0.f;
-    float m[NQ][2], l[NQ][2];
-    float limit[NQ][2], base[NQ][2];  // m + 8; m, or 0 while no key was seen
+    // Sums and references.  A reference is a logit and the exponent of a value norm
+    // (kNone: no key was seen), the largest sum of the two among the keys that the
+    // row sees: what the values are multiplied by, weight times norm, stays below
+    // 2^8, and no norm of a key that is hidden or of little weight takes bits from
+    // the others'.  (Apart, since beside a large logit the exponent would be lost
+    // from the weights, but not from the values.)  O and l are rescaled only when a
+    // reference has grown by more than 8.
+    constexpr float kNone = -1e30f;
+    float l[NQ][2], base[NQ][2], norm[NQ][2];
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m[q][e] = limit[q][e] = -INFINITY;
         l[q][e] = base[q][e] = 0.f;
+        norm[q][e] = kNone;
       }
     for (int key0 = k0 + warp * kBlock; key0 < k1; key0 += kStep) {
       cp_async_wait<kStages - 2>();
@@ -576,29 +583,30 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
           if (kk >= seen) vn[i] = 0.f;  // what lies behind the last key may be anything
         }
       }
-      // The exponents' references: the largest logit plus its value norm's
-      // exponent, of the keys that the row sees, so that what the values are
-      // multiplied by, weight times norm, stays below 2^8 and no norm of a key
-      // that is hidden or of little weight takes bits from the others'.  O and l
-      // are rescaled only when a reference has grown by more than 8.
-      const float ve[2] = {norm_exponent(vn[0]), norm_exponent(vn[1])};
+      const float ve[2] = {flash::norm_exponent(vn[0]) - 8.f, flash::norm_exponent(vn[1]) - 8.f};
       bool grow = false;
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) grow |= fmaxf(x[q][0][e] + ve[0], x[q][1][e] + ve[1]) > limit[q][e];
+        for (int e = 0; e < 2; ++e)
+          grow |= fmaxf(x[q][0][e] - base[q][e] + ve[0], x[q][1][e] - base[q][e] + ve[1]) > norm[q][e];
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int q = 0; q < NQ; ++q)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float t = fmaxf(x[q][0][e] + ve[0], x[q][1][e] + ve[1]);
+            float t = fmaxf(x[q][0][e], x[q][1][e]);
 #pragma unroll
             for (int b = 4; b < 32; b <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, b));
-            if (t > m[q][e]) {
-              const float f = ex2_half(m[q][e] - t);
-              m[q][e] = base[q][e] = t;
-              limit[q][e] = t + 8.f;
+            float n = fmaxf(x[q][0][e] - t + ve[0], x[q][1][e] - t + ve[1]);
+#pragma unroll
+            for (int b = 4; b < 32; b <<= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, b));
+            n += 8.f;
+            const float up = t - base[q][e] + (n - norm[q][e]);
+            if (t > -INFINITY && up > 0.f) {
+              const float f = ex2(-0.5f * up);
+              base[q][e] = t;
+              norm[q][e] = n;
               l[q][e] = f * l[q][e] * f;
 #pragma unroll
               for (int k = 0; k < MT; ++k) {
@@ -615,7 +623,7 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) w[i][e] = ex2(x[q][i][e] - base[q][e]);
+          for (int i = 0; i < 2; ++i) w[i][e] = ex2(x[q][i][e] - base[q][e] - norm[q][e]);
           l[q][e] += w[0][e] + w[1][e];
         }
 #pragma unroll
@@ -674,7 +682,7 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
 #pragma unroll
         for (int b = 4; b < 32; b <<= 1) l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], b);
         if (r == 0) {
-          s_m[warp][8 * q + 2 * c + e] = m[q][e];
+          s_m[warp][8 * q + 2 * c + e] = norm[q][e] == kNone ? -INFINITY : base[q][e] + norm[q][e];
           s_l[warp][8 * q + 2 * c + e] = l[q][e];
         }
       }

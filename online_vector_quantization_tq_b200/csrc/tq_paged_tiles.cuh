@@ -5,10 +5,12 @@
 // As the prompt kernel (tq_flash.cuh has the softmax), with key and value tiles
 // that are expanded from the packed pages instead of copied: both products run
 // on tcgen05 with fp16 operands.  A row's operand is its centroids times its
-// norm, scaled down by a power of two that is above all norms of the tile (keys)
-// or of the tiles so far (values) and that the softmax takes back.  Each thread
-// makes a table of its row's 2^w possible values, so that every element is
-// rounded once, and the softmax meets no factors per key.  (As fp32 factors of
+// norm, scaled down by a power of two that is above all norms of the tile, and
+// that the softmax takes back.  A norm less than 1 / kSpread of its tile's scale
+// (which the row may not even see) is scaled by a power of two of its own, and
+// the tile's softmax looks at factors per key.  Each thread makes a table of its
+// row's 2^w possible values, so that every element is rounded once, and the
+// softmax of a tile without such norms meets no factors per key.  (As fp32 factors of
 // logits and weights the norms made the softmax the bound: 316 us instead of
 // 287 on 512 new tokens over 16384 keys.)  Inner-product keys are operands of
 // twice the width, [c | +-64 gamma sqrt(pi/2)/d] times the norm, against queries
@@ -52,9 +54,11 @@ using namespace paged;
 constexpr int kTile = 128;
 constexpr int kTilesThreads = 640;  // warps 17-19 only complete the last warpgroup
 // Registers move to the softmax: a warpgroup's share, whose sum is no more
-// than the block was launched with (launch_tiles checks).
-constexpr int kSoftmaxRegs = 128, kExpandRegs = 72, kMmaRegs = 72;
+// than the block was launched with (launch_tiles checks).  (512 new tokens on
+// 16384 keys, us: 128 / 72 / 72 254, 136 / 72 / 64 247, 136 / 80 / 48 249, these 233.)
+constexpr int kSoftmaxRegs = 144, kExpandRegs = 72, kMmaRegs = 48;
 constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16;
+constexpr float kSpread = 512.f;  // (kept bits: 11 of the largest centroids, 8 or so of the smallest)
 constexpr int kNorms = 8;  // tiles whose scales are kept: more than the ring holds
 
 template <int D, bool IP>
@@ -66,8 +70,10 @@ struct TileSmem {
   static constexpr int kQTiles = IP && D == 128 ? 1 : 2;
   static constexpr int kRows = kTile * kQTiles;          // rows of a block
   static constexpr int kQ = 0, kQTile = kSlot * kWide, kRing = kQTiles * kQTile;
-  static constexpr int kNone = kRing + kSlots * kSlot;  // below 0 for a key on a bad page
-  static constexpr int kBytes = kNone + kNorms * kTile * 4 + 1024;
+  // a factor of each key's logit, below 0 for a key on a bad page, and of its value
+  static constexpr int kKeys = kRing + kSlots * kSlot, kValues = kKeys + kNorms * kTile * 4;
+  static_assert(kNorms * kTile == flash::kFactors, "where the softmax finds the factors of values");
+  static constexpr int kBytes = kValues + kNorms * kTile * 4 + 1024;
 };
 
 // Ring positions of key and value tiles: `lead` key tiles first (one where both
@@ -200,6 +206,18 @@ __device__ __forceinline__ void byte_tables(const float *c, float f, uint32_t (&
 
 // A norm's part in its tile's largest: what is not finite has none
 __device__ __forceinline__ float finite_or_0(float v) { return fabsf(v) < INFINITY ? v : 0.f; }
+// Power of two above v (v >= 0) that scales a tile's norms, as the bits of a
+// float whose reciprocal is normal too; of values no less than 2^-80
+// (flash::norm_exponent)
+constexpr uint32_t kLeastKey = 2, kLeastValue = 127 - 80;
+__device__ __forceinline__ uint32_t scale_bits(float v, uint32_t least) {
+  return min(max((__float_as_uint(v) >> 23) + 1u, least), 252u) << 23;
+}
+__device__ __forceinline__ float inverse_of(uint32_t bits) { return __uint_as_float(0x7F000000u - bits); }
+// Whether norm v of a tile scaled by `bits` has a scale of its own
+__device__ __forceinline__ bool stands_alone(float v, uint32_t bits) {
+  return v > 0.f && v * kSpread < __uint_as_float(bits);
+}
 
 template <int D, bool IP, int WK, int WV>
 __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const __grid_constant__ PagedParams p) {
@@ -207,15 +225,14 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
   constexpr int DQ = IP ? 2 * D : D;  // elements of a query operand's row
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((0u - sm100::smem_u32(smem_raw)) & 1023u);
-  float *s_none = reinterpret_cast<float *>(smem + SM::kNone);
+  float *s_keys = reinterpret_cast<float *>(smem + SM::kKeys), *s_values = reinterpret_cast<float *>(smem + SM::kValues);
   __shared__ uint64_t full[SM::kSlots], empty[SM::kSlots], q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], merge, merged;
   __shared__ uint32_t s_tmem;
   __shared__ int64_t s_run[5];
-  __shared__ int s_some, s_gap[kNorms][4];
+  __shared__ int s_some, s_gap[kNorms][4];          // of a warp's keys: 1 some on a bad page, 2 some scaled by themselves
   __shared__ float s_key[kNorms], s_value[kNorms];  // 2^e of a tile's keys, exponent of its values
   __shared__ float s_top[3][2][4];                  // keys' and values' largest norms, of each warp
   __shared__ float2 s_ml[kTile];
-  __shared__ float s_back;
   __shared__ volatile int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -331,23 +348,23 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
             n.x = -1.f;
           }
         }
-        float exponent = -100.f;
         for (int j = 0; j < g.tiles; ++j) {
           const int pg = page;
           const int64_t row = pg >= 0 ? row_of(j + 1, pg) : 0;
           page = page_of(j + 2);
           const int at = ring.key(j), nr = (ring.before + j) % kNorms;
-          const bool gap = __any_sync(0xffffffffu, n.x < 0.f);
-          const float none = n.x < 0.f ? -1.f : 0.f;
           put_top(0, ring.before + j, fmaxf(n.x, 0.f));
           put_top(1, ring.before + j, v);
           ok = agree(wait_slot(at));
           if (!ok) break;
-          const float e = flash::exponent_above(top_of(0, ring.before + j));
-          exponent = fmaxf(exponent, flash::exponent_above(top_of(1, ring.before + j)));
+          const uint32_t kscale = scale_bits(top_of(0, ring.before + j), kLeastKey);
+          const uint32_t vscale = scale_bits(top_of(1, ring.before + j), kLeastValue);
+          uint32_t kown = kscale, vown = vscale;
+          if (stands_alone(n.x, kscale)) kown = scale_bits(n.x, kLeastKey);
+          if (stands_alone(v, vscale)) vown = scale_bits(v, kLeastValue);
           // a norm that is not finite makes a NaN of every row that sees its key, and of no other
           const float f =
-              v + n.x + (IP ? fabsf(n.y) : 0.f) < INFINITY ? fmaxf(n.x, 0.f) * flash::ex2(-e) : NAN;
+              v + n.x + (IP ? fabsf(n.y) : 0.f) < INFINITY ? fmaxf(n.x, 0.f) * inverse_of(kown) : NAN;
           byte_tables<WK>(p.ckf, f, tlo, thi);
           uint8_t *slot = smem + SM::kRing + (at % SM::kSlots) * SM::kSlot;
 #pragma unroll
@@ -355,11 +372,13 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
             expand_group<WK>(slot, r, q, w[q], tlo, thi);
             if (pg >= 0) load_words<WK>(w[q], p.kcodes + row * (WK * D / 8) + q * (4 * WK));
           }
-          s_none[nr * kTile + r] = none;
+          s_keys[nr * kTile + r] = n.x < 0.f ? -1.f : __uint_as_float(kown) * inverse_of(kscale);
+          s_values[nr * kTile + r] = __uint_as_float(vown);
+          const int gap = __any_sync(0xffffffffu, n.x < 0.f) | __any_sync(0xffffffffu, kown != kscale || vown != vscale) << 1;
           if (lane == 0) s_gap[nr][warp - kKeyWarp] = gap;
           if (r == 0) {
-            s_key[nr] = flash::ex2(e);
-            s_value[nr] = exponent;
+            s_key[nr] = __uint_as_float(kscale);
+            s_value[nr] = (float)((int)(vscale >> 23) - 127);
           }
           sm100::fence_proxy_async();
           sm100::mbar_arrive(&full[at % SM::kSlots]);
@@ -391,7 +410,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
         }
       } else {
         uint32_t w[G][WV];
-        float v = 0.f, exponent = -100.f;
+        float v = 0.f;
         {
           const int pg = page_of(0);
           const int64_t row = pg >= 0 ? row_of(0, pg) : 0;
@@ -411,8 +430,9 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
           put_top(2, ring.before + j, v);
           ok = agree(wait_slot(at));
           if (!ok) break;
-          exponent = fmaxf(exponent, flash::exponent_above(top_of(2, ring.before + j)));  // (as the keys' threads find it)
-          byte_tables<WV>(p.cvf, finite_or_0(v) * flash::ex2(-exponent), tlo, thi);
+          uint32_t own = scale_bits(top_of(2, ring.before + j), kLeastValue);  // (as the keys' threads find it)
+          if (stands_alone(v, own)) own = scale_bits(v, kLeastValue);
+          byte_tables<WV>(p.cvf, finite_or_0(v) * inverse_of(own), tlo, thi);
           uint8_t *slot = smem + SM::kRing + (at % SM::kSlots) * SM::kSlot;
 #pragma unroll
           for (int q = 0; q < G; ++q) {
@@ -554,26 +574,26 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
         ok = sm100::mbar_poll_abort(&s_full[i], (uint32_t)(ns++ & 1), &s_abort, p.err, 125);
         if (!ok) break;
         sm100::tc_fence_after();
-        const float *none = s_none + nr * kTile;
+        const float *keys = s_keys + nr * kTile;
         // (a factor of 0 would turn a masked logit, -inf, into a NaN)
         const float m = fminf(fmaxf(mult * s_key[nr], 1.17549435e-38f), 3.402823466e38f), scale = s_value[nr];
-        const int end = (g.t0 + j + 1) * kTile;
-        if (end > lim_first || (s_gap[nr][0] | s_gap[nr][1] | s_gap[nr][2] | s_gap[nr][3]))
-          flash::softmax_tile_twice<D, true>(S, O, n == 0, m, lim - (end - kTile), st, none, scale, &p_half[i],
-                                                &p_full[i]);
-        else
-          flash::softmax_tile_twice<D, false>(S, O, n == 0, m, 0, st, none, scale, &p_half[i], &p_full[i]);
+        const int end = (g.t0 + j + 1) * kTile, see = lim - (end - kTile);
+        const int gap = s_gap[nr][0] | s_gap[nr][1] | s_gap[nr][2] | s_gap[nr][3];
+        bool done = false;
+        if (gap == 0 && end <= lim_first)
+          done = flash::softmax_tile_twice<D, false>(S, O, n == 0, m, 0, st, keys, scale, &p_half[i], &p_full[i]);
+        else if (gap < 2)
+          done = flash::softmax_tile_twice<D, true>(S, O, n == 0, m, see, st, keys, scale, &p_half[i], &p_full[i]);
+        if (!done) st = flash::softmax_tile_own<D>(S, O, n == 0, m, see, st, keys, &p_half[i], &p_full[i]);
       }
       if (ok && cnt) ok = sm100::mbar_poll_abort(&o_full[i], (uint32_t)(no++ & 1), &s_abort, p.err, 126);
       if (!ok) break;
       sm100::tc_fence_after();
-      float M = st.sum != 0.f ? st.ref : -INFINITY, L = st.sum, f0 = 0.f, f1 = 0.f;
-      const float back = flash::ex2(st.scale);  // the values' scale
-      if (L != 0.f) f0 = back;
+      float M = st.sum != 0.f ? st.exponent() : -INFINITY, L = st.sum, f0 = 0.f, f1 = 0.f;
+      if (L != 0.f) f0 = 1.f;
       if (g.turns) {
         if (i == 1) {
           s_ml[r] = make_float2(M, L);
-          if (r == 0) s_back = back;
           sm100::tc_fence_before();
           sm100::mbar_arrive(&merge);
         } else {
@@ -582,10 +602,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
           sm100::tc_fence_after();
           const float2 b = s_ml[r];
           const float top = fmaxf(M, b.x);
-          const float a0 = L != 0.f ? flash::ex2(M - top) : 0.f, a1 = b.y != 0.f ? flash::ex2(b.x - top) : 0.f;
-          f0 = a0 * back;
-          f1 = a1 * s_back;
-          L = a0 * L + a1 * b.y;
+          const float a0 = L != 0.f ? ex2_half(M - top) : 0.f, a1 = b.y != 0.f ? ex2_half(b.x - top) : 0.f;
+          f0 = a0 * a0;
+          f1 = a1 * a1;
+          L = a0 * L * a0 + a1 * b.y * a1;
           M = top;
         }
       }

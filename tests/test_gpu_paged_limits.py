@@ -142,7 +142,7 @@ def documented(got, y, limits, scale, ke, tk, ve, tv):
 
 
 # (new tokens, query heads of a KV head): few rows, of each block height, and many
-ROWS = [(4, 2), (4, 4), (5, 4), (16, 4)]
+ROWS = [(4, 2), (4, 4), (5, 4), (16, 4), (40, 4), (100, 2), (200, 2)]
 
 
 @pytest.mark.parametrize("n,group", ROWS)
@@ -203,3 +203,39 @@ def test_norms_of_very_different_sizes(tq, d, ip, n, group):  # noqa: F811
         worst = documented(out.double().cpu().numpy().reshape(rows, d), yy, limits, scale,
                            unpack(batch.rows[0][0][0], tk), tk, unpack(batch.rows[1][0][0], tv), tv)
         assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("n,group", ROWS)
+@pytest.mark.parametrize("d,ip,dtype", [(128, False, "bf16"), (128, True, "bf16"), (64, False, "f16"), (64, True, "f16")])
+def test_large_logits(tq, d, ip, dtype, n, group):  # noqa: F811
+    """Logits up to 2^60 (in fp16, whose queries end at 2^16, by the keys' norms):
+    finite results, and a row whose highest logit stands out by more than the
+    rounding of the operands (2^-10 of sum |y| |c|, which is below 2^-5 of the
+    largest) has that key's value."""
+    rng = np.random.default_rng(n + 2)
+    (qk, tk), (qv, tv) = quantizer(tq, d, 4, ip), quantizer(tq, d, 4, False, seed=1)
+    kv, rows = n + 300, n * group
+    batch = Batch(tq, qk, qv, 1, 16, [kv], rng)
+    limits = np.repeat(kv - n + 1 + np.arange(n), group)
+    keys = rng.uniform(8.0, 16.0, kv).astype(np.float32)
+    for up in (12, 18, 24, 30, 60):
+        big = 0 if dtype == "f16" else up
+        set_norms(batch, 0, keys * np.float32(2.0 ** (up - big)))
+        set_norms(batch, 1, rng.uniform(1.0, 64.0, kv).astype(np.float32))
+        ke, ve = unpack(batch.rows[0][0][0], tk), unpack(batch.rows[1][0][0], tv)
+        y = torch.from_numpy(rng.standard_normal((n, group * d)).astype(np.float32) * np.float32(2.0 ** big))
+        y = y.to(DT[dtype]).cuda()
+        out = tq.tq_attend_paged(qk, qv, y, torch.tensor([0, n], dtype=torch.int32, device="cuda"), *batch.caches,
+                                 batch.table_dev, torch.tensor([kv], dtype=torch.int32, device="cuda"), n, 1.0)
+        got = out.double().cpu().numpy().reshape(rows, d)
+        assert np.all(np.isfinite(got)), up
+        yt, p = o.prepare_query(y.double().cpu().numpy().reshape(rows, d), tk)
+        x = np.where(np.arange(kv)[None] < limits[:, None], o.score(yt, p, ke, tk), -np.inf)
+        order = np.sort(x, axis=1)
+        most = np.abs(np.where(np.isfinite(x), x, 0.0)).max(1)
+        clear = order[:, -1] - order[:, -2] > np.maximum(most * 2.0 ** -5, 40.0)
+        assert clear.sum() >= rows / 20
+        best = x.argmax(1)[clear]
+        ref = (ve["norm"][best][:, None] * tv.centroids[ve["codes"][best]]) @ tv.R
+        err = np.linalg.norm(got[clear] - ref, axis=1)
+        assert np.all(err <= 2.0 ** -9 * ve["norm"][best] + 2.0 ** -8 * np.linalg.norm(ref, axis=1)), up
