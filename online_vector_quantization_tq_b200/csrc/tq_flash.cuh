@@ -198,8 +198,13 @@ __device__ __forceinline__ void softmax_tile(uint32_t s, uint32_t o, bool first,
 #pragma unroll
   for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], x[124 + k]);
   const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mult;
-  move_reference<D, false>(o, first, most, 0.f, row);
+  const bool large = move_reference<D, false>(o, first, most, 0.f, row);
   const float base = row.ref == -INFINITY ? 0.f : -row.ref;
+  if (large) {
+#pragma unroll
+    for (int i = 0; i < 128; ++i) x[i] *= mult;
+    mult = 1.f;
+  }
   const float2 m2 = make_float2(mult, mult), b2 = make_float2(base, base);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
