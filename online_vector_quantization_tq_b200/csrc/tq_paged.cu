@@ -332,8 +332,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_paged_join_many(const _
   const Seq s = seq_of(p, s_item[0]);
   const PagedCut c = cut_of(s);
   const Place f = s_place;
-  const int head = s_item[1], first = s_item[2] * c.rows + s_item[3] * kJoinRows;
-  const int rows = min(min(kJoinRows, c.rows), s.n * p.group - first);
+  // the part's rows: no more than its block has (24 rows are two parts, of 16 and 8)
+  const int head = s_item[1], in0 = s_item[3] * kJoinRows, first = s_item[2] * c.rows + in0;
+  const int rows = min(min(kJoinRows, c.rows - in0), s.n * p.group - first);
   for (int r0 = warp; r0 < rows; r0 += N * kWarps) {
     float v[N][V];
     int64_t out[N];
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_paged_join_many(const _
       for (int i = 0; i < N; ++i) {
         M[i] = -INFINITY;
         L[i] = 0.f;
-        in[i] = s_item[3] * kJoinRows + min(r0 + i * kWarps, rows - 1);
+        in[i] = in0 + min(r0 + i * kWarps, rows - 1);
       }
 #pragma unroll 1
       for (int b = f.b0; b <= f.b1; b += kRuns) {
