@@ -539,7 +539,7 @@ def tq_attend_paged(qk: Quantizer, qv: Quantizer, y: torch.Tensor, q_start: torc
     npages, kv_heads, page_size = _check_caches(qk, qv, kcache, vcache)
     ldy, d = _ld_rows(y), qk.d
     total_q, wide = y.shape
-    if wide % (d * kv_heads) != 0:
+    if kv_heads == 0 or wide % (d * kv_heads) != 0:
         raise ValueError(f"y must have a whole number of heads of {d} for each of {kv_heads} KV heads")
     heads = wide // d
     _vector(kv_len, torch.int32, "kv_len")
