@@ -273,14 +273,18 @@ tq_status tq_paged_store(const tq_quantizer *qk, const tq_quantizer *qv, const t
  *       share it with another that may run at the same time.
  * out_h = sum_k softmax_k(scale s_hk) v^_k with s_hk the estimate of tq_score
  * (or, without sign bits, <y, x^_k>) and v^_k = ||v_k|| R^T c[codes_k].  The
- * rotated queries, the centroids (times their norms, for sequences of more
- * than 64 query rows per KV head) and the weights are fp16 operands (each
- * rounded to within 2^-11, under power-of-two scales), products are
- * accumulated in fp32 and the softmax is fp32: out is within about
+ * rotated queries, their projections, the centroids and the weights (times the
+ * value norms) are fp16 operands, each rounded to within 2^-11 under power-of-two
+ * scales; of sequences of more than 64 query rows per KV head the operands of
+ * bf16 calls are centroids times norms, those of sign bits residual norms.
+ * Products are accumulated in fp32 and the softmax is fp32: out is within about
  * 2^-9 sum_k softmax_k ||v_k|| / sqrt(d) of the exact value per coordinate
- * beside its own rounding, for scaled logits up to about 30.  With up to 64
- * rows the centroids' common factor leaves them within 2^-13 and fp16 queries
- * keep 22 bits.  Norms up to 2^100, of any sizes side by side: neither a norm
+ * beside its own rounding, for scaled logits up to about 30.  fp16 calls keep 22
+ * bits of the rotated queries, and there and with up to 64 rows the centroids'
+ * common factor leaves them within 2^-13: what is left, beside the result's own
+ * rounding, is mostly that of the weights (2-norm over 2-norm about 3e-4, with
+ * inner-product keys and sharp heads up to 5e-4).
+ * Norms up to 2^100, of any sizes side by side: neither a norm
  * that a token does not see nor one of little weight takes precision from the
  * others'.  A key, residual or value norm that
  * is not finite makes NaN of the tokens that see it, and of no other; the sign

@@ -239,11 +239,25 @@ __device__ __forceinline__ void softmax_tile(uint32_t s, uint32_t o, bool first,
 // with 0 of eight pairs on the FMA pipe 271, with 1 275, 2 281, 3 284.)
 //
 // keys: a factor of each key's logit in shared memory, below 0 where there is no
-// such key; under MASK these are left out.  A warp with large logits does nothing
-// and returns false: softmax_tile_own then takes the tile.
-template <bool MASK>
+// such key; under MASK these are left out.  EACH: the factors are not all one, and
+// each key's values are scaled down by a factor of their own, kFactors behind it
+// (its exponent kFactors further on), in place of 2^scale.  A warp with large
+// logits does nothing and returns false: softmax_tile_own then takes the tile.
+constexpr int kFactors = 8 * 128;
+template <bool MASK, bool EACH>
 __device__ __forceinline__ void hide(float (&x)[32], int col, int see, const float *keys) {
-  if constexpr (MASK) {
+  if constexpr (EACH) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const float4 k = *reinterpret_cast<const float4 *>(keys + col + i);
+      const float2 a = mul2(make_float2(x[i], x[i + 1]), make_float2(k.x, k.y));
+      const float2 b = mul2(make_float2(x[i + 2], x[i + 3]), make_float2(k.z, k.w));
+      x[i] = MASK && (k.x < 0.f || col + i >= see) ? -INFINITY : a.x;
+      x[i + 1] = MASK && (k.y < 0.f || col + i + 1 >= see) ? -INFINITY : a.y;
+      x[i + 2] = MASK && (k.z < 0.f || col + i + 2 >= see) ? -INFINITY : b.x;
+      x[i + 3] = MASK && (k.w < 0.f || col + i + 3 >= see) ? -INFINITY : b.y;
+    }
+  } else if constexpr (MASK) {
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
       const float4 k = *reinterpret_cast<const float4 *>(keys + col + i);
@@ -254,7 +268,7 @@ __device__ __forceinline__ void hide(float (&x)[32], int col, int see, const flo
     }
   }
 }
-template <int D, bool MASK>
+template <int D, bool MASK, bool EACH>
 __device__ __forceinline__ bool softmax_tile_twice(uint32_t s, uint32_t o, bool first, float mult, int see, Row &row,
                                                    const float *keys, float scale, uint64_t *half, uint64_t *full) {
   uint32_t buf[2][32];
@@ -265,14 +279,25 @@ __device__ __forceinline__ bool softmax_tile_twice(uint32_t s, uint32_t o, bool 
     sm100::tmem_wait_ld();
     sm100::tmem_ld32(s + 32 * ((c + 1) & 3), buf[(c + 1) & 1]);
     float(&x)[32] = reinterpret_cast<float(&)[32]>(buf[c & 1]);
-    hide<MASK>(x, 32 * c, see, keys);
+    hide<MASK, EACH>(x, 32 * c, see, keys);
+    if constexpr (EACH) {
+      const float4 *exps = reinterpret_cast<const float4 *>(keys + 2 * kFactors + 32 * c);
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        const float4 n = exps[i / 4];
+        const float2 a = fma2(make_float2(x[i], x[i + 1]), make_float2(mult, mult), make_float2(n.x, n.y));
+        const float2 b = fma2(make_float2(x[i + 2], x[i + 3]), make_float2(mult, mult), make_float2(n.z, n.w));
+        x[i] = a.x, x[i + 1] = a.y, x[i + 2] = b.x, x[i + 3] = b.y;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 32; i += 8)
 #pragma unroll
       for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], fmaxf(x[i + k], x[i + 4 + k]));
   }
-  const float highest = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mult;
+  const float highest = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * (EACH ? 1.f : mult);
   sm100::tmem_wait_ld();
+  if (EACH) scale = 0.f;  // (in `highest` already)
   if (move_reference<D, true>(o, first, highest, scale, row)) return false;
   const float base = scale - row.norm - (row.ref == -INFINITY ? 0.f : row.ref);
   const float2 m2 = make_float2(mult, mult), b2 = make_float2(base, base);
@@ -282,19 +307,21 @@ __device__ __forceinline__ bool softmax_tile_twice(uint32_t s, uint32_t o, bool 
     sm100::tmem_wait_ld();
     if (c < 3) sm100::tmem_ld32(s + 32 * (c + 1), buf[(c + 1) & 1]);
     float(&x)[32] = reinterpret_cast<float(&)[32]>(buf[c & 1]);
-    hide<MASK>(x, 32 * c, see, keys);
+    hide<MASK, EACH>(x, 32 * c, see, keys);
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float2 e = fma2(make_float2(x[2 * i], x[2 * i + 1]), m2, b2);
       e = make_float2(ex2(e.x), ex2(e.y));
       sum[i & 1] = add2(sum[i & 1], e);
+      if constexpr (EACH) e = mul2(e, *reinterpret_cast<const float2 *>(keys + kFactors + 32 * c + 2 * i));
       w[i] = pack16<false>(e);
     }
     sm100::tmem_st16(s + 16 * c, w);
     if (c & 1) hand_over(c == 1 ? half : full);
   }
-  row.sum += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) * ex2(-scale);
+  const float total = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+  row.sum += EACH ? total : total * ex2(-scale);
   return true;
 }
 
@@ -302,7 +329,6 @@ __device__ __forceinline__ bool softmax_tile_twice(uint32_t s, uint32_t o, bool 
 // down by a factor of each key's own, kFactors behind it.  Products are rounded
 // before the reference is subtracted.  Three passes over S: the highest logit,
 // the largest weight times norm relative to it, the weights.
-constexpr int kFactors = 8 * 128;
 __device__ __forceinline__ void own_logits(uint32_t s, int c, float mult, int see, const float *keys, float (&x)[32]) {
   sm100::tmem_ld32(s + 32 * c, reinterpret_cast<uint32_t(&)[32]>(x));
   sm100::tmem_wait_ld();

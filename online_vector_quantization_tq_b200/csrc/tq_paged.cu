@@ -124,17 +124,18 @@ __global__ void __launch_bounds__(256) k_paged_store(const __grid_constant__ Sto
 // Rotated queries (and their projections) of all rows as fp16 operands of the
 // kernel of many rows: row (token * heads + head) is R y / U, and for
 // inner-product keys S R y / (64 U) behind it, U a power of two above the row's
-// largest coordinate, which goes to qscale.  Coordinates stand where the
+// largest coordinate, which goes to qscale; of fp16 queries (LOW) at last what
+// the rounding of R y / U left over.  Coordinates stand where the
 // expansion of packed codes and signs puts them.  One thread a row, 64 rows a
 // block; the projection on the tensor cores, with y~ as two fp16 terms.
 // (37000 rows of d = 128 with the projection: 30 us; by a warp a row, 16 rows a
 // block, 115 us.)
 constexpr int kQueryRows = 64;
 
-template <int D, bool IP>
+template <int D, bool IP, bool LOW>
 __global__ void __launch_bounds__(kQueryRows) k_paged_queries(const __grid_constant__ PagedParams p, int w) {
-  constexpr int DQ = IP ? 2 * D : D, LD = D + 8;  // padded rows: fragments of 8 rows fall into different banks
-  __shared__ __align__(16) uint16_t yh[kQueryRows * LD], yl[IP ? kQueryRows * LD : 1];
+  constexpr int DQ = (1 + IP + LOW) * D, LD = D + 8;  // padded rows: fragments of 8 rows fall into different banks
+  __shared__ __align__(16) uint16_t yh[kQueryRows * LD], yl[IP || LOW ? kQueryRows * LD : 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row0 = (int64_t)blockIdx.x * kQueryRows, total = p.total_q * p.heads, row = row0 + tid;
   {
@@ -164,13 +165,37 @@ __global__ void __launch_bounds__(kQueryRows) k_paged_queries(const __grid_const
       const float2 x = make_float2(v[e] * down, v[e + 1] * down);
       const __half2 hi = __floats2half2_rn(x.x, x.y);
       *reinterpret_cast<__half2 *>(yh + tid * LD + e) = hi;
-      if constexpr (IP) {
+      if constexpr (IP || LOW) {
         const float2 h = __half22float2(hi);
         *reinterpret_cast<__half2 *>(yl + tid * LD + e) = __floats2half2_rn(x.x - h.x, x.y - h.y);
       }
     }
   }
   __syncthreads();
+  // 16-byte pieces, neighbours by neighbouring threads
+  const int rows = (int)min((int64_t)kQueryRows, total - row0);
+  uint4 *to = reinterpret_cast<uint4 *>(p.qprep + row0 * DQ);
+  auto put = [&](const uint16_t *part, int at, bool codes) {  // codes: in the order of the codes' operands
+    for (int i = tid; i < rows * (D / 8); i += kQueryRows) {
+      const int r = i / (D / 8), c = i % (D / 8);
+      uint4 x;
+      if (!codes || w != 1) {
+        x = *reinterpret_cast<const uint4 *>(part + r * LD + c * 8);
+      } else {  // one-bit codes: byte 8 (j % 4) + j / 4 of a group is coordinate j
+        uint32_t q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int b = (8 * c + 2 * e) % 32;  // coordinates of positions b and b + 1
+          const uint16_t *g = part + r * LD + 8 * c / 32 * 32;
+          q[e] = g[4 * (b % 8) + b / 8] | (uint32_t)g[4 * (b % 8 + 1) + b / 8] << 16;
+        }
+        x = make_uint4(q[0], q[1], q[2], q[3]);
+      }
+      to[r * (DQ / 8) + at / 8 + c] = x;
+    }
+  };
+  put(yh, 0, true);
+  if constexpr (LOW) put(yl, (1 + IP) * D, true);
   float acc[IP ? 2 : 1][IP ? D / 8 : 1][4];  // projections of the warp's 32 rows
   if constexpr (IP) {
     const int r = lane >> 2, c = lane & 3;
@@ -215,28 +240,7 @@ __global__ void __launch_bounds__(kQueryRows) k_paged_queries(const __grid_const
         }
     __syncthreads();
   }
-  // 16-byte pieces, neighbours by neighbouring threads
-  const int rows = (int)min((int64_t)kQueryRows, total - row0);
-  uint4 *to = reinterpret_cast<uint4 *>(p.qprep + row0 * DQ);
-  for (int i = tid; i < rows * (DQ / 8); i += kQueryRows) {
-    const int r = i / (DQ / 8), c = i % (DQ / 8);
-    uint4 x;
-    if (IP && c >= D / 8) {
-      x = *reinterpret_cast<const uint4 *>(yl + r * LD + (c - D / 8) * 8);
-    } else if (w != 1) {
-      x = *reinterpret_cast<const uint4 *>(yh + r * LD + c * 8);
-    } else {  // one-bit codes: byte 8 (j % 4) + j / 4 of a group is coordinate j
-      uint32_t q[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int b = (8 * c + 2 * e) % 32;  // coordinates of positions b and b + 1
-        const uint16_t *g = yh + r * LD + 8 * c / 32 * 32;
-        q[e] = g[4 * (b % 8) + b / 8] | (uint32_t)g[4 * (b % 8 + 1) + b / 8] << 16;
-      }
-      x = make_uint4(q[0], q[1], q[2], q[3]);
-    }
-    to[i] = x;
-  }
+  if constexpr (IP) put(yl, D, false);
 }
 
 // ---------------------------------------------------------------- join
@@ -508,7 +512,7 @@ Plan plan_of(const tq_quantizer *qk, bool f16, int64_t total_q, int64_t nseq, in
   // 16 sequences, d = 64); at d = 128 its registers do not suffice.
   const int rows = most <= 8 && !(f16 && d == 128) ? 8 : d == 64 && most > 16 && most <= 24 ? 24 : 16;
   L.few = PagedCut{rows, 6, 0, many ? kFewRows : 0x7fffffff, sms, 4, nullptr, nullptr, nullptr};
-  if (many) L.many = PagedCut{ip && d == 128 ? 128 : 256, 7, kFewRows, 0x7fffffff, sms, 2, nullptr, nullptr, nullptr};
+  if (many) L.many = PagedCut{paged_tile_rows(d, ip, f16), 7, kFewRows, 0x7fffffff, sms, 2, nullptr, nullptr, nullptr};
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -523,7 +527,7 @@ Plan plan_of(const tq_quantizer *qk, bool f16, int64_t total_q, int64_t nseq, in
   cut(L.few, L.few_o, L.few_ml, L.few_first);
   cut(L.many, L.many_o, L.many_ml, L.many_first);
   L.whole = take((size_t)total_q * heads * d * sizeof(float));
-  L.qprep = take(many ? (size_t)total_q * heads * d * (ip ? 4 : 2) : 0);
+  L.qprep = take(many ? (size_t)total_q * heads * d * 2 * (1 + ip + f16) : 0);
   L.qscale = take(many ? (size_t)total_q * heads * sizeof(float) : 0);
   L.total = off + 256;
   return L;
@@ -535,10 +539,9 @@ tq_status launch_paged(const PagedParams &prm, const tq_quantizer *qk, const tq_
   const int64_t rows = prm.total_q * prm.heads;
   if (prm.many.grid > 0) {
     const unsigned blocks = (unsigned)((rows + kQueryRows - 1) / kQueryRows);
-    if (qk->m)
-      k_paged_queries<D, true><<<blocks, kQueryRows, 0, st>>>(prm, qk->w);
-    else
-      k_paged_queries<D, false><<<blocks, kQueryRows, 0, st>>>(prm, qk->w);
+    auto kern = qk->m ? (prm.bf16 ? k_paged_queries<D, true, false> : k_paged_queries<D, true, true>)
+                      : (prm.bf16 ? k_paged_queries<D, false, false> : k_paged_queries<D, false, true>);
+    kern<<<blocks, kQueryRows, 0, st>>>(prm, qk->w);
     if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
     rc = qk->m ? paged_tiles_launch<D, true>(prm, qk->w, qv->w, st) : paged_tiles_launch<D, false>(prm, qk->w, qv->w, st);
     if (rc != TQ_OK) return rc;

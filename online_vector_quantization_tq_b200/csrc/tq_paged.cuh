@@ -55,10 +55,16 @@ struct PagedParams {
   int64_t ldo;
   PagedCut few, many;  // for the kernel of few rows and the kernel of many (its grid 0: not launched)
   float *whole;     // [total_q * heads][D]: normalized rows of blocks that one run had whole, rotated domain
-  uint16_t *qprep;  // many: [total_q * heads][D or 2 D] rotated queries, and their projections, fp16
+  // many: [total_q * heads][D to 3 D] rotated queries, then their projections (inner-product keys), then the
+  // rotated queries' low terms (fp16 queries), fp16
+  uint16_t *qprep;
   float *qscale;    // many: [total_q * heads] power of two that undoes their scaling
   int *err;
 };
+
+// Rows of a block of the kernel of many rows: two query tiles of 128, or one where
+// two would leave no room for keys.  low: of fp16 queries
+constexpr int paged_tile_rows(int d, bool ip, bool low) { return (ip || low) && d == 128 ? 128 : 256; }
 
 // Few rows: one kernel per (D, inner-product keys) file, chosen by the code
 // widths of keys and values.  Many rows: likewise.

@@ -16,13 +16,20 @@
 // twice the width, [c | +-64 gamma sqrt(pi/2)/d] times the norm, against queries
 // [R y | S R y / 64].
 //
+// fp16 results (LOW) would show the rounding of these operands: their centroids
+// are operands under the codebook's common factor, within 2^-13, with the norms as
+// fp32 factors of logits and weights, and the rotated queries' low terms are
+// multiplied too, as a third part [R y | S R y / 64 | low] of the query tile,
+// against the centroids once more.  (Error against 64 bits, 2-norm over 2-norm:
+// 1.5e-3 before, 2.0e-4 the result's own rounding.)
+//
 // One block per SM works off its run of units (PagedCut; a unit is a tile of
 // 128 keys).  Two warpgroups of softmax share the tensor cores:
 //   a block of more than 128 rows: each has a tile of 128 of the rows, and
 //     both go through the same key tiles;
-//   fewer rows (and inner-product keys of d = 128, whose two query tiles would
-//     leave no room for keys): both have the same rows, and take the key tiles
-//     in turn; their results are added up at the end.
+//   fewer rows (and, at d = 128, inner-product keys and fp16, whose two query
+//     tiles would leave no room for keys): both have the same rows, and take the
+//     key tiles in turn; their results are added up at the end.
 //
 //   warps 0-3, 4-7   softmax; they also fetch their queries and put out results
 //   warps 8-11       expand keys, one row a thread; norms
@@ -61,19 +68,21 @@ constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16;
 constexpr float kSpread = 512.f;  // (kept bits: 11 of the largest centroids, 8 or so of the smallest)
 constexpr int kNorms = 8;  // tiles whose scales are kept: more than the ring holds
 
-template <int D, bool IP>
+template <int D, bool IP, bool LOW>
 struct TileSmem {
   static constexpr int kHalf = kTile * 128;              // 128 rows of 64 elements
   static constexpr int kSlot = kHalf * (D / 64);
-  static constexpr int kSlots = D == 64 ? 8 : 4;
+  static constexpr int kSlots = D == 64 ? (IP && LOW ? 6 : 8) : (IP && LOW ? 3 : 4);
   static constexpr int kWide = IP ? 2 : 1;               // slots of a key tile
-  static constexpr int kQTiles = IP && D == 128 ? 1 : 2;
+  static constexpr int kParts = kWide + (LOW ? 1 : 0);   // of a query tile
+  static constexpr int kQTiles = (IP || LOW) && D == 128 ? 1 : 2;
   static constexpr int kRows = kTile * kQTiles;          // rows of a block
-  static constexpr int kQ = 0, kQTile = kSlot * kWide, kRing = kQTiles * kQTile;
+  static constexpr int kQ = 0, kQTile = kSlot * kParts, kRing = kQTiles * kQTile;
   // a factor of each key's logit, below 0 for a key on a bad page, and of its value
   static constexpr int kKeys = kRing + kSlots * kSlot, kValues = kKeys + kNorms * kTile * 4;
   static_assert(kNorms * kTile == flash::kFactors, "where the softmax finds the factors of values");
-  static constexpr int kBytes = kValues + kNorms * kTile * 4 + 1024;
+  static constexpr int kExps = kValues + kNorms * kTile * 4;  // LOW: the values' exponents
+  static constexpr int kBytes = kExps + (LOW ? kNorms * kTile * 4 : 0) + 1024;
 };
 
 // Ring positions of key and value tiles: `lead` key tiles first (one where both
@@ -83,8 +92,8 @@ struct TileSmem {
 // told from the one before the last because a filler's positions are never
 // more than the ring's slots apart, and slots become free in (nearly) the order
 // of their positions.  Where every key tile has two of the four slots, starting
-// each segment with its own lead would set value tiles five apart: there the
-// order runs on from one segment to the next.
+// each segment with its own lead would set value tiles five apart: there (and
+// with three slots) the order runs on from one segment to the next.
 template <int WIDE, bool ON>
 struct RingPlan {
   int lead, tiles;
@@ -103,8 +112,8 @@ struct RingPlan {
   }
 };
 
-template <int D, bool IP>
-using Ring = RingPlan<TileSmem<D, IP>::kWide, IP && D == 128>;
+template <int D, bool IP, bool LOW>
+using Ring = RingPlan<TileSmem<D, IP, LOW>::kWide, IP && D == 128>;
 
 // Tiles of a segment, as every role sees them
 struct Segment {
@@ -113,9 +122,9 @@ struct Segment {
   int hidden, seen;
   int t0, tiles;  // key tiles
 };
-template <int D, bool IP>
+template <int D, bool IP, bool LOW>
 __device__ __forceinline__ Segment segment_of(const PagedParams &p, const Cursor &cur) {
-  using SM = TileSmem<D, IP>;
+  using SM = TileSmem<D, IP, LOW>;
   Segment g;
   g.rows = cur.s.n * p.group;
   g.row0 = cur.block * SM::kRows;
@@ -204,6 +213,22 @@ __device__ __forceinline__ void byte_tables(const float *c, float f, uint32_t (&
   }
 }
 
+// The same of fp16 centroids as they are
+template <int W>
+__device__ __forceinline__ void byte_tables(const uint16_t *c, uint32_t (&lo)[4], uint32_t (&hi)[4]) {
+  constexpr int kFirst = W == 4 ? 8 : 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    lo[i] = hi[i] = 0u;
+    if (4 * i < (W == 4 ? 8 : 1 << W)) {
+      const uint32_t a = c[kFirst + 4 * i] | (uint32_t)c[kFirst + 4 * i + 1] << 16;
+      const uint32_t b = c[kFirst + 4 * i + 2] | (uint32_t)c[kFirst + 4 * i + 3] << 16;
+      lo[i] = sm100::prmt(a, b, 0x6420u);
+      hi[i] = sm100::prmt(a, b, 0x7531u);
+    }
+  }
+}
+
 // A norm's part in its tile's largest: what is not finite has none
 __device__ __forceinline__ float finite_or_0(float v) { return fabsf(v) < INFINITY ? v : 0.f; }
 // Power of two above v (v >= 0) that scales a tile's norms, as the bits of a
@@ -219,10 +244,10 @@ __device__ __forceinline__ bool stands_alone(float v, uint32_t bits) {
   return v > 0.f && v * kSpread < __uint_as_float(bits);
 }
 
-template <int D, bool IP, int WK, int WV>
+template <int D, bool IP, bool LOW, int WK, int WV>
 __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const __grid_constant__ PagedParams p) {
-  using SM = TileSmem<D, IP>;
-  constexpr int DQ = IP ? 2 * D : D;  // elements of a query operand's row
+  using SM = TileSmem<D, IP, LOW>;
+  constexpr int DQ = SM::kParts * D;  // elements of a query operand's row
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((0u - sm100::smem_u32(smem_raw)) & 1023u);
   float *s_keys = reinterpret_cast<float *>(smem + SM::kKeys), *s_values = reinterpret_cast<float *>(smem + SM::kValues);
@@ -267,7 +292,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
   sm100::tc_fence_after();
   const uint32_t tmem = s_tmem;
   Cursor cur = start_run(p, p.many, s_run);
-  Ring<D, IP> ring{1, 0, 0, 0};
+  Ring<D, IP, LOW> ring{1, 0, 0, 0};
   // the next segment's tiles in the ring
   auto enter = [&](const Segment &g) {
     ring.lead = g.turns ? 2 : 1;
@@ -300,9 +325,15 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
     };
     auto agree = [&](bool mine) { return !sm100::named_barrier_or(keys ? 1 : 2, kTile, !mine); };
     constexpr int kBehind = -2;  // a page index: the key lies behind those that are seen
+    if constexpr (LOW) {
+      if (keys)
+        byte_tables<WK>(p.ck, tlo, thi);
+      else
+        byte_tables<WV>(p.cv, tlo, thi);
+    }
     bool ok = true;
     do {
-      const Segment g = segment_of<D, IP>(p, cur);
+      const Segment g = segment_of<D, IP, LOW>(p, cur);
       enter(g);
       const int32_t *table = p.table + (int64_t)cur.seq * p.ldt;
       const int64_t page_rows = (int64_t)p.kv_heads * p.page_size, head_row = (int64_t)cur.head * p.page_size;
@@ -353,25 +384,31 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
           const int64_t row = pg >= 0 ? row_of(j + 1, pg) : 0;
           page = page_of(j + 2);
           const int at = ring.key(j), nr = (ring.before + j) % kNorms;
-          put_top(0, ring.before + j, fmaxf(n.x, 0.f));
-          put_top(1, ring.before + j, v);
+          if constexpr (!LOW) {
+            put_top(0, ring.before + j, fmaxf(n.x, 0.f));
+            put_top(1, ring.before + j, v);
+          }
           ok = agree(wait_slot(at));
           if (!ok) break;
+          // a norm that is not finite makes a NaN of every row that sees its key, and of no other
+          const bool finite = v + n.x + (IP ? fabsf(n.y) : 0.f) < INFINITY;
+          float signs_by;  // factor of the sign bits' operand
+          if constexpr (LOW) {
+            s_keys[nr * kTile + r] = finite ? n.x : NAN;
+            s_values[nr * kTile + r] = finite ? v : 0.f;
+            reinterpret_cast<float *>(smem + SM::kExps)[nr * kTile + r] = flash::norm_exponent(finite ? v : 0.f);
+            const int gap = __any_sync(0xffffffffu, n.x < 0.f);
+            if (lane == 0) s_gap[nr][warp - kKeyWarp] = gap;
+            signs_by = 1.f / p.kunit;
+          } else {
           const uint32_t kscale = scale_bits(top_of(0, ring.before + j), kLeastKey);
           const uint32_t vscale = scale_bits(top_of(1, ring.before + j), kLeastValue);
           uint32_t kown = kscale, vown = vscale;
           if (stands_alone(n.x, kscale)) kown = scale_bits(n.x, kLeastKey);
           if (stands_alone(v, vscale)) vown = scale_bits(v, kLeastValue);
-          // a norm that is not finite makes a NaN of every row that sees its key, and of no other
-          const float f =
-              v + n.x + (IP ? fabsf(n.y) : 0.f) < INFINITY ? fmaxf(n.x, 0.f) * inverse_of(kown) : NAN;
+          const float f = finite ? fmaxf(n.x, 0.f) * inverse_of(kown) : NAN;
           byte_tables<WK>(p.ckf, f, tlo, thi);
-          uint8_t *slot = smem + SM::kRing + (at % SM::kSlots) * SM::kSlot;
-#pragma unroll
-          for (int q = 0; q < G; ++q) {
-            expand_group<WK>(slot, r, q, w[q], tlo, thi);
-            if (pg >= 0) load_words<WK>(w[q], p.kcodes + row * (WK * D / 8) + q * (4 * WK));
-          }
+          signs_by = f;
           s_keys[nr * kTile + r] = n.x < 0.f ? -1.f : __uint_as_float(kown) * inverse_of(kscale);
           s_values[nr * kTile + r] = __uint_as_float(vown);
           const int gap = __any_sync(0xffffffffu, n.x < 0.f) | __any_sync(0xffffffffu, kown != kscale || vown != vscale) << 1;
@@ -380,13 +417,20 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
             s_key[nr] = __uint_as_float(kscale);
             s_value[nr] = (float)((int)(vscale >> 23) - 127);
           }
+          }
+          uint8_t *slot = smem + SM::kRing + (at % SM::kSlots) * SM::kSlot;
+#pragma unroll
+          for (int q = 0; q < G; ++q) {
+            expand_group<WK>(slot, r, q, w[q], tlo, thi);
+            if (pg >= 0) load_words<WK>(w[q], p.kcodes + row * (WK * D / 8) + q * (4 * WK));
+          }
           sm100::fence_proxy_async();
           sm100::mbar_arrive(&full[at % SM::kSlots]);
           if constexpr (IP) {
             ok = agree(wait_slot(at + 1));
             if (!ok) break;
             uint8_t *signs = smem + SM::kRing + ((at + 1) % SM::kSlots) * SM::kSlot;
-            const uint32_t h = __half_as_ushort(__float2half_rn(f * n.y * (64.f * p.kappa)));
+            const uint32_t h = __half_as_ushort(__float2half_rn(signs_by * n.y * (64.f * p.kappa)));
             const uint32_t minus = (h | h << 16) ^ 0x80008000u;
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {  // elements 2 k and 2 k + 1 of a group: bits k and k + 16 of its word
@@ -420,19 +464,21 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
             for (int i = 0; i < WV; ++i) w[q][i] = 0u;
             if (pg >= 0) load_words<WV>(w[q], p.vcodes + row * (WV * D / 8) + q * (4 * WV));
           }
-          if (pg >= 0) v = fabsf(__ldg(&p.vnorms[row].x));
+          if (!LOW && pg >= 0) v = fabsf(__ldg(&p.vnorms[row].x));
         }
         for (int j = 0; j < g.tiles; ++j) {
           const int pg = page;
           const int64_t row = pg >= 0 ? row_of(j + 1, pg) : 0;
           page = page_of(j + 2);
           const int at = ring.value(j);
-          put_top(2, ring.before + j, v);
+          if constexpr (!LOW) put_top(2, ring.before + j, v);
           ok = agree(wait_slot(at));
           if (!ok) break;
-          uint32_t own = scale_bits(top_of(2, ring.before + j), kLeastValue);  // (as the keys' threads find it)
-          if (stands_alone(v, own)) own = scale_bits(v, kLeastValue);
-          byte_tables<WV>(p.cvf, finite_or_0(v) * inverse_of(own), tlo, thi);
+          if constexpr (!LOW) {
+            uint32_t own = scale_bits(top_of(2, ring.before + j), kLeastValue);  // (as the keys' threads find it)
+            if (stands_alone(v, own)) own = scale_bits(v, kLeastValue);
+            byte_tables<WV>(p.cvf, finite_or_0(v) * inverse_of(own), tlo, thi);
+          }
           uint8_t *slot = smem + SM::kRing + (at % SM::kSlots) * SM::kSlot;
 #pragma unroll
           for (int q = 0; q < G; ++q) {
@@ -440,7 +486,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
             if (pg >= 0) load_words<WV>(w[q], p.vcodes + row * (WV * D / 8) + q * (4 * WV));
           }
           v = 0.f;
-          if (pg >= 0) v = fabsf(__ldg(&p.vnorms[row].x));
+          if (!LOW && pg >= 0) v = fabsf(__ldg(&p.vnorms[row].x));
           sm100::fence_proxy_async();
           sm100::mbar_arrive(&full[at % SM::kSlots]);
         }
@@ -459,7 +505,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
         return sm100::mbar_poll_abort(&full[at % SM::kSlots], (uint32_t)((at / SM::kSlots) & 1), &s_abort, p.err, 122);
       };
       do {
-        const Segment g = segment_of<D, IP>(p, cur);
+        const Segment g = segment_of<D, IP, LOW>(p, cur);
         enter(g);
         const int cnt[2] = {tiles_of(p, cur, g, 0), tiles_of(p, cur, g, 1)};
         auto logits = [&](int i, int j) {  // S_i = Q K_j^T
@@ -475,6 +521,14 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
             for (int ks = 0; ks < D / 16; ++ks) {
               const uint32_t off = ((ks / 4) * SM::kHalf + (ks % 4) * 32) / 16;
               sm100::mma_f16(tmem + kTile * i, q + (w * SM::kSlot / 16 + off), k + off, iqk, (w | ks) != 0);
+            }
+            if constexpr (LOW) {
+              if (w == 0)
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                  const uint32_t off = ((ks / 4) * SM::kHalf + (ks % 4) * 32) / 16;
+                  sm100::mma_f16(tmem + kTile * i, q + (SM::kWide * SM::kSlot / 16 + off), k + off, iqk, true);
+                }
             }
           }
           sm100::mma_commit(&s_full[i]);
@@ -544,11 +598,11 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
     const int i = warp >> 2, r = tid & (kTile - 1);
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t S = tmem + kTile * i + lanes, O = tmem + 2 * kTile + kTile * i + lanes;
-    const float unit = fabsf(p.scale) * 1.4426950408889634f;
+    const float unit = fabsf(p.scale) * 1.4426950408889634f * (LOW ? p.kunit : 1.f);
     int ns = 0, no = 0, nm = 0;  // uses of s_full, of o_full, of merge
     bool ok = true;
     do {
-      const Segment g = segment_of<D, IP>(p, cur);
+      const Segment g = segment_of<D, IP, LOW>(p, cur);
       enter(g);
       const int cnt = tiles_of(p, cur, g, i);
       const int first = g.row0 + (g.turns ? 0 : kTile * i), row = first + r;
@@ -575,21 +629,23 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
         if (!ok) break;
         sm100::tc_fence_after();
         const float *keys = s_keys + nr * kTile;
-        // (a factor of 0 would turn a masked logit, -inf, into a NaN)
-        const float m = fminf(fmaxf(mult * s_key[nr], 1.17549435e-38f), 3.402823466e38f), scale = s_value[nr];
         const int end = (g.t0 + j + 1) * kTile, see = lim - (end - kTile);
         const int gap = s_gap[nr][0] | s_gap[nr][1] | s_gap[nr][2] | s_gap[nr][3];
+        // (a factor of 0 would turn a masked logit, -inf, into a NaN)
+        const float m = fminf(fmaxf(LOW ? mult : mult * s_key[nr], 1.17549435e-38f), 3.402823466e38f);
+        const float scale = LOW ? 0.f : s_value[nr];
         bool done = false;
         if (gap == 0 && end <= lim_first)
-          done = flash::softmax_tile_twice<D, false>(S, O, n == 0, m, 0, st, keys, scale, &p_half[i], &p_full[i]);
+          done = flash::softmax_tile_twice<D, false, LOW>(S, O, n == 0, m, 0, st, keys, scale, &p_half[i], &p_full[i]);
         else if (gap < 2)
-          done = flash::softmax_tile_twice<D, true>(S, O, n == 0, m, see, st, keys, scale, &p_half[i], &p_full[i]);
+          done = flash::softmax_tile_twice<D, true, LOW>(S, O, n == 0, m, see, st, keys, scale, &p_half[i], &p_full[i]);
         if (!done) st = flash::softmax_tile_own<D>(S, O, n == 0, m, see, st, keys, &p_half[i], &p_full[i]);
       }
       if (ok && cnt) ok = sm100::mbar_poll_abort(&o_full[i], (uint32_t)(no++ & 1), &s_abort, p.err, 126);
       if (!ok) break;
       sm100::tc_fence_after();
       float M = st.sum != 0.f ? st.exponent() : -INFINITY, L = st.sum, f0 = 0.f, f1 = 0.f;
+      const float back = LOW ? p.vunit : 1.f;  // of the values' operands
       if (L != 0.f) f0 = 1.f;
       if (g.turns) {
         if (i == 1) {
@@ -620,6 +676,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
         } else if (mine) {
           p.many.part_ml[slot] = make_float2(M, L);
         }
+        f0 *= back;
+        f1 *= back;
         const bool other = g.turns && __any_sync(0xffffffffu, f1 != 0.f);
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -668,11 +726,13 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
   if (warp == kMmaWarp) sm100::tmem_dealloc(tmem, 512);
 }
 
-template <int D, bool IP, int WK, int WV>
+template <int D, bool IP, bool LOW, int WK, int WV>
 tq_status launch_tiles(const PagedParams &prm, cudaStream_t st) {
-  auto kern = k_attend_paged_tiles<D, IP, WK, WV>;
-  constexpr int smem = TileSmem<D, IP>::kBytes;
+  using SM = TileSmem<D, IP, LOW>;
+  auto kern = k_attend_paged_tiles<D, IP, LOW, WK, WV>;
+  constexpr int smem = SM::kBytes;
   static_assert(smem <= 232448 - 8192, "shared memory");
+  static_assert(SM::kRows == paged_tile_rows(D, IP, LOW), "the plan's blocks of rows");
   static std::atomic<uint64_t> ready{0};
   const tq_status rc = once_per_device(ready, [&] {
     cudaFuncAttributes fa;  // (a split of registers beyond what the block holds would wait for ever)
@@ -685,12 +745,17 @@ tq_status launch_tiles(const PagedParams &prm, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
+template <int D, bool IP, int WK, int WV>
+tq_status launch_tiles_low(const PagedParams &prm, cudaStream_t st) {
+  return prm.bf16 ? launch_tiles<D, IP, false, WK, WV>(prm, st) : launch_tiles<D, IP, true, WK, WV>(prm, st);
+}
+
 template <int D, bool IP, int WK>
 tq_status launch_tiles_wv(const PagedParams &prm, int wv, cudaStream_t st) {
   switch (wv) {
-    case 2: return launch_tiles<D, IP, WK, 2>(prm, st);
-    case 3: return launch_tiles<D, IP, WK, 3>(prm, st);
-    case 4: return launch_tiles<D, IP, WK, 4>(prm, st);
+    case 2: return launch_tiles_low<D, IP, WK, 2>(prm, st);
+    case 3: return launch_tiles_low<D, IP, WK, 3>(prm, st);
+    case 4: return launch_tiles_low<D, IP, WK, 4>(prm, st);
   }
   return TQ_ERR_UNSUPPORTED;
 }

@@ -236,7 +236,8 @@ class Model:
 
 
 # slots, slots of a key tile, order that runs on, whether blocks of two query tiles occur
-VARIANTS = [(4, 1, False, True), (8, 1, False, True), (8, 2, False, True), (4, 2, True, False)]
+VARIANTS = [(4, 1, False, True), (8, 1, False, True), (8, 2, False, True), (4, 2, True, False),
+            (4, 1, False, False), (6, 2, False, True), (3, 2, True, False)]  # the last three: fp16
 
 
 def segments(rng, tall, first_unseen):
