@@ -207,7 +207,7 @@ tq_status tq_attend(const tq_quantizer *qv, const float *logits, int64_t ldl, in
  * its output, whatever it holds.  Takes no workspace; lengths are read on the
  * device, so a captured call can be replayed with others.  A bounded wait that
  * ran out is reported by tq_sync_check(q).
- * total is at most 2^27.  total == 0 or nseq == 0: no-op. */
+ * total is at most 2^27, nseq at most 2^18.  total == 0 or nseq == 0: no-op. */
 tq_status tq_attend_prompt(const tq_quantizer *q, tq_dtype dtype, const void *y, int64_t ldy, const void *k,
                            int64_t ldk, const void *v, int64_t ldv, int64_t total,
                            const int32_t *cu_seqlens, int64_t nseq, int64_t heads, int64_t kv_heads,

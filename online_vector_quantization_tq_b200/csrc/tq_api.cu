@@ -145,7 +145,8 @@ tq_status tq_attend_prompt(const tq_quantizer *q, tq_dtype dtype, const void *y,
   if ((q->d != 64 && q->d != 128) || (dtype != TQ_BF16 && dtype != TQ_F16) || heads / kv_heads > 128)
     return TQ_ERR_UNSUPPORTED;
   // (a prompt of 2^27 tokens passes a work item in about a second, within the kernel's limit on waits)
-  if (total > (1 << 27) || nseq > (1 << 24) || heads > (1 << 16)) return TQ_ERR_TOO_LARGE;
+  // (sequences, empty ones among them, are looked at one after the other: up to 2^18 in well under a second)
+  if (total > (1 << 27) || nseq > (1 << 18) || heads > (1 << 16)) return TQ_ERR_TOO_LARGE;
   if (total == 0 || nseq == 0) return TQ_OK;
   if (!y || !k || !v || !cu_seqlens || !out || !std::isfinite(scale)) return TQ_ERR_INVALID_ARG;
   const int64_t w = heads * q->d, wk = kv_heads * q->d;

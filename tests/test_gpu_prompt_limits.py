@@ -1,10 +1,11 @@
-"""Prompt attention with logits far beyond what a softmax tells apart."""
+"""Prompt attention with logits far beyond what a softmax tells apart, and with
+very many sequences."""
 import math
 
 import pytest
 import torch
 
-from tests.test_gpu_prompt import DT, handle, make, tq  # noqa: F401
+from tests.test_gpu_prompt import DT, check, handle, make, run_case, tq  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +33,36 @@ def test_large_logits(tq, d, dtype, ups):  # noqa: F811
             assert int(clear.sum()) > n // 2
             ref = v[top.indices[:, 0]].to(DT[dtype])
             assert torch.equal(out[:, h * d:(h + 1) * d][clear], ref[clear]), up
+
+
+def test_hundreds_of_sequences(tq):  # noqa: F811
+    """More sequences than one look of the search takes, of unequal numbers of work
+    items, empty ones among them."""
+    lens = [(37 * i) % 5 * ((i * 13) % 29) for i in range(700)]
+    lens[5], lens[300], lens[699] = 900, 513, 640
+    run_case(tq, 64, 2, 4, lens, "bf16", seed=51)
+    run_case(tq, 128, 1, 16, [1 + i % 3 for i in range(257)], "f16", seed=52)
+
+
+@pytest.mark.parametrize("nseq", [8191, 8193, 100000, 1 << 18])
+def test_very_many_sequences(tq, nseq):  # noqa: F811
+    """Beyond the sequences whose lengths the kernel keeps; most of one token, a few
+    long, some empty.  A token alone in its sequence has its own value."""
+    d, q = 64, handle(tq, 64)
+    lens = torch.ones(nseq, dtype=torch.int64)
+    lens[::7] = 0
+    long = {0: 130, 8190: 70, nseq // 2: 300, nseq - 1: 65}
+    for i, n in long.items():
+        lens[i] = n
+    starts = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)])
+    total = int(starts[-1])
+    y, k, v = make(total, 1, 1, d, "bf16", 9)
+    cu = starts.to(torch.int32).cuda()
+    out = tq.tq_attend_prompt(q, y, k, v, cu, 0.125)
+    tq.tq_sync_check(q)
+    alone = torch.ones(total, dtype=torch.bool)
+    for i, n in long.items():
+        alone[int(starts[i]): int(starts[i]) + n] = False
+    alone = alone.cuda()
+    assert torch.equal(out[alone], v[alone])
+    check(out, y, k, v, [int(starts[i]) for i in long], list(long.values()), 1, 1, d, 0.125, "bf16")
