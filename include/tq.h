@@ -292,7 +292,8 @@ tq_status tq_paged_store(const tq_quantizer *qk, const tq_quantizer *qv, const t
  * Lengths and tables are read on the device: the call can be captured in a
  * graph and replayed with other values in the same buffers.  A bounded wait
  * that ran out is reported by tq_sync_check(qk).  max_pages*page_size is at
- * most 2^29, npages*kv_heads*page_size below 2^32, total_q*heads below 2^31.
+ * most 2^29, npages*kv_heads*page_size below 2^32, total_q*heads below 2^31,
+ * nseq at most 2^18.
  * The workspace holds 4 d bytes per query row (token x head), twice that and
  * more where max_new rows need the kernel of many rows, and per SM the partial
  * results of two blocks of rows.

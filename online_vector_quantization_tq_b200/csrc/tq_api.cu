@@ -208,7 +208,8 @@ static tq_status check_paged_sizes(const tq_quantizer *qk, const tq_quantizer *q
     return TQ_ERR_INVALID_ARG;
   if (!tq::attend_paged_supported(qk, qv)) return TQ_ERR_UNSUPPORTED;
   const int64_t big = (int64_t)1 << 30;
-  if (total_q > big || nseq > (1 << 24) || heads > (1 << 16) || max_new > big / heads ||
+  // (sequences, empty ones among them, are looked at one after the other: up to 2^18 in well under a second)
+  if (total_q > big || nseq > (1 << 18) || heads > (1 << 16) || max_new > big / heads ||
       max_pages > ((int64_t)1 << 29) / page_size)
     return TQ_ERR_TOO_LARGE;
   return TQ_OK;

@@ -274,9 +274,9 @@ __device__ __forceinline__ Place place_of(const PagedParams &p, const PagedCut &
 // Output rows from the normalized rows of whole blocks, or from the partial
 // results of the runs that share a block (added up in their order), rotated
 // back.  Many rows: a block of threads takes up to 16 rows of one block, whose
-// place it finds once; each warp has two rows and four runs of each in flight.
+// sequence it finds by a search 32 ways in the sums of sum_parts, and whose place once; each warp has two rows and four runs of each in flight.
 // (64 rows a block, a run at a time: 92 us for 1024 rows of 17 runs each.)
-constexpr int kJoinRows = 16, kJoinThreads = 256;
+constexpr int kJoinThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) k_attend_paged_join_many(const __grid_constant__ PagedParams p) {
@@ -299,36 +299,27 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_paged_join_many(const _
     c.part_ml = few ? p.few.part_ml : p.many.part_ml;
     return c;
   };
-  auto parts_of = [&](const PagedCut &c) { return (c.rows + kJoinRows - 1) / kJoinRows; };
   if (warp == 0) {
-    if (lane == 0) s_item[0] = -1;
-    __syncwarp();
-    int64_t before = 0;
-    for (int i0 = 0; i0 < p.nseq && before <= blockIdx.x; i0 += 32) {
-      int64_t n = 0;
-      if (i0 + lane < p.nseq) {
-        const Seq s = seq_of(p, i0 + lane);
+    const int64_t *sums = p.join_first;
+    int lo = 0, hi = p.nseq;  // sums[lo] <= this block < sums[hi]
+    const bool some = blockIdx.x < __ldg(sums + hi);
+    while (some && hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, i = lo + step * (lane + 1);
+      lo += step * __popc(__ballot_sync(0xffffffffu, i < hi && __ldg(sums + i) <= blockIdx.x));
+      hi = min(hi, lo + step);
+    }
+    if (lane == 0) {
+      s_item[0] = some ? lo : -1;
+      if (some) {
+        const Seq s = seq_of(p, lo);
         const PagedCut c = cut_of(s);
-        n = (int64_t)blocks_of(p, c, s) * parts_of(c) * p.kv_heads;
-      }
-      int64_t in = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t b = __shfl_up_sync(0xffffffffu, in, o);
-        if (lane >= o) in += b;
-      }
-      const int64_t at = blockIdx.x - (before + in - n);
-      if (at >= 0 && at < n) {
-        const Seq s = seq_of(p, i0 + lane);
-        const PagedCut c = cut_of(s);
+        const int64_t at = blockIdx.x - __ldg(sums + lo);
         const int per = blocks_of(p, c, s) * parts_of(c), rest = (int)(at - divide(at, per) * per);
-        s_item[0] = i0 + lane;
         s_item[1] = (int)divide(at, per);
         s_item[2] = rest / parts_of(c);
         s_item[3] = rest % parts_of(c);
-        s_place = place_of(p, c, s, i0 + lane, s_item[1], s_item[2]);
+        s_place = place_of(p, c, s, lo, s_item[1], s_item[2]);
       }
-      before += __shfl_sync(0xffffffffu, in, 31);
     }
   }
   __syncthreads();
@@ -496,7 +487,7 @@ constexpr int kFewRows = 64;
 // Sizes of a call and where its pieces lie in the workspace
 struct Plan {
   PagedCut few{}, many{};
-  size_t few_o, few_ml, few_first, many_o, many_ml, many_first, whole, qprep, qscale, total;
+  size_t few_o, few_ml, few_first, many_o, many_ml, many_first, join_first, whole, qprep, qscale, total;
 };
 
 // f16: of the queries
@@ -526,6 +517,7 @@ Plan plan_of(const tq_quantizer *qk, bool f16, int64_t total_q, int64_t nseq, in
   };
   cut(L.few, L.few_o, L.few_ml, L.few_first);
   cut(L.many, L.many_o, L.many_ml, L.many_first);
+  L.join_first = take((size_t)(nseq + 1) * sizeof(int64_t));
   L.whole = take((size_t)total_q * heads * d * sizeof(float));
   L.qprep = take(many ? (size_t)total_q * heads * d * 2 * (1 + ip + f16) : 0);
   L.qscale = take(many ? (size_t)total_q * heads * sizeof(float) : 0);
@@ -548,7 +540,7 @@ tq_status launch_paged(const PagedParams &prm, const tq_quantizer *qk, const tq_
   }
   rc = qk->m ? paged_rows_launch<D, true>(prm, qk->w, qv->w, st) : paged_rows_launch<D, false>(prm, qk->w, qv->w, st);
   if (rc != TQ_OK) return rc;
-  if (prm.many.grid > 0 || rows >= 16 * (int64_t)prm.few.grid) {
+  if (prm.join_first) {
     // parts of blocks of rows: as many as the rows fill, and of one block more per sequence and KV head
     int64_t most = 0;
     for (const PagedCut *c : {&prm.few, &prm.many}) {
@@ -664,6 +656,8 @@ tq_status attend_paged_launch(const tq_quantizer *qk, const tq_quantizer *qv, co
   prm.many.first = reinterpret_cast<int64_t *>(base + L.many_first);
   prm.many.part_o = reinterpret_cast<float *>(base + L.many_o);
   prm.many.part_ml = reinterpret_cast<float2 *>(base + L.many_ml);
+  if (L.many.grid > 0 || a.total_q * a.heads >= 16 * (int64_t)L.few.grid)
+    prm.join_first = reinterpret_cast<int64_t *>(base + L.join_first);
   prm.whole = reinterpret_cast<float *>(base + L.whole);
   prm.qprep = reinterpret_cast<uint16_t *>(base + L.qprep);
   prm.qscale = reinterpret_cast<float *>(base + L.qscale);

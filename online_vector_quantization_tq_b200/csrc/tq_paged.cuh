@@ -53,6 +53,9 @@ struct PagedParams {
   float kappa;
   void *out;
   int64_t ldo;
+  // [nseq + 1]: parts of blocks of rows of the sequences before, which the join by parts takes (written by block 0 of
+  // the kernel of few rows); null: the join goes by rows
+  int64_t *join_first;
   PagedCut few, many;  // for the kernel of few rows and the kernel of many (its grid 0: not launched)
   float *whole;     // [total_q * heads][D]: normalized rows of blocks that one run had whole, rotated domain
   // many: [total_q * heads][D to 3 D] rotated queries, then their projections (inner-product keys), then the
@@ -297,6 +300,33 @@ struct Cursor {
     }
   }
 };
+
+// The join takes blocks of rows in parts of up to kJoinRows rows
+constexpr int kJoinRows = 16;
+__device__ __forceinline__ int parts_of(const PagedCut &c) { return (c.rows + kJoinRows - 1) / kJoinRows; }
+
+// Sums of join parts over the sequences, by one warp
+__device__ __forceinline__ void sum_parts(const PagedParams &p) {
+  const int lane = threadIdx.x & 31;
+  int64_t total = 0;
+  for (int i0 = 0; i0 < p.nseq; i0 += 32) {
+    int64_t n = 0;
+    if (i0 + lane < p.nseq) {
+      const Seq s = seq_of(p, i0 + lane);
+      n = (int64_t)(s.n * p.group <= p.few.upto ? blocks_of(p, p.few, s) * parts_of(p.few)
+                                                : blocks_of(p, p.many, s) * parts_of(p.many)) * p.kv_heads;
+    }
+    int64_t in = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t b = __shfl_up_sync(0xffffffffu, in, o);
+      if (lane >= o) in += b;
+    }
+    if (i0 + lane < p.nseq) p.join_first[i0 + lane] = total + in - n;
+    total += __shfl_sync(0xffffffffu, in, 31);
+  }
+  if (lane == 0) p.join_first[p.nseq] = total;
+}
 
 // The start of this block's run, found by one warp (block 0's also writes
 // c.first): sequence, head, block, unit and units of the run; false if there

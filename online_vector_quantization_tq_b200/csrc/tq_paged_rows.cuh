@@ -216,6 +216,7 @@ k_attend_paged(const __grid_constant__ PagedParams p) {
   if (warp == 0) {
     const bool some = find_run(p, p.few, s_run);
     if (lane == 0) s_some = some;
+    if (blockIdx.x == 0 && p.join_first) sum_parts(p);
   } else {
     for (int i = tid - 32; i < 256 * 16; i += kThreads - 32) {  // 16-byte pieces: 4 copies
       const int byte = i >> 4, part = i & 15;

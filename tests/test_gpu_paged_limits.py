@@ -241,3 +241,42 @@ def test_large_logits(tq, d, ip, dtype, n, group):  # noqa: F811
         ref = (ve["norm"][best][:, None] * tv.centroids[ve["codes"][best]]) @ tv.R
         err = np.linalg.norm(got[clear] - ref, axis=1)
         assert np.all(err <= 2.0 ** -9 * ve["norm"][best] + 2.0 ** -8 * np.linalg.norm(ref, axis=1)), up
+
+
+@pytest.mark.parametrize("nseq,n,heads", [(700, 1, 8), (3000, 1, 32), (3000, 40, 2), (1 << 18, 1, 2)])
+def test_very_many_sequences(tq, nseq, n, heads):  # noqa: F811
+    """Every sequence one of 192 kinds (queries, page, up to 48 + n keys), some of them
+    without new tokens, a few with more: as the 192 kinds alone, each within the
+    documented precision of the exact result."""
+    d, kinds, page = 64, 192, 16
+    (qk, tk), (qv, tv) = quantizer(tq, d, 4, False), quantizer(tq, d, 4, False, seed=1)
+    rng = np.random.default_rng(nseq + n)
+    width = (48 + n + page - 1) // page + 1
+    caches = []
+    for q in (qk, qv):
+        c = q.empty_paged(kinds * width, 1, page)
+        c.codes.random_(0, 256)
+        c.norms.copy_(torch.from_numpy(rng.uniform(0.5, 8.0, c.norms.shape).astype(np.float32)))
+        caches.append(c)
+    y = torch.from_numpy(rng.standard_normal((kinds, n, heads * d)).astype(np.float32)).bfloat16().cuda()
+    lens = torch.from_numpy(rng.integers(n, 48 + n, kinds)).cuda()
+    table = torch.arange(kinds * width, device="cuda").view(kinds, width)
+
+    def call(kind, news):
+        starts = torch.cat([torch.zeros(1, dtype=torch.int64, device="cuda"), news.cumsum(0)])
+        rows = torch.arange(int(starts[-1]), device="cuda")
+        seq = torch.searchsorted(starts, rows, right=True) - 1
+        at = rows - starts[seq]
+        yy = y[kind[seq], at]
+        out = tq.tq_attend_paged(qk, qv, yy, starts.to(torch.int32), *caches, table[kind].to(torch.int32),
+                                 lens[kind].to(torch.int32), n, 0.1)
+        tq.tq_sync_check(qk)
+        return out, kind[seq], at
+    ref = call(torch.arange(kinds, device="cuda"), torch.full((kinds,), n, device="cuda"))[0].view(kinds, n, heads * d)
+    kind = torch.from_numpy(rng.integers(0, kinds, nseq)).cuda()
+    news = torch.full((nseq,), n, device="cuda")
+    news[::5] = 0
+    out, of, at = call(kind, news)
+    diff = (out.float() - ref[of, at].float()).view(-1, d).norm(dim=1)
+    bound = 2 * (2.0 ** -9 * 8.0 + 2.0 ** -8 * (out.float().view(-1, d).norm(dim=1) + 2.0 ** -9 * 8.0))
+    assert bool((diff <= bound).all())
