@@ -144,6 +144,13 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
     return t
 
 
+def _like(y: torch.Tensor, stream) -> torch.Tensor:
+    """_empty of y's shape and type, in half the host's time where it is the current stream's."""
+    if stream is None:
+        return torch.empty_like(y, memory_format=torch.contiguous_format)
+    return _empty(y.shape, y.dtype, y.device, stream)
+
+
 def _workspace(nbytes: int, device, stream=None) -> torch.Tensor:
     """Scratch of a call on `stream`, from that stream's memory (see _empty)."""
     n = max(int(nbytes), 16)
@@ -488,7 +495,7 @@ def tq_attend_prompt(q: Quantizer, y: torch.Tensor, k: torch.Tensor, v: torch.Te
     if nseq < 0:
         raise ValueError("cu_seqlens must have one entry more than there are sequences")
     if out is None:
-        out = _empty(y.shape, y.dtype, y.device, stream)
+        out = _like(y, stream)
     elif out.dtype != dtype or out.shape != y.shape:
         raise ValueError("out must have y's shape and type")
     device = _one_device(q, "y k v cu_seqlens out", y, k, v, cu_seqlens, out)
@@ -548,7 +555,7 @@ def tq_attend_paged(qk: Quantizer, qv: Quantizer, y: torch.Tensor, q_start: torc
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != nseq:
         raise TypeError(f"page_table must be an int32 tensor of {nseq} rows")
     if out is None:
-        out = _empty(y.shape, y.dtype, y.device, stream)
+        out = _like(y, stream)
     elif out.dtype != y.dtype or out.shape != y.shape:
         raise ValueError("out must have y's shape and type")
     max_pages = page_table.shape[1]
