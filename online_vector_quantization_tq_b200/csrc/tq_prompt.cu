@@ -50,6 +50,8 @@ constexpr int kPromptThreads = 384;
 // Registers move to the softmax: a warpgroup's share, whose sum is no more
 // than the block was launched with (launch_prompt checks).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
+// The search for work items (Items): sequences of a group, groups at most, sequences whose levels are kept
+constexpr int kGroup = 128, kGroups = 2048, kCached = 4096;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kGuardWarp = 10;
 
 struct PromptParams {
@@ -69,8 +71,8 @@ struct PromptSmem {
   static constexpr int kHalf = kTile * 128;        // 128 rows x 64 elements, 128-byte swizzle
   static constexpr int kOne = kHalf * (D / 64);    // one tile of D elements a row
   static constexpr int kQ = 0, kK = 2 * kOne, kV = kK + kStages * kOne;
-  static constexpr int kLevels = kV + kStages * kOne;  // of Items
-  static constexpr int kBytes = kLevels + 1024;        // and 4 for each of the levels
+  static constexpr int kMost = kV + kStages * kOne, kLevels = kMost + 4 * kGroups;  // of Items
+  static constexpr int kBytes = kLevels + 4 * kCached + 1024;
 };
 
 // The items, longest first.  A sequence of n tokens has ceil(n / span) levels
@@ -78,19 +80,18 @@ struct PromptSmem {
 // level 0.  Items are ordered by falling level, then sequence, then KV head.
 // Used by one warp, which asks for them in this order.  Levels of up to 128
 // sequences stay in registers, and an item's level is found by bisection.  Of
-// more, the search goes on from where it found the last item: over a call it
-// looks at each level of each sequence once, 128 sequences at a time.  (512
+// more, in groups of 128, the search goes on from where it found the last item:
+// over a call it looks once at each level of the groups that have it.  (512
 // prompts of up to 100 tokens: 270 us; bisecting anew for each item 710 us.  Three
 // prompts of up to 4100 tokens, whose 228 levels hold few items each: 98 us; by
-// walking down the levels 118 us.)  The levels of the first kCached sequences are
-// in shared memory.
-constexpr int kCached = 8192;
+// walking down the levels 118 us.)  In shared memory: each group's highest level,
+// and the levels of the first kCached sequences.
 
 struct Items {
-  const int *cached;  // a whole number of 128
-  int few[4];         // the levels of up to 128 sequences
-  int level, i0;      // the place: sequences from i0 on that have `level`
-  int64_t before;     // items per head in front of it
+  const int *cached, *most;  // levels, and of each group the highest
+  int few[4];                // the levels of up to 128 sequences
+  int level, group;          // the place: groups from here on that have `level`
+  int64_t before;            // items per head in front of it
 
   static __device__ int start_of(const PromptParams &p, int i) {
     return (int)min(max((int64_t)__ldg(p.cu + i), (int64_t)0), p.total);
@@ -103,21 +104,33 @@ struct Items {
     const int span = 2 * p.tokens;
     return i < p.nseq ? (length(p, i) + span - 1) / span : 0;
   }
-  // levels of the lane's sequences i + 32 e
-  __device__ void load(const PromptParams &p, int i, int (&n)[4]) const {
+  static __device__ int groups_of(const PromptParams &p) { return (p.nseq + kGroup - 1) / kGroup; }
+  // Before the search, by all warps
+  static __device__ void prepare(const PromptParams &p, int *cached, int *most, int warp, int warps) {
+    const int lane = threadIdx.x & 31;
+    for (int g = warp; g < ((groups_of(p) + 31) & ~31); g += warps) {
+      int top = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int seq = i + 32 * e + (threadIdx.x & 31);
-      n[e] = i < kCached ? cached[seq] : levels_of(p, seq);
+      for (int e = 0; e < kGroup / 32; ++e) {
+        const int seq = g * kGroup + 32 * e + lane, n = levels_of(p, seq);
+        if (seq < kCached) cached[seq] = n;
+        top = max(top, n);
+      }
+      top = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
+      if (lane == 0) most[g] = top;
     }
   }
-  __device__ Items(const PromptParams &p, const int *levels) : cached(levels), level(0), i0(0), before(0) {
-    for (int i = 0; i < p.nseq; i += 128) {
-      int n[4];
-      load(p, i, n);
+  // levels of the lane's sequences of group g
+  __device__ void load(const PromptParams &p, int g, int (&n)[4]) const {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) level = max(level, n[e]);
+    for (int e = 0; e < kGroup / 32; ++e) {
+      const int seq = g * kGroup + 32 * e + (threadIdx.x & 31);
+      n[e] = (g + 1) * kGroup <= kCached ? cached[seq] : levels_of(p, seq);
     }
+  }
+  __device__ Items(const PromptParams &p, const int *levels, const int *tops)
+      : cached(levels), most(tops), level(0), group(0), before(0) {
+    for (int g = threadIdx.x & 31; g < groups_of(p); g += 32) level = max(level, most[g]);
     level = (int)__reduce_max_sync(0xffffffffu, (unsigned)level) - 1;
     load(p, 0, few);
   }
@@ -132,7 +145,7 @@ struct Items {
   __device__ bool find(const PromptParams &p, int64_t index, int4 &item) {
     const int64_t rank = index < 0x7fffffff ? (uint32_t)index / (uint32_t)p.kv_heads : index / p.kv_heads;
     item.y = (int)(index - rank * p.kv_heads);
-    if (p.nseq <= 128) {
+    if (p.nseq <= kGroup) {
       if (rank >= above(-1)) return false;
       int lo = -1;  // above(lo) > rank >= above(level)
       while (level - lo > 1) {
@@ -144,14 +157,22 @@ struct Items {
       }
       before = above(level);
     }
-    for (; level >= 0; --level, i0 = 0)
-      for (; i0 < p.nseq; i0 += 128) {
+    const int lane = threadIdx.x & 31, groups = groups_of(p);
+    for (; level >= 0; --level, group = 0)
+      while (group < groups) {
+        const int g0 = group & ~31;
+        const uint32_t have = __ballot_sync(0xffffffffu, g0 + lane >= group && most[g0 + lane] > level);
+        if (have == 0) {
+          group = g0 + 32;
+          continue;
+        }
+        group = g0 + __ffs(have) - 1;
         int n[4], count = 0;
-        if (p.nseq <= 128) {
+        if (p.nseq <= kGroup) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) n[e] = few[e];
         } else {
-          load(p, i0, n);
+          load(p, group, n);
         }
         uint32_t m[4];
 #pragma unroll
@@ -161,13 +182,14 @@ struct Items {
         }
         if (rank >= before + count) {
           before += count;
+          ++group;
           continue;
         }
         int left = (int)(rank - before);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if (left >= 0 && left < __popc(m[e])) {
-            const int seq = i0 + 32 * e + __fns(m[e], 0, left + 1);
+            const int seq = group * kGroup + 32 * e + __fns(m[e], 0, left + 1);
             item.x = level;
             item.z = start_of(p, seq);
             item.w = length(p, seq);
@@ -261,8 +283,8 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
   __shared__ volatile int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  int *levels = reinterpret_cast<int *>(smem + SM::kLevels);
-  for (int i = tid; i < min((p.nseq + 127) & ~127, kCached); i += kPromptThreads) levels[i] = Items::levels_of(p, i);
+  int *levels = reinterpret_cast<int *>(smem + SM::kLevels), *most = reinterpret_cast<int *>(smem + SM::kMost);
+  Items::prepare(p, levels, most, kPromptThreads / 32 - 1 - warp, kPromptThreads / 32);
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < 2; ++i) {
       sm100::mbar_init(&q_full[i], 1);
@@ -310,7 +332,7 @@ k_attend_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kLoadWarp) {
       const uint32_t qbytes = (uint32_t)p.group * p.tokens * 128 * (D / 64);
-      Items items(p, levels);
+      Items items(p, levels, most);
       int keys = 0, values = 0, queries[2] = {0, 0};  // copies issued
       for (int k = 0;; ++k) {
         const int64_t round = (int64_t)k * gridDim.x;
@@ -569,15 +591,14 @@ tq_status launch_prompt(const PromptArgs &a, int *err, cudaStream_t st) {
   const int64_t most = (a.total / (2 * tokens) + std::min(a.nseq, a.total)) * a.kv_heads;
   const int64_t blocks = std::min<int64_t>(most, current_sms());
   auto kern = k_attend_prompt<D, BF16>;
-  constexpr int most_smem = PromptSmem<D>::kBytes + 4 * kCached;
-  static_assert(most_smem <= 232448 - 1024, "shared memory");
-  const int smem = PromptSmem<D>::kBytes + 4 * (int)std::min<int64_t>((a.nseq + 127) & ~127, kCached);
+  constexpr int smem = PromptSmem<D>::kBytes;
+  static_assert(smem <= 232448 - 1024, "shared memory");
   static std::atomic<uint64_t> ready{0};
   const tq_status rc = once_per_device(ready, [&] {
     cudaFuncAttributes fa;  // (a split of registers beyond what the block holds would wait for ever)
     return cudaFuncGetAttributes(&fa, kern) == cudaSuccess &&
            fa.numRegs * kPromptThreads >= 128 * (2 * kSoftmaxRegs + kOtherRegs) &&
-           cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem) == cudaSuccess;
+           cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
   });
   if (rc != TQ_OK) return rc;
   kern<<<(unsigned)blocks, kPromptThreads, smem, st>>>(mq, mk, mv, p);

@@ -66,3 +66,24 @@ def test_very_many_sequences(tq, nseq):  # noqa: F811
     alone = alone.cuda()
     assert torch.equal(out[alone], v[alone])
     check(out, y, k, v, [int(starts[i]) for i in long], list(long.values()), 1, 1, d, 0.125, "bf16")
+
+
+def test_one_long_sequence_among_very_many(tq):  # noqa: F811
+    """Hundreds of levels that one sequence has alone, a group of many query heads
+    and 2^18 sequences: the search passes over the others."""
+    d, group, q = 64, 128, handle(tq, 64)
+    nseq, at, n = 1 << 18, 200000, 3000
+    lens = torch.zeros(nseq, dtype=torch.int64)
+    lens[::97] = 1
+    lens[at] = n
+    starts = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)])
+    total = int(starts[-1])
+    y, k, v = make(total, group, 1, d, "bf16", 10)
+    out = tq.tq_attend_prompt(q, y, k, v, starts.to(torch.int32).cuda(), 0.125)
+    tq.tq_sync_check(q)
+    s = int(starts[at])
+    alone = torch.ones(total, dtype=torch.bool, device="cuda")
+    alone[s:s + n] = False
+    assert torch.equal(out[alone], v[alone].repeat(1, group))
+    some = slice(0, 2 * d)  # two of the heads
+    check(out[:, some], y[:, some], k, v, [s], [n], 2, 1, d, 0.125, "bf16")
