@@ -252,16 +252,26 @@ struct Place {
   bool seen;  // the block has keys
   __device__ int64_t at(const PagedCut &c, int b) const { return ((int64_t)2 * b + (b == b0 ? 1 : 0)) * c.rows; }
 };
+// (by a warp: a long chunk has thousands of blocks, whose units are added up)
 __device__ __forceinline__ Place place_of(const PagedParams &p, const PagedCut &c, const Seq &s, int seq, int head,
                                           int block) {
   Place f{};
   int64_t before = 0, all = 0;
-  for (int k = 0, n = blocks_of(p, c, s); k < n; ++k) {
-    const int u = units_of(p, c, s, k);
-    all += u;
-    if (k < block) before += u;
+  const int units = units_of(p, c, s, block), blocks = blocks_of(p, c, s);
+  if (blocks == 1) {
+    all = units;
+  } else {
+    for (int k = threadIdx.x & 31; k < blocks; k += 32) {
+      const int u = units_of(p, c, s, k);
+      all += u;
+      if (k < block) before += u;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
   }
-  const int units = units_of(p, c, s, block);
   f.seen = units > 0;
   if (!f.seen) return f;
   const int64_t u0 = __ldg(c.first + seq) + head * all + before, u1 = u0 + units - 1;
@@ -308,19 +318,20 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_paged_join_many(const _
       lo += step * __popc(__ballot_sync(0xffffffffu, i < hi && __ldg(sums + i) <= blockIdx.x));
       hi = min(hi, lo + step);
     }
-    if (lane == 0) {
-      s_item[0] = some ? lo : -1;
-      if (some) {
-        const Seq s = seq_of(p, lo);
-        const PagedCut c = cut_of(s);
-        const int64_t at = blockIdx.x - __ldg(sums + lo);
-        const int per = blocks_of(p, c, s) * parts_of(c), rest = (int)(at - divide(at, per) * per);
-        s_item[1] = (int)divide(at, per);
+    if (some) {
+      const Seq s = seq_of(p, lo);
+      const PagedCut c = cut_of(s);
+      const int64_t at = blockIdx.x - __ldg(sums + lo);
+      const int per = blocks_of(p, c, s) * parts_of(c), head = (int)divide(at, per), rest = (int)(at - (int64_t)head * per);
+      const Place f = place_of(p, c, s, lo, head, rest / parts_of(c));
+      if (lane == 0) {
+        s_item[1] = head;
         s_item[2] = rest / parts_of(c);
         s_item[3] = rest % parts_of(c);
-        s_place = place_of(p, c, s, lo, s_item[1], s_item[2]);
+        s_place = f;
       }
     }
+    if (lane == 0) s_item[0] = some ? lo : -1;
   }
   __syncthreads();
   if (s_item[0] < 0) return;
