@@ -490,9 +490,10 @@ __global__ void __launch_bounds__(128) k_attend_paged_join(const __grid_constant
 
 // Sequences of more rows go to the kernel of many rows, whose blocks of 128
 // or 256 rows cost the same however few of their rows are there (8 sequences
-// of 8000 keys and 8 KV heads, d = 128, us by few / by many: 32 rows 74 / 135,
-// 64 rows 119 / 139, 96 rows 166 / 141; 40 sequences, 64 rows 494 / 520, 96 rows
-// 723 / 532).
+// of 8000 keys and 8 KV heads, d = 128, us by few / by many: 32 rows 84 / 117,
+// 64 rows 137 / 120, 96 rows 194 / 124; 40 sequences, 64 rows 580 / 439, 96 rows
+// 860 / 450).  Time alone would set the limit near 48; up to 64 rows keep the
+// kernel of few, whose bf16 calls' operands are not rounded with their norms.
 constexpr int kFewRows = 64;
 
 // Sizes of a call and where its pieces lie in the workspace
