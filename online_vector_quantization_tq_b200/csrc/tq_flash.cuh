@@ -109,13 +109,8 @@ struct Row {
   __device__ float exponent() const { return ref + norm; }  // of sum and O
 };
 
-// Exponent of the power of two above v (v >= 0), within what fp32 factors hold
-__device__ __forceinline__ float exponent_above(float v) {
-  return fminf(fmaxf((float)((int)(__float_as_uint(v) >> 23) - 126), -100.f), 100.f);
-}
-
-// The same of a value norm, no less than -80 (a weight is at most 2^8 over its
-// key's norm, and the sum of 2^29 of them has to fit fp32)
+// Exponent e of a value norm v below 2^e (v >= 0), no less than -80 (a weight is at
+// most 2^8 over its key's norm, and the sum of 2^29 of them has to fit fp32)
 __device__ __forceinline__ float norm_exponent(float v) {
   return fmaxf(__uint_as_float((__float_as_uint(v) >> 23) + 0x4B000000u) - (8388608.f + 126.f), -80.f);
 }
@@ -328,7 +323,8 @@ __device__ __forceinline__ bool softmax_tile_twice(uint32_t s, uint32_t o, bool 
 // The same tile with a factor of each key's logit, `keys`, and with values scaled
 // down by a factor of each key's own, kFactors behind it.  Products are rounded
 // before the reference is subtracted.  Three passes over S: the highest logit,
-// the largest weight times norm relative to it, the weights.
+// the largest weight times norm relative to it, the weights.  A function of its
+// own for tiles that are rare (norms far apart, large logits).
 __device__ __forceinline__ void own_logits(uint32_t s, int c, float mult, int see, const float *keys, float (&x)[32]) {
   sm100::tmem_ld32(s + 32 * c, reinterpret_cast<uint32_t(&)[32]>(x));
   sm100::tmem_wait_ld();

@@ -10,18 +10,18 @@
 // (which the row may not even see) is scaled by a power of two of its own, and
 // the tile's softmax looks at factors per key.  Each thread makes a table of its
 // row's 2^w possible values, so that every element is rounded once, and the
-// softmax of a tile without such norms meets no factors per key.  (As fp32 factors of
-// logits and weights the norms made the softmax the bound: 316 us instead of
-// 287 on 512 new tokens over 16384 keys.)  Inner-product keys are operands of
-// twice the width, [c | +-64 gamma sqrt(pi/2)/d] times the norm, against queries
-// [R y | S R y / 64].
+// softmax of a tile without such norms meets no factors per key.  (As fp32
+// factors of logits and weights the norms make the softmax the bound: see LOW.)
+// Inner-product keys are operands of twice the width, [c | +-64 gamma
+// sqrt(pi/2)/d] times the norm, against queries [R y | S R y / 64].
 //
 // fp16 results (LOW) would show the rounding of these operands: their centroids
 // are operands under the codebook's common factor, within 2^-13, with the norms as
 // fp32 factors of logits and weights, and the rotated queries' low terms are
 // multiplied too, as a third part [R y | S R y / 64 | low] of the query tile,
 // against the centroids once more.  (Error against 64 bits, 2-norm over 2-norm:
-// 1.5e-3 before, 2.0e-4 the result's own rounding.)
+// 3.1e-4, 2.0e-4 of it the result's own rounding, against 1.5e-3 with the others'
+// operands; 512 new tokens on 16384 keys 310 us against 230.)
 //
 // One block per SM works off its run of units (PagedCut; a unit is a tile of
 // 128 keys).  Two warpgroups of softmax share the tensor cores:
@@ -401,22 +401,23 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
             if (lane == 0) s_gap[nr][warp - kKeyWarp] = gap;
             signs_by = 1.f / p.kunit;
           } else {
-          const uint32_t kscale = scale_bits(top_of(0, ring.before + j), kLeastKey);
-          const uint32_t vscale = scale_bits(top_of(1, ring.before + j), kLeastValue);
-          uint32_t kown = kscale, vown = vscale;
-          if (stands_alone(n.x, kscale)) kown = scale_bits(n.x, kLeastKey);
-          if (stands_alone(v, vscale)) vown = scale_bits(v, kLeastValue);
-          const float f = finite ? fmaxf(n.x, 0.f) * inverse_of(kown) : NAN;
-          byte_tables<WK>(p.ckf, f, tlo, thi);
-          signs_by = f;
-          s_keys[nr * kTile + r] = n.x < 0.f ? -1.f : __uint_as_float(kown) * inverse_of(kscale);
-          s_values[nr * kTile + r] = __uint_as_float(vown);
-          const int gap = __any_sync(0xffffffffu, n.x < 0.f) | __any_sync(0xffffffffu, kown != kscale || vown != vscale) << 1;
-          if (lane == 0) s_gap[nr][warp - kKeyWarp] = gap;
-          if (r == 0) {
-            s_key[nr] = __uint_as_float(kscale);
-            s_value[nr] = (float)((int)(vscale >> 23) - 127);
-          }
+            const uint32_t kscale = scale_bits(top_of(0, ring.before + j), kLeastKey);
+            const uint32_t vscale = scale_bits(top_of(1, ring.before + j), kLeastValue);
+            uint32_t kown = kscale, vown = vscale;
+            if (stands_alone(n.x, kscale)) kown = scale_bits(n.x, kLeastKey);
+            if (stands_alone(v, vscale)) vown = scale_bits(v, kLeastValue);
+            const float f = finite ? fmaxf(n.x, 0.f) * inverse_of(kown) : NAN;
+            byte_tables<WK>(p.ckf, f, tlo, thi);
+            signs_by = f;
+            s_keys[nr * kTile + r] = n.x < 0.f ? -1.f : __uint_as_float(kown) * inverse_of(kscale);
+            s_values[nr * kTile + r] = __uint_as_float(vown);
+            const int gap = __any_sync(0xffffffffu, n.x < 0.f) |
+                            __any_sync(0xffffffffu, kown != kscale || vown != vscale) << 1;
+            if (lane == 0) s_gap[nr][warp - kKeyWarp] = gap;
+            if (r == 0) {
+              s_key[nr] = __uint_as_float(kscale);
+              s_value[nr] = (float)((int)(vscale >> 23) - 127);
+            }
           }
           uint8_t *slot = smem + SM::kRing + (at % SM::kSlots) * SM::kSlot;
 #pragma unroll
