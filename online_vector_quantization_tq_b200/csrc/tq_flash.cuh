@@ -130,34 +130,37 @@ __device__ __forceinline__ void scale_rows(uint32_t o, float f) {
   sm100::tmem_wait_st();
 }
 
-// A logit this large (base 2) makes the fused a * mult - reference differ from
-// the rounded product that the reference is by more than a weight's rounding;
-// from 2^28 on the weights would leave fp32.  Then the product is rounded first.
-constexpr float kLargeLogit = 65536.f;
+// From logits this large (base 2) on the fused a * mult - reference differs from
+// the rounded product that the reference is by more than an fp16 weight near 1 is
+// rounded by (2^-12), and from 2^28 on the weights would leave fp32.  Such a row's
+// products are rounded first, so that its highest logit's weight is 1.  In the paged
+// cache's kernel, where they cost a warp two more passes, from 2^16 on alone.
+constexpr float kLargeRow = 4096.f, kLargeLogit = 65536.f;
 
 // Moves a row's reference up to a tile's highest logit (base 2) and the exponent
-// of the values there, where the two together have grown by more than the slack,
-// by whole warps; sum and O follow (the sum by a root of the factor twice: a
-// factor of 2^-126 or less is 0, and the sum may be 2^180 above what it is then
-// added to).  first: O is not there yet.  Returns whether the warp has large
-// logits; SMALL: if so, nothing is moved.
+// of the values there, where the two together have grown by more than the slack;
+// sum and O follow (the sum by a root of the factor twice: a factor of 2^-126 or
+// less is 0, and the sum may be 2^180 above what it is then added to).  first: O is
+// not there yet.  Whether a row moves, and by how much, is its own affair: moving
+// all rows of a warp with the first that has to would put its neighbours, rows
+// that it does not see among them, into a row's roundings.  Returns whether the
+// row has large logits; SMALL: whether any of the warp has, and nothing is moved.
 template <int D, bool SMALL>
 __device__ __forceinline__ bool move_reference(uint32_t o, bool first, float most, float norm, Row &row) {
   const float up = (most - row.ref) + (norm - row.norm);  // infinite for the first visible keys, a NaN for none so far
   const float top = fmaxf(most, row.ref);
-  const bool large = fabsf(top) > kLargeLogit && top > -INFINITY;
+  const bool large = fabsf(top) > (SMALL ? kLargeLogit : kLargeRow) && top > -INFINITY;
   if (!__any_sync(0xffffffffu, up > kSlack || large)) return false;
-  const bool some = __any_sync(0xffffffffu, large);
-  if (some && SMALL) return true;
+  if (SMALL && __any_sync(0xffffffffu, large)) return true;
   float f = 1.f;
-  if (up > 0.f) {
+  if (up > kSlack) {
     f = ex2(-0.5f * up);
     row.ref = most;
     row.norm = norm;
   }
   row.sum = f * row.sum * f;
   if (!first && __any_sync(0xffffffffu, f != 1.f)) scale_rows<D>(o, f * f);
-  return some;
+  return large;
 }
 
 // Weights are in TMEM: the product that reads them may start
@@ -200,6 +203,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t s, uint32_t o, bool first,
     for (int i = 0; i < 128; ++i) x[i] *= mult;
     mult = 1.f;
   }
+  __syncwarp();
   const float2 m2 = make_float2(mult, mult), b2 = make_float2(base, base);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
