@@ -284,11 +284,11 @@ tq_status tq_paged_store(const tq_quantizer *qk, const tq_quantizer *qv, const t
  * common factor leaves them within 2^-13: what is left, beside the result's own
  * rounding, is mostly that of the weights (2-norm over 2-norm about 3e-4, with
  * inner-product keys and sharp heads up to 5e-4).
- * Norms up to 2^100, of any sizes side by side: neither a norm
- * that a token does not see nor one of little weight takes precision from the
- * others'.  A key, residual or value norm that
+ * Norms up to 2^100, of any sizes side by side (residual norms, which are of unit
+ * vectors, up to 2^14): neither a norm that a token does not see nor one of little
+ * weight takes precision from the others'.  A key, residual or value norm that
  * is not finite makes NaN of the tokens that see it, and of no other; the sign
- * of a norm does not count.
+ * of a key's or a value's norm does not count.
  * Lengths and tables are read on the device: the call can be captured in a
  * graph and replayed with other values in the same buffers.  A bounded wait
  * that ran out is reported by tq_sync_check(qk).  max_pages*page_size is at

@@ -15,6 +15,7 @@
 #include <limits>
 #include <new>
 #include <thread>
+#include <utility>
 #include <vector>
 
 #include "tq_internal.h"
@@ -357,6 +358,58 @@ const char *tq_status_string(tq_status s) {
 
 // mse: TurboQuant-MSE (all b bits to the codebook, no QJL stage, m = 0);
 // otherwise b - 1 codebook bits and an m-row QJL sketch.
+// Common factors in [1, 2), 1/256 apart, under which the fp16 centroids are
+// closest to the codebook, and what undoes each: the least-squares fit, since a
+// rounding that all coordinates of a key have in common scales its logit.  Errors
+// weigh as a logit has them, by c^2: with the codes' own probabilities (the
+// coordinate law is nearly normal at these d) and with all codes alike, the worse of
+// the two, an rms of 2^-20 (four levels) to 2^-13.8 (sixteen).
+static void choose_attend_factors(tq_quantizer *q) {
+  using namespace tq;
+  constexpr int kTries = 16384;
+  const int L = 1 << q->w, half = L / 2;  // (the codebook is symmetric)
+  double c[8], p[8], ps = 0.0, us = 0.0;
+  for (int k = 0; k < half; ++k) {
+    const double lo = k ? q->thresholds[half + k - 1] : 0.0, hi = half + k < L - 1 ? q->thresholds[half + k] : 1.0;
+    c[k] = q->centroids[half + k];
+    p[k] = std::erf(hi * std::sqrt(q->d / 2.0)) - std::erf(lo * std::sqrt(q->d / 2.0));
+    ps += p[k] * c[k] * c[k];
+    us += c[k] * c[k];
+  }
+  std::vector<std::pair<float, int>> order(kTries);
+  std::vector<double> undo(kTries);
+  for (int i = 0; i < kTries; ++i) {
+    const double f = 1.0 + i / (double)kTries;
+    double a[8], ca = 0.0, aa = 0.0, pe = 0.0, ue = 0.0;
+    for (int k = 0; k < half; ++k) {
+      a[k] = half_bits_to_double(double_to_half_bits(c[k] * f));
+      const double w = p[k] / ps + 1.0 / us;
+      ca += w * c[k] * a[k];
+      aa += w * a[k] * a[k];
+    }
+    undo[i] = ca / aa;
+    for (int k = 0; k < half; ++k) {
+      const double e = a[k] * undo[i] - c[k];
+      pe += p[k] * e * e;
+      ue += e * e;
+    }
+    order[i] = {(float)std::max(pe / ps, ue / us), i};
+  }
+  std::sort(order.begin(), order.end());
+  int found = 0, picked[kAttendFactors];
+  for (const auto &o : order) {
+    bool far = true;
+    for (int k = 0; k < found; ++k) far = far && std::abs(o.second - picked[k]) >= kTries / 256;
+    if (!far) continue;
+    const double f = 1.0 + o.second / (double)kTries;
+    for (int k = 0; k < std::min(L, 8); ++k)
+      q->attend_ck[found][k] = double_to_half_bits(q->centroids[L > 8 ? 8 + k : k] * f);
+    q->attend_by[found] = (float)(1.0 / undo[o.second]);
+    picked[found++] = o.second;
+    if (found == kAttendFactors) break;
+  }
+}
+
 static tq_status build_quantizer(int d, int b, int m, uint64_t seed, tq_rotation rot, bool device, bool mse,
                                  tq_quantizer **out) {
   using namespace tq;
@@ -603,6 +656,7 @@ static tq_status build_quantizer(int d, int b, int m, uint64_t seed, tq_rotation
     }
     for (int k = 0; k < L; ++k) q->attend_c[k] = double_to_half_bits(q->centroids[k] * best);
     q->attend_unit = (float)(1.0 / best);
+    if (m > 0 && (d == 64 || d == 128)) choose_attend_factors(q);
   }
   KernelTables &kt = q->kt;
   kt.d = d;

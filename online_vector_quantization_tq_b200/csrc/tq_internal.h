@@ -11,6 +11,7 @@
 namespace tq {
 
 constexpr int kMaxLevels = 16;  // 2^w for w <= 4
+constexpr int kAttendFactors = 16;  // common factors of centroids that attention over pages chooses from
 
 // Small, POD view of a quantizer that kernels take by value.
 struct KernelTables {
@@ -66,6 +67,9 @@ struct tq_quantizer {
   // attention over pages: centroid c_k ~ attend_c[k] (fp16 bits) * attend_unit
   uint16_t attend_c[tq::kMaxLevels] = {};
   float attend_unit = 1.f;
+  // the same under several factors (inner-product keys): up to eight centroids, the upper eight of sixteen
+  uint16_t attend_ck[tq::kAttendFactors][8] = {};
+  float attend_by[tq::kAttendFactors] = {};
   tq::KernelTables kt{};
 };
 

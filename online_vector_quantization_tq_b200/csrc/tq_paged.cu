@@ -652,6 +652,8 @@ tq_status attend_paged_launch(const tq_quantizer *qk, const tq_quantizer *qv, co
     prm.ckf[i] = i < (1 << qk->w) ? (float)qk->centroids[i] : 0.f;
     prm.cvf[i] = i < (1 << qv->w) ? (float)qv->centroids[i] : 0.f;
   }
+  std::memcpy(prm.cks, qk->attend_ck, sizeof(prm.cks));
+  std::memcpy(prm.cks_by, qk->attend_by, sizeof(prm.cks_by));
   prm.kunit = qk->attend_unit;
   prm.vunit = qv->attend_unit;
   prm.kdiag = qk->kt.diag_bits;

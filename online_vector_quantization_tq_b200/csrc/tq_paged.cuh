@@ -48,6 +48,9 @@ struct PagedParams {
   uint16_t ck[16], cv[16];  // fp16 centroids, in units of kunit and vunit
   float kunit, vunit;
   float ckf[16], cvf[16];   // the same in fp32
+  // fp16 centroids of the keys under several factors (many rows, inner-product keys, fp16 queries)
+  uint16_t cks[kAttendFactors][8];
+  float cks_by[kAttendFactors];
   const uint32_t *kdiag, *vdiag;
   const uint16_t *qjl;  // d x d fp16 (inner-product keys)
   float kappa;

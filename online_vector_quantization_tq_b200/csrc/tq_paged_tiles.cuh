@@ -21,7 +21,11 @@
 // multiplied too, as a third part [R y | S R y / 64 | low] of the query tile,
 // against the centroids once more.  (Error against 64 bits, 2-norm over 2-norm:
 // 3.1e-4, 2.0e-4 of it the result's own rounding, against 1.5e-3 with the others'
-// operands; 512 new tokens on 16384 keys 310 us against 230.)
+// operands; 512 new tokens on 16384 keys 302 us against 228.)  The residual norms
+// of inner-product keys stay operands; each key takes the one of 16 common factors
+// (and its table of centroids) that brings its residual norm nearest to an fp16
+// number, a seventh of what rounding it would cost.  (Keys of 2 bits, whose sign
+// bits make the most of a logit: 4.6e-4, with one factor for all 1.15e-3.)
 //
 // One block per SM works off its run of units (PagedCut; a unit is a tile of
 // 128 keys).  Two warpgroups of softmax share the tensor cores:
@@ -213,6 +217,13 @@ __device__ __forceinline__ void byte_tables(const float *c, float f, uint32_t (&
   }
 }
 
+// The same of up to eight fp16 centroids in a row
+__device__ __forceinline__ void byte_tables(uint4 c, uint32_t (&lo)[4], uint32_t (&hi)[4]) {
+  lo[0] = sm100::prmt(c.x, c.y, 0x6420u), hi[0] = sm100::prmt(c.x, c.y, 0x7531u);
+  lo[1] = sm100::prmt(c.z, c.w, 0x6420u), hi[1] = sm100::prmt(c.z, c.w, 0x7531u);
+  lo[2] = lo[3] = hi[2] = hi[3] = 0u;
+}
+
 // The same of fp16 centroids as they are
 template <int W>
 __device__ __forceinline__ void byte_tables(const uint16_t *c, uint32_t (&lo)[4], uint32_t (&hi)[4]) {
@@ -258,6 +269,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
   __shared__ float s_key[kNorms], s_value[kNorms];  // 2^e of a tile's keys, exponent of its values
   __shared__ float s_top[3][2][4];                  // keys' and values' largest norms, of each warp
   __shared__ float2 s_ml[kTile];
+  __shared__ uint4 s_codes[IP && LOW ? kAttendFactors : 1];  // the keys' centroids under each factor
+  __shared__ float2 s_by[IP && LOW ? kAttendFactors : 1];    // the factor, and what undoes it beside p.kunit
   __shared__ volatile int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -280,6 +293,11 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
     sm100::mbar_init(&merged, kTile);
     s_abort = 0;
     sm100::fence_barrier_init();
+  } else if (IP && LOW && warp == 2 && lane < kAttendFactors) {
+    const uint16_t *c = p.cks[lane];
+    s_codes[lane] = make_uint4(c[0] | (uint32_t)c[1] << 16, c[2] | (uint32_t)c[3] << 16, c[4] | (uint32_t)c[5] << 16,
+                               c[6] | (uint32_t)c[7] << 16);
+    s_by[lane] = make_float2(p.cks_by[lane], 1.0f / (p.cks_by[lane] * p.kunit));
   }
   __syncthreads();
   if (!s_some) return;
@@ -326,9 +344,9 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
     auto agree = [&](bool mine) { return !sm100::named_barrier_or(keys ? 1 : 2, kTile, !mine); };
     constexpr int kBehind = -2;  // a page index: the key lies behind those that are seen
     if constexpr (LOW) {
-      if (keys)
+      if (keys && !IP)  // (of inner-product keys each has its own)
         byte_tables<WK>(p.ck, tlo, thi);
-      else
+      if (!keys)
         byte_tables<WV>(p.cv, tlo, thi);
     }
     bool ok = true;
@@ -392,14 +410,28 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
           if (!ok) break;
           // a norm that is not finite makes a NaN of every row that sees its key, and of no other
           const bool finite = v + n.x + (IP ? fabsf(n.y) : 0.f) < INFINITY;
-          float signs_by;  // factor of the sign bits' operand
+          float signs_by;  // value of the sign bits' operand
           if constexpr (LOW) {
-            s_keys[nr * kTile + r] = finite ? n.x : NAN;
+            float undo = 1.f;
+            if constexpr (IP) {
+              // the factor that takes the residual norm nearest to an fp16 number (in steps of fp32)
+              const float g = n.y * (64.f * p.kappa);
+              uint32_t best = 0xffffffffu;
+#pragma unroll
+              for (int k = 0; k < kAttendFactors; ++k) {
+                const int off = (int)((__float_as_uint(g * p.cks_by[k]) + 0x1000u) & 0x1FFFu) - 0x1000;
+                best = min(best, (uint32_t)abs(off) * kAttendFactors + k);
+              }
+              best %= kAttendFactors;
+              byte_tables(s_codes[best], tlo, thi);
+              signs_by = g * s_by[best].x;
+              undo = s_by[best].y;
+            }
+            s_keys[nr * kTile + r] = finite ? n.x * undo : NAN;
             s_values[nr * kTile + r] = finite ? v : 0.f;
             reinterpret_cast<float *>(smem + SM::kExps)[nr * kTile + r] = flash::norm_exponent(finite ? v : 0.f);
             const int gap = __any_sync(0xffffffffu, n.x < 0.f);
             if (lane == 0) s_gap[nr][warp - kKeyWarp] = gap;
-            signs_by = 1.f / p.kunit;
           } else {
             const uint32_t kscale = scale_bits(top_of(0, ring.before + j), kLeastKey);
             const uint32_t vscale = scale_bits(top_of(1, ring.before + j), kLeastValue);
@@ -408,7 +440,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
             if (stands_alone(v, vscale)) vown = scale_bits(v, kLeastValue);
             const float f = finite ? fmaxf(n.x, 0.f) * inverse_of(kown) : NAN;
             byte_tables<WK>(p.ckf, f, tlo, thi);
-            signs_by = f;
+            signs_by = f * n.y * (64.f * p.kappa);
             s_keys[nr * kTile + r] = n.x < 0.f ? -1.f : __uint_as_float(kown) * inverse_of(kscale);
             s_values[nr * kTile + r] = __uint_as_float(vown);
             const int gap = __any_sync(0xffffffffu, n.x < 0.f) |
@@ -431,7 +463,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) k_attend_paged_tiles(const _
             ok = agree(wait_slot(at + 1));
             if (!ok) break;
             uint8_t *signs = smem + SM::kRing + ((at + 1) % SM::kSlots) * SM::kSlot;
-            const uint32_t h = __half_as_ushort(__float2half_rn(signs_by * n.y * (64.f * p.kappa)));
+            const uint32_t h = __half_as_ushort(__float2half_rn(signs_by));
             const uint32_t minus = (h | h << 16) ^ 0x80008000u;
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {  // elements 2 k and 2 k + 1 of a group: bits k and k + 16 of its word
